@@ -1,0 +1,766 @@
+// Attention, forward and backward, on 16-bit matrix instructions.
+//
+//   S = scale Q K^T,  L_i = log sum_j exp(S_ij),  P = exp(S - L),  O = P V
+//   D_i = sum_d dO_id O_id,  dP = dO V^T,  dS = P (dP - D)
+//   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO
+//
+// One pass over the keys with a running maximum and sum (forward); the
+// backward pass recomputes P from the saved L and holds nothing of size
+// n_q x n_k. dQ is summed over keys by one kernel and dK, dV over queries (and
+// the heads of a group) by another, each in its own registers: S and dP are
+// formed twice (7 products instead of 5), and in return no atomics, no fp32
+// copy of dQ in memory, and equal inputs give equal bits.
+//
+// Operand layout. v_mfma_f32_32x32x16 takes eight consecutive k values of one
+// row per lane and leaves, in lane l and register r, column l % 32 and row
+// 8 (r / 4) + 4 (l / 32) + r % 4. The forward and dQ kernels form S^T = K Q^T,
+// so a lane owns one query: maximum, sum, L and D are one value per lane, and
+// the 8 registers of 16 keys are, rounded to 16 bits, already the B operand
+// of the next product (O^T = V^T P^T, dQ^T = K^T dS^T) if its A operand lists
+// the keys in the same order: 4 (l / 32) + {0 .. 3} and 8 more. That A
+// operand is the transpose of what LDS holds, and ds_read_b64_tr_b16 delivers
+// it: 16 lanes read four rows of 16 columns and lane i gets column i of the
+// four rows, just the group of four keys the order asks for. The dK/dV kernel
+// is the same with keys and queries exchanged (a lane owns one key).
+//
+// LDS. Tiles of 64 rows are copied by global_load_lds, 16 bytes a lane, into
+// rows of 256 bytes (128 for head_dim <= 64). The 16-byte group q of row r
+// sits in slot q ^ swz(r); with swz taking the low two row bits as the high
+// slot bits, both the reads of 16 rows at one group (A operands) and of four
+// rows at four groups (transposed) touch every bank once.
+#include "train.h"
+
+namespace matopt {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Read by every load that falls outside a sequence or past head_dim.
+__device__ __attribute__((aligned(64))) uint32_t g_attn_zero[16];
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kTile = 64;       // rows of an LDS tile
+constexpr int kWaves = 4;       // wavefronts of a workgroup, each with 32 rows of its own
+constexpr int kRows = 32 * kWaves;
+// A running maximum is raised only where it would grow by more than this
+// (in powers of two): P stays below 2^8, far from any overflow, its relative
+// rounding is unchanged, and the accumulators are rescaled in the first tile
+// and rarely after it.
+constexpr float kGrow = 8.f;
+constexpr float kLowest = -1e30f;   // a maximum before any key: finite, so that exp2(-inf - m) = 0
+
+struct Tensor {
+    char* p;
+    int64_t batch, token, head;   // strides in bytes
+};
+
+struct AttnArgs {
+    Tensor q, k, v, o, dout, dq, dk, dv;
+    float *lse, *delta;
+    const int32_t *q_start, *k_start, *q_lens, *k_lens;
+    int64_t q_tokens, k_tokens;   // rows of lse and delta; packed: the token axes
+    int32_t batch, heads, kv_heads, head_dim, q_len, k_len, causal, window;
+    float scale;
+};
+
+template <class T>
+struct Frag;
+template <>
+struct Frag<__bf16> {
+    typedef __bf16 type __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f32x16 mma(type a, type b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Frag<_Float16> {
+    typedef _Float16 type __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f32x16 mma(type a, type b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+typedef __attribute__((address_space(3))) char* lds_char;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Geometry of one LDS tile of kTile rows. DB: 32-column blocks of head_dim.
+template <int DB>
+struct Geo {
+    static constexpr int RB = DB > 2 ? 256 : 128;   // bytes per row
+    static constexpr int SLOTS = RB / 16;
+    static constexpr int BYTES = kTile * RB;
+    static constexpr int CHUNKS = BYTES / 1024;     // 1 KiB per wavefront and copy instruction
+    static constexpr int PER_WAVE = CHUNKS / kWaves;
+    static __device__ __forceinline__ int swz(int row) {
+        return DB > 2 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+    }
+};
+
+// Where one sequence's rows are.
+struct Seq {
+    int nq, nk, q_rows, k_rows;   // lengths, and the rows whose results are stored
+    int64_t q0, k0;               // first row in the token axis (packed), or 0
+    int64_t l0;                   // first row in lse and delta
+};
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
+
+__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
+    Seq s;
+    if (a.q_start) {
+        // offsets that do not ascend, or leave the token axis, cannot make an access leave it
+        const int64_t qb = min(max((int64_t)gptr(a.q_start)[b], (int64_t)0), a.q_tokens);
+        const int64_t qe = min(max((int64_t)gptr(a.q_start)[b + 1], qb), a.q_tokens);
+        const int64_t kb = min(max((int64_t)gptr(a.k_start)[b], (int64_t)0), a.k_tokens);
+        const int64_t ke = min(max((int64_t)gptr(a.k_start)[b + 1], kb), a.k_tokens);
+        s.nq = s.q_rows = (int)min(qe - qb, (int64_t)a.q_len);
+        s.nk = s.k_rows = (int)min(ke - kb, (int64_t)a.k_len);
+        s.q0 = s.l0 = qb;
+        s.k0 = kb;
+    } else {
+        s.nq = a.q_lens ? clampi(gptr(a.q_lens)[b], 0, a.q_len) : a.q_len;
+        s.nk = a.k_lens ? clampi(gptr(a.k_lens)[b], 0, a.k_len) : a.k_len;
+        s.q_rows = a.q_len;
+        s.k_rows = a.k_len;
+        s.q0 = s.k0 = 0;
+        s.l0 = (int64_t)b * a.q_len;
+    }
+    return s;
+}
+
+__device__ __forceinline__ char* rows_of(const Tensor& t, int b, int64_t row0, int h) {
+    return t.p + (int64_t)b * t.batch + row0 * t.token + (int64_t)h * t.head;
+}
+
+// Copies 64-row tiles of one tensor into LDS.
+template <int DB>
+struct Copy {
+    using G = Geo<DB>;
+    uint32_t off[G::PER_WAVE];   // per lane: byte offset of its 16 bytes from the tile's first row
+    int row[G::PER_WAVE];        // its row; past any tile where its columns are past head_dim
+    int64_t token;
+
+    __device__ __forceinline__ void init(int64_t token_stride, int head_dim) {
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        token = token_stride;
+#pragma unroll
+        for (int i = 0; i < G::PER_WAVE; ++i) {
+            row[i] = (wave * G::PER_WAVE + i) * (1024 / G::RB) + lane / G::SLOTS;
+            const int group = (lane % G::SLOTS) ^ G::swz(row[i]);
+            off[i] = (uint32_t)(row[i] * token_stride) + 16 * group;
+            if (8 * group >= head_dim) row[i] = 1 << 30;
+        }
+    }
+    // rows first .. first + 63 of a sequence of n rows
+    __device__ __forceinline__ void tile(char* lds, const char* base, int first, int n) const {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const char* origin = base + (int64_t)first * token;
+#pragma unroll
+        for (int i = 0; i < G::PER_WAVE; ++i) {
+            const void* src = row[i] < n - first ? (const void*)(origin + off[i]) : (const void*)g_attn_zero;
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                             (__attribute__((address_space(3))) void*)(lds + (wave * G::PER_WAVE + i) * 1024),
+                                             16, 0, 0);
+        }
+    }
+};
+
+// Barrier after which every wavefront sees the tiles that all of them copied.
+// The copies are vector-memory operations, which a workgroup fence does not
+// wait for, so each wavefront waits for its own (and for its LDS reads of the
+// tile that the next copy overwrites) before it arrives.
+__device__ __forceinline__ void tile_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// A lane's LDS offsets within a tile.
+template <class T, int DB>
+struct Lane {
+    using G = Geo<DB>;
+    using F = typename Frag<T>::type;
+    int rowo[2 * DB];   // A operand, k step s: row l % 32, group 2 s + l / 32
+    int tro[DB][2];     // transposed: columns of block db, rows 4 (l / 32) + l % 16 / 4 (+ 8)
+
+    __device__ __forceinline__ void init() {
+        const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+#pragma unroll
+        for (int s = 0; s < 2 * DB; ++s) rowo[s] = l32 * G::RB + (((2 * s + h) ^ G::swz(l32)) << 4);
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int row = 8 * p + 4 * h + ((lane & 15) >> 2);
+                const int group = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+                tro[d][p] = row * G::RB + ((group ^ G::swz(row)) << 4) + 8 * (lane & 1);
+            }
+    }
+    // rows 32 blk .. of the tile, k step s
+    __device__ __forceinline__ F rows(const char* tile, int blk, int s) const {
+        return *(const F*)(tile + rowo[s] + blk * 32 * G::RB);
+    }
+    // columns 32 d .. as rows of A, tile rows 16 st .. 16 st + 15 as k, in the accumulators' order
+    __device__ __forceinline__ F cols(const char* tile, int st, int d) const {
+        const lds_char t = (lds_char)tile;
+        typedef __attribute__((address_space(3))) s16x4* ptr;
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(t + tro[d][0] + st * 16 * G::RB));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(t + tro[d][1] + st * 16 * G::RB));
+        return __builtin_bit_cast(F, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+// B operand fragments of 32 rows in registers: row l % 32 (of n), k 16 s + 8 (l / 32) ..
+template <class T, int DB>
+__device__ __forceinline__ void load_rows(typename Frag<T>::type (&f)[2 * DB], const char* base, int64_t token, int row,
+                                          int n, int head_dim) {
+    const int h = (threadIdx.x & 63) >> 5;
+    const char* p = base + (int64_t)row * token;
+#pragma unroll
+    for (int s = 0; s < 2 * DB; ++s) {
+        const int c = 16 * s + 8 * h;
+        u32x4 w = {0, 0, 0, 0};
+        if (row < n && c < head_dim) w = *gptr((const u32x4*)(p + 2 * c));
+        f[s] = __builtin_bit_cast(typename Frag<T>::type, w);
+    }
+}
+
+// Sum or maximum over the two half-waves (lanes l and l + 32).
+__device__ __forceinline__ float other_half(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float((threadIdx.x & 63) < 32 ? r[1] : r[0]);
+}
+
+// Registers 8 k .. 8 k + 7 of an accumulator, rounded to 16 bits.
+template <class T>
+__device__ __forceinline__ typename Frag<T>::type pack8(const f32x16& x, int k) {
+    typename Frag<T>::type f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = (T)x[8 * k + e];
+    return f;
+}
+
+// A 32-row block of an output whose transpose is in accumulators: lane's row,
+// columns 32 d + 8 g + 4 h .. + 3 in registers 4 g ..
+template <class T, int DB>
+__device__ __forceinline__ void store_t(const f32x16 (&acc)[DB], float mul, char* row, int head_dim) {
+    const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            if (32 * d + 8 * g >= head_dim) continue;
+            typedef T t4 __attribute__((ext_vector_type(4)));
+            t4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = (T)(acc[d][4 * g + e] * mul);
+            *gptr((u32x2*)(row + 2 * (32 * d + 8 * g + 4 * h))) = __builtin_bit_cast(u32x2, v);
+        }
+}
+
+// Workgroup id -> (row block, head-and-batch index). Ids go to the XCDs in
+// turn, so id % 8 keeps a head on one XCD, whose L2 then serves its keys to
+// all its row blocks; `heavy_last` runs the blocks from the last to the first
+// (a causal sequence's last queries see the most keys), longest work first.
+__device__ __forceinline__ void locate(int id, int blocks, int pairs, bool reverse, int& blk, int& pair) {
+    if (pairs % 8 == 0) {
+        const int per = pairs / 8, r = id / 8;
+        pair = (r % per) * 8 + id % 8;
+        blk = r / per;
+    } else {
+        pair = id % pairs;
+        blk = id / pairs;
+    }
+    if (reverse) blk = blocks - 1 - blk;
+}
+
+// Keys [lo, hi) that query i of a sequence sees.
+struct Sight {
+    int nk, off, window, causal;
+    __device__ __forceinline__ int hi(int i) const { return causal ? clampi(i + off + 1, 0, nk) : nk; }
+    __device__ __forceinline__ int lo(int i) const { return window ? max(i + off - window + 1, 0) : 0; }
+};
+
+// --------------------------------------------------------------- forward ----
+
+template <class T, int DB>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_forward_kernel(AttnArgs a, int blocks) {
+    using G = Geo<DB>;
+    using FT = Frag<T>;
+    using F = typename FT::type;
+    __shared__ __attribute__((aligned(1024))) char smem[4 * G::BYTES];
+    int blk, pair;
+    locate(blockIdx.x, blocks, a.batch * a.heads, a.causal, blk, pair);
+    const int b = pair / a.heads, hq = pair % a.heads, hk = hq / (a.heads / a.kv_heads);
+    const Seq sq = sequence(a, b);
+    const int i0 = blk * kRows;
+    if (i0 >= sq.q_rows) return;
+    const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int w0 = i0 + 32 * wave, i = w0 + l32;   // the wavefront's first query, the lane's query
+    const Sight see = {sq.nk, sq.nk - sq.nq, a.window, a.causal};
+
+    Lane<T, DB> ln;
+    ln.init();
+    F qf[2 * DB];
+    load_rows<T, DB>(qf, rows_of(a.q, b, sq.q0, hq), a.q.token, i, sq.nq, a.head_dim);
+    Copy<DB> ck, cv;
+    ck.init(a.k.token, a.head_dim);
+    cv.init(a.v.token, a.head_dim);
+    const char* kb = rows_of(a.k, b, sq.k0, hk);
+    const char* vb = rows_of(a.v, b, sq.k0, hk);
+
+    f32x16 o[DB] = {};
+    float m = kLowest, l = 0.f;
+    const float c = a.scale * kLog2e;
+    // keys that any query of the workgroup sees, and of this wavefront
+    const int last = min(i0 + kRows, sq.nq) - 1, wlast = min(w0 + 32, sq.nq) - 1;
+    const int first_t = i0 < sq.nq ? see.lo(i0) / kTile : 0;
+    const int end_t = i0 < sq.nq ? (see.hi(last) + kTile - 1) / kTile : 0;
+    const int whi = w0 < sq.nq ? see.hi(wlast) : 0, wlo = see.lo(w0);
+    const int hi = i < sq.nq ? see.hi(i) : 0, lo = see.lo(i);
+    // tiles below this index and at or above that one need no mask
+    const int full_hi = see.hi(w0) / kTile, full_lo = (see.lo(max(wlast, w0)) + kTile - 1) / kTile;
+
+    auto kt = [&](int t) { return smem + (t & 1) * G::BYTES; };
+    auto vt = [&](int t) { return smem + (2 + (t & 1)) * G::BYTES; };
+    if (first_t < end_t) {
+        ck.tile(kt(first_t), kb, first_t * kTile, sq.nk);
+        cv.tile(vt(first_t), vb, first_t * kTile, sq.nk);
+    }
+    for (int t = first_t; t < end_t; ++t) {
+        tile_barrier();
+        if (t + 1 < end_t) {
+            ck.tile(kt(t + 1), kb, (t + 1) * kTile, sq.nk);
+            cv.tile(vt(t + 1), vb, (t + 1) * kTile, sq.nk);
+        }
+        if (t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
+        const char *kl = kt(t), *vl = vt(t);
+        f32x16 s[2] = {};
+#pragma unroll
+        for (int ks = 0; ks < 2 * DB; ++ks)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) s[n] = FT::mma(ln.rows(kl, n, ks), qf[ks], s[n]);
+        if (t >= full_hi || t < full_lo || w0 + 32 > sq.nq) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int j = t * kTile + 32 * n + 8 * (r >> 2) + 4 * h + (r & 3);
+                    if (j >= hi || j < lo) s[n][r] = -INFINITY;
+                }
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[n][r]);
+        if (__any(mx * c > m + kGrow)) {
+            mx = fmaxf(mx, other_half(mx));
+            const float mn = fmaxf(m, mx * c);
+            const float k = __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= k;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[d][r] *= k;
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[n][r] = __builtin_amdgcn_exp2f(fmaf(s[n][r], c, -m));
+                l += s[n][r];
+            }
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {
+            const F p = pack8<T>(s[st >> 1], st & 1);
+#pragma unroll
+            for (int d = 0; d < DB; ++d) o[d] = FT::mma(ln.cols(vl, st, d), p, o[d]);
+        }
+    }
+    if (i >= sq.q_rows) return;
+    l += other_half(l);
+    store_t<T, DB>(o, l == 0.f ? 0.f : 1.f / l, rows_of(a.o, b, sq.q0, hq) + (int64_t)i * a.o.token, a.head_dim);
+    if (h == 0) gptr(a.lse)[(int64_t)hq * a.q_tokens + sq.l0 + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// -------------------------------------------------------------- backward ----
+
+// dQ, and D for the other kernel. A lane owns one query, as in the forward pass.
+template <class T, int DB>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs a, int blocks) {
+    using G = Geo<DB>;
+    using FT = Frag<T>;
+    using F = typename FT::type;
+    __shared__ __attribute__((aligned(1024))) char smem[4 * G::BYTES];
+    int blk, pair;
+    locate(blockIdx.x, blocks, a.batch * a.heads, a.causal, blk, pair);
+    const int b = pair / a.heads, hq = pair % a.heads, hk = hq / (a.heads / a.kv_heads);
+    const Seq sq = sequence(a, b);
+    const int i0 = blk * kRows;
+    if (i0 >= sq.q_rows) return;
+    const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int w0 = i0 + 32 * wave, i = w0 + l32;
+    const Sight see = {sq.nk, sq.nk - sq.nq, a.window, a.causal};
+
+    Lane<T, DB> ln;
+    ln.init();
+    F qf[2 * DB], gf[2 * DB];
+    float D = 0.f;
+    {
+        F of[2 * DB];
+        load_rows<T, DB>(of, rows_of(a.o, b, sq.q0, hq), a.o.token, i, sq.nq, a.head_dim);
+        load_rows<T, DB>(gf, rows_of(a.dout, b, sq.q0, hq), a.dout.token, i, sq.nq, a.head_dim);
+        load_rows<T, DB>(qf, rows_of(a.q, b, sq.q0, hq), a.q.token, i, sq.nq, a.head_dim);
+#pragma unroll
+        for (int s = 0; s < 2 * DB; ++s)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) D = fmaf((float)of[s][e], (float)gf[s][e], D);
+        D += other_half(D);
+    }
+    const int64_t at = (int64_t)hq * a.q_tokens + sq.l0 + i;
+    // a row that sees no key has L = -inf: with +inf in its place P is 0
+    float L2 = INFINITY;
+    if (i < sq.nq) {
+        L2 = gptr(a.lse)[at] * kLog2e;
+        if (L2 == -INFINITY) L2 = INFINITY;
+        if (h == 0) gptr(a.delta)[at] = D;
+    }
+    Copy<DB> ck, cv;
+    ck.init(a.k.token, a.head_dim);
+    cv.init(a.v.token, a.head_dim);
+    const char* kb = rows_of(a.k, b, sq.k0, hk);
+    const char* vb = rows_of(a.v, b, sq.k0, hk);
+    f32x16 dq[DB] = {};
+    const float c = a.scale * kLog2e;
+    const int last = min(i0 + kRows, sq.nq) - 1, wlast = min(w0 + 32, sq.nq) - 1;
+    const int first_t = i0 < sq.nq ? see.lo(i0) / kTile : 0;
+    const int end_t = i0 < sq.nq ? (see.hi(last) + kTile - 1) / kTile : 0;
+    const int whi = w0 < sq.nq ? see.hi(wlast) : 0, wlo = see.lo(w0);
+    const int hi = i < sq.nq ? see.hi(i) : 0, lo = see.lo(i);
+    const int full_hi = see.hi(w0) / kTile, full_lo = (see.lo(max(wlast, w0)) + kTile - 1) / kTile;
+
+    auto kt = [&](int t) { return smem + (t & 1) * G::BYTES; };
+    auto vt = [&](int t) { return smem + (2 + (t & 1)) * G::BYTES; };
+    if (first_t < end_t) {
+        ck.tile(kt(first_t), kb, first_t * kTile, sq.nk);
+        cv.tile(vt(first_t), vb, first_t * kTile, sq.nk);
+    }
+    for (int t = first_t; t < end_t; ++t) {
+        tile_barrier();
+        if (t + 1 < end_t) {
+            ck.tile(kt(t + 1), kb, (t + 1) * kTile, sq.nk);
+            cv.tile(vt(t + 1), vb, (t + 1) * kTile, sq.nk);
+        }
+        if (t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
+        const char *kl = kt(t), *vl = vt(t);
+        const bool edge = t >= full_hi || t < full_lo;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            f32x16 s = {}, dp = {};
+#pragma unroll
+            for (int ks = 0; ks < 2 * DB; ++ks) {
+                s = FT::mma(ln.rows(kl, n, ks), qf[ks], s);
+                dp = FT::mma(ln.rows(vl, n, ks), gf[ks], dp);
+            }
+            if (edge) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int j = t * kTile + 32 * n + 8 * (r >> 2) + 4 * h + (r & 3);
+                    if (j >= hi || j < lo) s[r] = -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -L2)) * (dp[r] - D);
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                const F p = pack8<T>(s, st);
+#pragma unroll
+                for (int d = 0; d < DB; ++d) dq[d] = FT::mma(ln.cols(kl, 2 * n + st, d), p, dq[d]);
+            }
+        }
+    }
+    if (i < sq.q_rows)
+        store_t<T, DB>(dq, a.scale, rows_of(a.dq, b, sq.q0, hq) + (int64_t)i * a.dq.token, a.head_dim);
+}
+
+// dK and dV of 128 keys, summed over the queries that see them and over the
+// heads of the group. A lane owns one key.
+template <class T, int DB>
+__global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnArgs a, int blocks) {
+    using G = Geo<DB>;
+    using FT = Frag<T>;
+    using F = typename FT::type;
+    __shared__ __attribute__((aligned(1024))) char smem[4 * G::BYTES];
+    __shared__ __attribute__((aligned(16))) float stat[2][2][kTile];   // [buffer][L, D]
+    int blk, pair;
+    locate(blockIdx.x, blocks, a.batch * a.kv_heads, false, blk, pair);
+    const int b = pair / a.kv_heads, hk = pair % a.kv_heads, group = a.heads / a.kv_heads;
+    const Seq sq = sequence(a, b);
+    const int j0 = blk * kRows;
+    if (j0 >= sq.k_rows) return;
+    const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int w0 = j0 + 32 * wave, j = w0 + l32;   // the wavefront's first key, the lane's key
+    const int off = sq.nk - sq.nq;
+
+    Lane<T, DB> ln;
+    ln.init();
+    F kf[2 * DB], vf[2 * DB];
+    load_rows<T, DB>(kf, rows_of(a.k, b, sq.k0, hk), a.k.token, j, sq.nk, a.head_dim);
+    load_rows<T, DB>(vf, rows_of(a.v, b, sq.k0, hk), a.v.token, j, sq.nk, a.head_dim);
+    Copy<DB> cq, cg;
+    cq.init(a.q.token, a.head_dim);
+    cg.init(a.dout.token, a.head_dim);
+    f32x16 dk[DB] = {}, dv[DB] = {};
+    const float c = a.scale * kLog2e;
+
+    // queries [lo, hi) that see key j: j <= i + off, and j > i + off - window
+    auto qlo = [&](int key) { return a.causal ? clampi(key - off, 0, sq.nq) : 0; };
+    auto qhi = [&](int key) { return a.window ? clampi(key - off + a.window, 0, sq.nq) : sq.nq; };
+    const int jl = min(j0 + kRows, sq.nk) - 1, wl = min(w0 + 32, sq.nk) - 1;
+    const bool any = j0 < sq.nk;
+    const int first_t = any ? qlo(j0) / kTile : 0;
+    const int end_t = any ? (qhi(jl) + kTile - 1) / kTile : 0;
+    const int tiles = max(end_t - first_t, 0);
+    const int wlo = qlo(w0), whi = w0 < sq.nk ? qhi(wl) : 0;
+    const int lo = qlo(j), hi = j < sq.nk ? qhi(j) : 0;
+    const int full_lo = (qlo(max(wl, w0)) + kTile - 1) / kTile, full_hi = qhi(w0) / kTile;
+
+    auto qt = [&](int t) { return smem + (t & 1) * G::BYTES; };
+    auto gt = [&](int t) { return smem + (2 + (t & 1)) * G::BYTES; };
+    // step n: query tile n % tiles of the group's head n / tiles
+    auto fill = [&](int n) {
+        const int hq = hk * group + n / tiles, first = (first_t + n % tiles) * kTile;
+        cq.tile(qt(n), rows_of(a.q, b, sq.q0, hq), first, sq.nq);
+        cg.tile(gt(n), rows_of(a.dout, b, sq.q0, hq), first, sq.nq);
+        if (threadIdx.x < kTile) {
+            const int i = first + threadIdx.x;
+            const int64_t at = (int64_t)hq * a.q_tokens + sq.l0 + i;
+            float L = INFINITY, D = 0.f;
+            if (i < sq.nq) {
+                L = gptr(a.lse)[at] * kLog2e;
+                if (L == -INFINITY) L = INFINITY;
+                D = gptr(a.delta)[at];
+            }
+            stat[n & 1][0][threadIdx.x] = L;
+            stat[n & 1][1][threadIdx.x] = D;
+        }
+    };
+    const int steps = tiles * group;
+    if (steps > 0) fill(0);
+    for (int n = 0; n < steps; ++n) {
+        tile_barrier();
+        if (n + 1 < steps) fill(n + 1);
+        const int t = first_t + n % tiles;
+        if (t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
+        const char *ql = qt(n), *gl = gt(n);
+        const bool edge = t < full_lo || t >= full_hi || w0 + 32 > sq.nk;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            f32x16 s = {}, dp = {};
+#pragma unroll
+            for (int ks = 0; ks < 2 * DB; ++ks) {
+                s = FT::mma(ln.rows(ql, u, ks), kf[ks], s);
+                dp = FT::mma(ln.rows(gl, u, ks), vf[ks], dp);
+            }
+            if (edge) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int i = t * kTile + 32 * u + 8 * (r >> 2) + 4 * h + (r & 3);
+                    if (i >= hi || i < lo) s[r] = -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 L = *(const f32x4*)&stat[n & 1][0][32 * u + 8 * g + 4 * h];
+                const f32x4 D = *(const f32x4*)&stat[n & 1][1][32 * u + 8 * g + 4 * h];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[4 * g + e] = __builtin_amdgcn_exp2f(fmaf(s[4 * g + e], c, -L[e]));
+                    dp[4 * g + e] = s[4 * g + e] * (dp[4 * g + e] - D[e]);
+                }
+            }
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                const F p = pack8<T>(s, st), ds = pack8<T>(dp, st);
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    dv[d] = FT::mma(ln.cols(gl, 2 * u + st, d), p, dv[d]);
+                    dk[d] = FT::mma(ln.cols(ql, 2 * u + st, d), ds, dk[d]);
+                }
+            }
+        }
+    }
+    if (j >= sq.k_rows) return;
+    store_t<T, DB>(dk, a.scale, rows_of(a.dk, b, sq.k0, hk) + (int64_t)j * a.dk.token, a.head_dim);
+    store_t<T, DB>(dv, 1.f, rows_of(a.dv, b, sq.k0, hk) + (int64_t)j * a.dv.token, a.head_dim);
+}
+
+// ------------------------------------------------------------------ host ----
+
+opt_status check_attention(const opt_attention_desc* a) {
+    if (!a) return fail(OPT_EINVAL, "desc is NULL");
+    if (a->dtype != OPT_BF16 && a->dtype != OPT_F16) return fail(OPT_EUNSUPPORTED, "dtype must be OPT_BF16 or OPT_F16");
+    if (a->batch < 0 || a->q_len < 0 || a->k_len < 0) return fail(OPT_EINVAL, "negative batch or length");
+    if (a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads)
+        return fail(OPT_EINVAL, "heads must be a positive multiple of kv_heads");
+    if (a->head_dim < 8 || a->head_dim % 8) return fail(OPT_EINVAL, "head_dim must be a positive multiple of 8");
+    if (a->head_dim > 128) return fail(OPT_EUNSUPPORTED, "head_dim must be <= 128");
+    if (a->q_len > (1 << 30) || a->k_len > (1 << 30)) return fail(OPT_EUNSUPPORTED, "sequence too long");
+    if (a->window < 0) return fail(OPT_EINVAL, "window must be >= 0");
+    if (a->window > 0 && !a->causal) return fail(OPT_EUNSUPPORTED, "a window needs causal");
+    if (!(a->scale > 0.f) || !(a->scale < INFINITY)) return fail(OPT_EINVAL, "scale must be positive and finite");
+    if ((a->q_start != nullptr) != (a->k_start != nullptr)) return fail(OPT_EINVAL, "q_start and k_start come together");
+    if (a->q_start && (a->q_lens || a->k_lens)) return fail(OPT_EINVAL, "lengths and packed offsets exclude each other");
+    for (const int32_t* p : {a->q_start, a->k_start, a->q_lens, a->k_lens})
+        if (!train_aligned(p, 4)) return fail(OPT_EINVAL, "an offset or length array is not aligned to 4 bytes");
+    if (a->q_start && (a->q_tokens < 0 || a->k_tokens < 0)) return fail(OPT_EINVAL, "negative q_tokens or k_tokens");
+    const int64_t longest = a->q_len > a->k_len ? a->q_len : a->k_len;
+    if ((longest / kRows + 1) * a->batch * a->heads > INT32_MAX) return fail(OPT_EUNSUPPORTED, "too many row blocks");
+    return OPT_OK;
+}
+
+opt_status tensor(const opt_attention_desc* a, const opt_attention_tensor* t, const char* name, bool empty, Tensor& out) {
+    if (!t) return fail(OPT_EINVAL, "%s is NULL", name);
+    if (empty) return OPT_OK;
+    if (!t->data) return fail(OPT_EINVAL, "%s has no data", name);
+    if (!train_aligned(t->data, 16)) return fail(OPT_EINVAL, "%s is not 16-byte aligned", name);
+    if (t->batch_stride < 0 || t->token_stride < 0 || t->head_stride < 0) return fail(OPT_EINVAL, "negative stride of %s", name);
+    if (t->batch_stride % 8 || t->token_stride % 8 || t->head_stride % 8)
+        return fail(OPT_EINVAL, "strides of %s must be multiples of 8", name);
+    if (t->token_stride > (1 << 24)) return fail(OPT_EUNSUPPORTED, "token stride of %s is above 2^24", name);
+    out = {(char*)t->data, t->batch_stride * 2, t->token_stride * 2, t->head_stride * 2};
+    return OPT_OK;
+}
+
+// An output's rows must not share memory: with more than one of each, no stride may be 0.
+opt_status output(const opt_attention_desc* a, const opt_attention_tensor* t, const char* name, bool empty, int heads,
+                  int len, Tensor& out) {
+    if (opt_status st = tensor(a, t, name, empty, out)) return st;
+    if (empty) return OPT_OK;
+    if ((!a->q_start && a->batch > 1 && t->batch_stride == 0) || (len > 1 && t->token_stride < a->head_dim) ||
+        (heads > 1 && t->head_stride < a->head_dim))
+        return fail(OPT_EINVAL, "rows of %s overlap", name);
+    return OPT_OK;
+}
+
+AttnArgs attn_args(const opt_attention_desc* a) {
+    AttnArgs x = {};
+    x.q_start = a->q_start, x.k_start = a->k_start, x.q_lens = a->q_lens, x.k_lens = a->k_lens;
+    x.q_tokens = a->q_start ? a->q_tokens : (int64_t)a->batch * a->q_len;
+    x.k_tokens = a->q_start ? a->k_tokens : (int64_t)a->batch * a->k_len;
+    x.batch = a->batch, x.heads = a->heads, x.kv_heads = a->kv_heads, x.head_dim = a->head_dim;
+    x.q_len = a->q_len, x.k_len = a->k_len, x.causal = a->causal != 0, x.window = a->window, x.scale = a->scale;
+    return x;
+}
+
+int row_blocks(int len) { return (len + kRows - 1) / kRows; }
+
+enum Kind { FORWARD, DQ, DKV };
+template <class T, int DB>
+void launch(Kind kind, const AttnArgs& x, hipStream_t s) {
+    const int blocks = row_blocks(kind == DKV ? x.k_len : x.q_len);
+    const int64_t grid = (int64_t)blocks * x.batch * (kind == DKV ? x.kv_heads : x.heads);
+    if (grid == 0) return;
+    const dim3 g((uint32_t)grid), n(64 * kWaves);
+    if (kind == FORWARD) attn_forward_kernel<T, DB><<<g, n, 0, s>>>(x, blocks);
+    else if (kind == DQ) attn_dq_kernel<T, DB><<<g, n, 0, s>>>(x, blocks);
+    else attn_dkv_kernel<T, DB><<<g, n, 0, s>>>(x, blocks);
+}
+template <class T>
+void launch(Kind kind, const AttnArgs& x, hipStream_t s) {
+    if (x.head_dim <= 32) launch<T, 1>(kind, x, s);
+    else if (x.head_dim <= 64) launch<T, 2>(kind, x, s);
+    else if (x.head_dim <= 96) launch<T, 3>(kind, x, s);
+    else launch<T, 4>(kind, x, s);
+}
+void launch(Kind kind, int32_t dtype, const AttnArgs& x, hipStream_t s) {
+    dtype == OPT_BF16 ? launch<__bf16>(kind, x, s) : launch<_Float16>(kind, x, s);
+}
+
+uint64_t attn_bytes(const opt_attention_desc* a, bool backward) {
+    if (!backward) return 0;
+    const AttnArgs x = attn_args(a);
+    return ((uint64_t)x.q_tokens * (uint64_t)x.heads * 4 + 255) / 256 * 256;
+}
+
+opt_status check_workspace(const void* ws, uint64_t bytes, uint64_t need) {
+    if (bytes < need) return fail(OPT_ENOWS, "workspace of %llu bytes, %llu needed", (unsigned long long)bytes,
+                                  (unsigned long long)need);
+    if (need && (!ws || !train_aligned(ws, 256))) return fail(OPT_EINVAL, "workspace is NULL or not 256-byte aligned");
+    return OPT_OK;
+}
+
+}  // namespace
+}  // namespace matopt
+
+using namespace matopt;
+
+extern "C" {
+
+opt_status opt_attention_workspace_size(const opt_attention_desc* a, int32_t backward, uint64_t* bytes) {
+    if (!bytes) return fail(OPT_EINVAL, "bytes is NULL");
+    if (opt_status st = check_attention(a)) return st;
+    *bytes = attn_bytes(a, backward != 0);
+    return OPT_OK;
+}
+
+opt_status opt_attention_forward(const opt_attention_desc* a, const opt_attention_tensor* q,
+                                 const opt_attention_tensor* k, const opt_attention_tensor* v,
+                                 const opt_attention_tensor* out, float* lse, void* workspace,
+                                 uint64_t workspace_bytes, void* stream) {
+    if (opt_status st = check_attention(a)) return st;
+    AttnArgs x = attn_args(a);
+    const bool no_q = x.q_tokens == 0 || a->q_len == 0 || a->batch == 0, no_k = x.k_tokens == 0 || a->k_len == 0;
+    if (opt_status st = tensor(a, q, "q", no_q, x.q)) return st;
+    if (opt_status st = tensor(a, k, "k", no_k || no_q, x.k)) return st;
+    if (opt_status st = tensor(a, v, "v", no_k || no_q, x.v)) return st;
+    if (opt_status st = output(a, out, "out", no_q, a->heads, a->q_len, x.o)) return st;
+    if (!no_q && (!lse || !train_aligned(lse, 4))) return fail(OPT_EINVAL, "lse is NULL or not aligned to 4 bytes");
+    if (opt_status st = check_workspace(workspace, workspace_bytes, attn_bytes(a, false))) return st;
+    if (no_q) return OPT_OK;
+    if (opt_status st = train_pending()) return st;
+    x.lse = lse;
+    launch(FORWARD, a->dtype, x, (hipStream_t)stream);
+    return train_launched("attention");
+}
+
+opt_status opt_attention_backward(const opt_attention_desc* a, const opt_attention_tensor* dout,
+                                  const opt_attention_tensor* q, const opt_attention_tensor* k,
+                                  const opt_attention_tensor* v, const opt_attention_tensor* out, const float* lse,
+                                  const opt_attention_tensor* dq, const opt_attention_tensor* dk,
+                                  const opt_attention_tensor* dv, void* workspace, uint64_t workspace_bytes,
+                                  void* stream) {
+    if (opt_status st = check_attention(a)) return st;
+    AttnArgs x = attn_args(a);
+    const bool no_q = x.q_tokens == 0 || a->q_len == 0 || a->batch == 0;
+    const bool no_k = x.k_tokens == 0 || a->k_len == 0 || a->batch == 0;
+    if (opt_status st = tensor(a, dout, "dout", no_q, x.dout)) return st;
+    if (opt_status st = tensor(a, q, "q", no_q, x.q)) return st;
+    if (opt_status st = tensor(a, k, "k", no_k, x.k)) return st;
+    if (opt_status st = tensor(a, v, "v", no_k, x.v)) return st;
+    if (opt_status st = tensor(a, out, "out", no_q, x.o)) return st;
+    if (!no_q && (!lse || !train_aligned(lse, 4))) return fail(OPT_EINVAL, "lse is NULL or not aligned to 4 bytes");
+    if (opt_status st = output(a, dq, "dq", no_q, a->heads, a->q_len, x.dq)) return st;
+    if (opt_status st = output(a, dk, "dk", no_k, a->kv_heads, a->k_len, x.dk)) return st;
+    if (opt_status st = output(a, dv, "dv", no_k, a->kv_heads, a->k_len, x.dv)) return st;
+    if (opt_status st = check_workspace(workspace, workspace_bytes, attn_bytes(a, true))) return st;
+    if (no_q && no_k) return OPT_OK;
+    if (opt_status st = train_pending()) return st;
+    x.lse = (float*)lse;
+    x.delta = (float*)workspace;
+    if (!no_q) launch(DQ, a->dtype, x, (hipStream_t)stream);
+    if (!no_k) launch(DKV, a->dtype, x, (hipStream_t)stream);
+    return train_launched("attention backward");
+}
+
+}  // extern "C"

@@ -1,0 +1,432 @@
+// Clipped policy loss with a KL term on logits (HBM-bandwidth bound).
+//
+//   z = scale x,  lse = log sum_j exp(z_j),  logp = z_t - lse
+//   r = exp(logp - old),  d = ref - logp
+//   term  = max(-A r, -A clip(r)) + kl (exp(d) - d - 1)
+//   slope = w ((-A r where that is the larger or equal) + kl (1 - exp(d)))
+//   dx_j  = grad scale slope ([j = t] - exp(z_j - lse))
+//
+// One workgroup per row. The row is read once: each thread keeps its groups
+// of eight logits in registers as they are stored (up to 80 registers of 1024
+// threads: 160 K 16-bit or 80 K 32-bit logits, more than half of a CU's register file), takes the
+// maximum, the sum of exponentials and the gradient from there, so a pass
+// moves one read and one write of the logits. Longer rows keep a running
+// maximum and sum and read the row a second time. The exponentials are taken
+// in base 2, with log2(e) folded into the scale.
+//
+// The loss is the sum of the rows' terms, which a second kernel adds in
+// 64 bits in a fixed order.
+#include "train.h"
+
+namespace matopt {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct PolicyArgs {
+    const void *logits, *target;
+    const float *old_logp, *ref_logp, *advantage, *weight;
+    float *logp, *lse, *slope, *term;   // logp, lse, slope: NULL where the call does not return them
+    void* dlogits;                      // NULL: forward only
+    int64_t ld, ldd;
+    int32_t vocab, target_i64;
+    float scale, lo, hi, kl, grad;
+};
+
+// Eight logits as stored.
+template <class T>
+struct Raw8 {
+    static constexpr int W = sizeof(T) * 2;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const T* p) {
+        const auto* q = (const __attribute__((address_space(1))) u32x4u*)p;
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+            const u32x4u r = q[i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[4 * i + e] = r[e];
+        }
+    }
+    __device__ __forceinline__ void set(int e, T x) {
+        if constexpr (sizeof(T) == 4) {
+            w[e] = __builtin_bit_cast(uint32_t, x);
+        } else {
+            const uint32_t b = __builtin_bit_cast(uint16_t, x);
+            w[e >> 1] = e & 1 ? (w[e >> 1] & 0xffffu) | b << 16 : (w[e >> 1] & 0xffff0000u) | b;
+        }
+    }
+    // the first n elements, -inf (which adds nothing to a sum of exponentials) past them
+    __device__ __forceinline__ void load_n(const T* p, int n) {
+        if (n >= 8) return load(p);
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) set(e, e < n ? gptr(p)[e] : (T)-INFINITY);
+    }
+    // Makes the registers look rewritten, so that the compiler converts them
+    // again in the next phase rather than keep the converted values, twice
+    // the registers, across phases (88 spilled at 131072 16-bit logits).
+    __device__ __forceinline__ void again() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) asm volatile("" : "+v"(w[i]));
+    }
+    __device__ __forceinline__ float get(int e) const {
+        if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, w[e]);
+        else return (float)__builtin_bit_cast(T, (uint16_t)(e & 1 ? w[e >> 1] >> 16 : w[e >> 1]));
+    }
+};
+
+template <int NT, bool MAX>
+__device__ __forceinline__ float block_reduce(float x, float* part) {
+    x = MAX ? wave_max(x) : wave_sum(x);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+    __syncthreads();
+    float s = part[0];
+#pragma unroll
+    for (int k = 1; k < NT / 64; ++k) s = MAX ? fmaxf(s, part[k]) : s + part[k];
+    return s;
+}
+
+__device__ __forceinline__ int64_t target_of(const PolicyArgs& a, uint32_t row) {
+    return a.target_i64 ? gptr((const int64_t*)a.target)[row] : gptr((const int32_t*)a.target)[row];
+}
+
+// What a row's log probability makes of the loss: its term and slope.
+__device__ __forceinline__ void row_loss(const PolicyArgs& a, uint32_t row, float w, float logp, float& term,
+                                         float& slope) {
+    const float adv = gptr(a.advantage)[row];
+    const float r = expf(logp - gptr(a.old_logp)[row]);
+    const float clipped = fminf(fmaxf(r, a.lo), a.hi);
+    const float free = -adv * r, bound = -adv * clipped;
+    term = fmaxf(free, bound);
+    slope = free >= bound ? free : 0.f;
+    if (a.kl != 0.f) {
+        const float d = gptr(a.ref_logp)[row] - logp, e = expm1f(d);
+        term += a.kl * (e - d);
+        slope -= a.kl * e;
+    }
+    if (logp != logp) term = slope = logp;   // max and >= would lose a NaN
+    term *= w;
+    slope *= w;
+}
+
+// NV: groups of eight a thread keeps; 0: the row is read twice.
+template <class T, int NT, int NV>
+__global__ __launch_bounds__(NT) void policy_row_kernel(PolicyArgs a) {
+    __shared__ float part[2][NT / 64];
+    const uint32_t row = blockIdx.x;
+    const int tid = threadIdx.x, V = a.vocab, G = (V + 7) >> 3;
+    const T* x = (const T*)a.logits + (int64_t)row * a.ld;
+    T* dx = a.dlogits ? (T*)a.dlogits + (int64_t)row * a.ldd : nullptr;
+    const float w = gptr(a.weight)[row];
+    if (w == 0.f) {
+        if (dx) {
+            const float z[8] = {};
+            for (int g = tid; g < G; g += NT) store_n(dx + 8 * (int64_t)g, V - 8 * g, z);
+        }
+        if (tid == 0) {
+            gptr(a.term)[row] = 0.f;
+            if (a.logp) gptr(a.logp)[row] = 0.f;
+            if (a.lse) gptr(a.lse)[row] = 0.f;
+            if (a.slope) gptr(a.slope)[row] = 0.f;
+        }
+        return;
+    }
+    const float c = a.scale * kLog2e;
+    const int64_t t = target_of(a, row);
+    const bool valid = t >= 0 && t < V;
+    const float xt = valid ? (float)gptr(x)[t] : NAN;   // before any store: dlogits may be logits
+
+    Raw8<T> keep[NV > 0 ? NV : 1];
+    float m = -INFINITY, s = 0.f;
+    if constexpr (NV > 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int g = tid + i * NT;
+            keep[i].load_n(x + 8 * (int64_t)(g < G ? g : 0), g < G ? V - 8 * g : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, keep[i].get(e));
+        m = block_reduce<NT, true>(m * c, part[0]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            keep[i].again();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f(fmaf(keep[i].get(e), c, -m));
+        }
+        s = block_reduce<NT, false>(s, part[1]);
+    } else {
+        constexpr int U = 4;
+        for (int g0 = tid; g0 < G; g0 += U * NT) {
+            Raw8<T> r[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int g = g0 + u * NT;
+                r[u].load_n(x + 8 * (int64_t)(g < G ? g : 0), g < G ? V - 8 * g : 0);
+            }
+            float top = m;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, r[u].get(e) * c);
+            if (top == -INFINITY) {   // nothing yet but -inf, or a NaN, which must reach the sum
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s += r[u].get(e) != r[u].get(e) ? NAN : 0.f;
+                continue;
+            }
+            s *= __builtin_amdgcn_exp2f(m - top);
+            m = top;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f(fmaf(r[u].get(e), c, -m));
+        }
+        const float all = block_reduce<NT, true>(m, part[0]);
+        if (m != -INFINITY) s *= __builtin_amdgcn_exp2f(m - all);
+        m = all;
+        s = block_reduce<NT, false>(s, part[1]);
+    }
+    const float lse2 = m + log2f(s);   // of z, in base 2
+    const float lse = lse2 * kLn2;
+    const float logp = fmaf(xt, a.scale, -lse);
+    float term, slope;
+    row_loss(a, row, w, logp, term, slope);
+    if (tid == 0) {
+        gptr(a.term)[row] = term;
+        if (a.logp) gptr(a.logp)[row] = logp;
+        if (a.lse) gptr(a.lse)[row] = lse;
+        if (a.slope) gptr(a.slope)[row] = slope;
+    }
+    if (!dx) return;
+    const float k = a.grad * a.scale * slope;
+    auto write = [&](int g, const Raw8<T>& r) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = -k * __builtin_amdgcn_exp2f(fmaf(r.get(e), c, -lse2));
+        store_n(dx + 8 * (int64_t)g, V - 8 * g, o);
+    };
+    if constexpr (NV > 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            keep[i].again();
+            if (tid + i * NT < G) write(tid + i * NT, keep[i]);
+        }
+    } else {
+        for (int g = tid; g < G; g += NT) {
+            Raw8<T> r;
+            r.load_n(x + 8 * (int64_t)g, V - 8 * g);
+            write(g, r);
+        }
+    }
+    // the target's entry, by the thread that wrote its group
+    if (valid && (int)(t >> 3) % NT == tid)
+        gptr(dx)[t] = from_f32<T>(k * (1.f - __builtin_amdgcn_exp2f(fmaf(xt, c, -lse2))));
+}
+
+// dlogits from the saved log-sum and slope: kBackPer groups of a row per thread.
+constexpr int kBackThreads = 256, kBackPer = 4;
+template <class T>
+__global__ __launch_bounds__(kBackThreads) void policy_backward_kernel(PolicyArgs a, const float* grad) {
+    const uint32_t row = blockIdx.x;
+    const int V = a.vocab, G = (V + 7) >> 3, g0 = blockIdx.y * (kBackThreads * kBackPer) + threadIdx.x;
+    const T* x = (const T*)a.logits + (int64_t)row * a.ld;
+    T* dx = (T*)a.dlogits + (int64_t)row * a.ldd;
+    const float slope = gptr(a.slope)[row];
+    const float k = slope == 0.f ? 0.f : (grad ? *gptr(grad) : 1.f) * a.scale * slope;
+    const float c = a.scale * kLog2e, lse2 = gptr(a.lse)[row] * kLog2e;
+    const int64_t t = target_of(a, row);
+    Raw8<T> r[kBackPer];
+#pragma unroll
+    for (int i = 0; i < kBackPer; ++i) {
+        const int g = g0 + i * kBackThreads;
+        if (k != 0.f) r[i].load_n(x + 8 * (int64_t)(g < G ? g : 0), g < G ? V - 8 * g : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kBackPer; ++i) {
+        const int g = g0 + i * kBackThreads;
+        if (g >= G) continue;
+        float o[8] = {};
+        if (k != 0.f) {   // a row without slope is not read: it may hold anything
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(r[i].get(e), c, -lse2));
+                o[e] = 8 * (int64_t)g + e == t ? k * (1.f - p) : -k * p;
+            }
+        }
+        store_n(dx + 8 * (int64_t)g, V - 8 * g, o);
+    }
+}
+
+constexpr int kLossThreads = 1024;
+__global__ __launch_bounds__(kLossThreads) void policy_sum_kernel(int64_t rows, const float* term, float* loss) {
+    __shared__ double part[kLossThreads / 64];
+    double s = 0.0;
+    for (int64_t r = threadIdx.x; r < rows; r += kLossThreads) s += gptr(term)[r];
+#pragma unroll
+    for (int m = 32; m; m >>= 1) s += __shfl_xor(s, m);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x) return;
+    s = part[0];
+    for (int k = 1; k < kLossThreads / 64; ++k) s += part[k];
+    *gptr(loss) = (float)s;
+}
+
+// Small vocabularies take small workgroups, so that several rows share a CU;
+// past what 1024 threads hold in 80 registers the row is streamed.
+template <class T>
+void launch_rows(const PolicyArgs& a, int64_t rows, hipStream_t s) {
+    const dim3 grid((uint32_t)rows);
+    const int64_t v = a.vocab;
+    constexpr int K = 4 / sizeof(T);   // logits per register
+    if (v <= 8 * 256 * 2) policy_row_kernel<T, 256, 2><<<grid, 256, 0, s>>>(a);
+    else if (v <= 8 * 256 * 4) policy_row_kernel<T, 256, 4><<<grid, 256, 0, s>>>(a);
+    else if (v <= 8 * 1024 * 2) policy_row_kernel<T, 1024, 2><<<grid, 1024, 0, s>>>(a);
+    else if (v <= 8 * 1024 * 4) policy_row_kernel<T, 1024, 4><<<grid, 1024, 0, s>>>(a);
+    else if (v <= 8 * 1024 * 8) policy_row_kernel<T, 1024, 8><<<grid, 1024, 0, s>>>(a);
+    else if (v <= 8 * 1024 * 8 * K) policy_row_kernel<T, 1024, 8 * K><<<grid, 1024, 0, s>>>(a);
+    else if (v <= 8 * 1024 * 10 * K) policy_row_kernel<T, 1024, 10 * K><<<grid, 1024, 0, s>>>(a);
+    else policy_row_kernel<T, 1024, 0><<<grid, 1024, 0, s>>>(a);
+}
+
+opt_status check_policy(const opt_policy_desc* a) {
+    if (!a) return fail(OPT_EINVAL, "desc is NULL");
+    if (!train_dtype(a->dtype)) return fail(OPT_EUNSUPPORTED, "dtype must be OPT_F32, OPT_BF16 or OPT_F16");
+    if (a->rows < 0 || a->vocab < 1) return fail(OPT_EINVAL, "rows must be >= 0 and vocab >= 1");
+    if (a->rows > INT32_MAX || a->vocab > INT32_MAX - 65536) return fail(OPT_EUNSUPPORTED, "rows or vocab too large");
+    if (a->ld < a->vocab) return fail(OPT_EINVAL, "ld < vocab");
+    if (!(a->logit_scale > 0.f) || !(a->logit_scale < INFINITY)) return fail(OPT_EINVAL, "logit_scale must be positive and finite");
+    if (!(a->clip_low >= 0.f && a->clip_low <= 1.f) || !(a->clip_high >= 0.f))
+        return fail(OPT_EINVAL, "clip_low must be in [0, 1] and clip_high >= 0");
+    if (!(a->kl_coef >= 0.f)) return fail(OPT_EINVAL, "kl_coef must be >= 0");
+    return OPT_OK;
+}
+
+opt_status check_vector(const void* p, uintptr_t align, const char* name) {
+    if (!p) return fail(OPT_EINVAL, "%s is NULL", name);
+    if (!train_aligned(p, align)) return fail(OPT_EINVAL, "%s is not aligned to its element size", name);
+    return OPT_OK;
+}
+
+opt_status check_rows(const opt_policy_desc* a, const opt_policy_rows* in) {
+    if (!in) return fail(OPT_EINVAL, "rows' inputs are NULL");
+    if (opt_status st = check_vector(in->target, a->target_i64 ? 8 : 4, "target")) return st;
+    if (opt_status st = check_vector(in->old_logp, 4, "old_logp")) return st;
+    if (opt_status st = check_vector(in->advantage, 4, "advantage")) return st;
+    if (opt_status st = check_vector(in->weight, 4, "weight")) return st;
+    if (a->kl_coef != 0.f)
+        if (opt_status st = check_vector(in->ref_logp, 4, "ref_logp")) return st;
+    return OPT_OK;
+}
+
+opt_status check_dlogits(const opt_policy_desc* a, const void* logits, const void* dlogits, int64_t ldd) {
+    if (opt_status st = check_vector(dlogits, train_bytes(a->dtype), "dlogits")) return st;
+    if (ldd < a->vocab) return fail(OPT_EINVAL, "ldd < vocab");
+    if (dlogits == logits && ldd != a->ld) return fail(OPT_EINVAL, "dlogits in place of logits needs ldd == ld");
+    return OPT_OK;
+}
+
+PolicyArgs policy_args(const opt_policy_desc* a, const void* logits, const opt_policy_rows* in) {
+    PolicyArgs p = {};
+    p.logits = logits;
+    if (in) {
+        p.target = in->target, p.old_logp = in->old_logp, p.ref_logp = in->ref_logp;
+        p.advantage = in->advantage, p.weight = in->weight;
+    }
+    p.ld = a->ld, p.vocab = (int32_t)a->vocab, p.target_i64 = a->target_i64;
+    p.scale = a->logit_scale, p.lo = 1.f - a->clip_low, p.hi = 1.f + a->clip_high, p.kl = a->kl_coef, p.grad = 1.f;
+    return p;
+}
+
+uint64_t policy_bytes(const opt_policy_desc* a) { return ((uint64_t)a->rows * 4 + 255) / 256 * 256; }
+
+opt_status run_rows(const opt_policy_desc* a, PolicyArgs p, float* loss, void* ws, uint64_t ws_bytes, void* stream) {
+    if (opt_status st = check_vector(loss, 4, "loss")) return st;
+    if (ws_bytes < policy_bytes(a)) return fail(OPT_ENOWS, "workspace too small");
+    if (a->rows && (!ws || !train_aligned(ws, 256))) return fail(OPT_EINVAL, "workspace is NULL or not 256-byte aligned");
+    if (opt_status st = train_pending()) return st;
+    p.term = (float*)ws;
+    const hipStream_t s = (hipStream_t)stream;
+    if (a->rows) {
+        if (a->dtype == OPT_F32) launch_rows<float>(p, a->rows, s);
+        else if (a->dtype == OPT_BF16) launch_rows<__bf16>(p, a->rows, s);
+        else launch_rows<_Float16>(p, a->rows, s);
+    }
+    policy_sum_kernel<<<1, kLossThreads, 0, s>>>(a->rows, p.term, loss);
+    return train_launched("policy loss");
+}
+
+}  // namespace
+}  // namespace matopt
+
+using namespace matopt;
+
+extern "C" {
+
+opt_status opt_policy_loss_workspace_size(const opt_policy_desc* a, uint64_t* bytes) {
+    if (!bytes) return fail(OPT_EINVAL, "bytes is NULL");
+    if (opt_status st = check_policy(a)) return st;
+    *bytes = policy_bytes(a);
+    return OPT_OK;
+}
+
+opt_status opt_policy_loss_forward(const opt_policy_desc* a, const void* logits, const opt_policy_rows* in,
+                                   float* loss, float* logp, float* lse, float* slope, void* workspace,
+                                   uint64_t workspace_bytes, void* stream) {
+    if (opt_status st = check_policy(a)) return st;
+    PolicyArgs p = policy_args(a, logits, in);
+    if (a->rows) {
+        if (opt_status st = check_vector(logits, train_bytes(a->dtype), "logits")) return st;
+        if (opt_status st = check_rows(a, in)) return st;
+        if (opt_status st = check_vector(logp, 4, "logp")) return st;
+        if (opt_status st = check_vector(lse, 4, "lse")) return st;
+        if (opt_status st = check_vector(slope, 4, "slope")) return st;
+        p.logp = logp, p.lse = lse, p.slope = slope;
+    }
+    return run_rows(a, p, loss, workspace, workspace_bytes, stream);
+}
+
+opt_status opt_policy_loss_step(const opt_policy_desc* a, const void* logits, const opt_policy_rows* in, float grad,
+                                float* loss, float* logp, void* dlogits, int64_t ldd, void* workspace,
+                                uint64_t workspace_bytes, void* stream) {
+    if (opt_status st = check_policy(a)) return st;
+    PolicyArgs p = policy_args(a, logits, in);
+    if (a->rows) {
+        if (opt_status st = check_vector(logits, train_bytes(a->dtype), "logits")) return st;
+        if (opt_status st = check_rows(a, in)) return st;
+        if (opt_status st = check_dlogits(a, logits, dlogits, ldd)) return st;
+        if (!train_aligned(logp, 4)) return fail(OPT_EINVAL, "logp is not aligned to its element size");
+        p.logp = logp, p.dlogits = dlogits, p.ldd = ldd, p.grad = grad;
+    }
+    return run_rows(a, p, loss, workspace, workspace_bytes, stream);
+}
+
+opt_status opt_policy_loss_backward(const opt_policy_desc* a, const void* logits, const void* target,
+                                    const float* lse, const float* slope, const float* grad, void* dlogits,
+                                    int64_t ldd, void* stream) {
+    if (opt_status st = check_policy(a)) return st;
+    if (a->rows == 0) return OPT_OK;
+    if (opt_status st = check_vector(logits, train_bytes(a->dtype), "logits")) return st;
+    if (opt_status st = check_vector(target, a->target_i64 ? 8 : 4, "target")) return st;
+    if (opt_status st = check_vector(lse, 4, "lse")) return st;
+    if (opt_status st = check_vector(slope, 4, "slope")) return st;
+    if (opt_status st = check_dlogits(a, logits, dlogits, ldd)) return st;
+    if (!train_aligned(grad, 4)) return fail(OPT_EINVAL, "grad is not aligned to its element size");
+    const int64_t chunks = ((a->vocab + 7) / 8 + kBackThreads * kBackPer - 1) / (kBackThreads * kBackPer);
+    if (chunks > 65535) return fail(OPT_EUNSUPPORTED, "vocab too large");
+    if (opt_status st = train_pending()) return st;
+    PolicyArgs p = policy_args(a, logits, nullptr);
+    p.target = target, p.lse = (float*)lse, p.slope = (float*)slope, p.dlogits = dlogits, p.ldd = ldd;
+    const dim3 grid((uint32_t)a->rows, (uint32_t)chunks);
+    const hipStream_t s = (hipStream_t)stream;
+    if (a->dtype == OPT_F32) policy_backward_kernel<float><<<grid, kBackThreads, 0, s>>>(p, grad);
+    else if (a->dtype == OPT_BF16) policy_backward_kernel<__bf16><<<grid, kBackThreads, 0, s>>>(p, grad);
+    else policy_backward_kernel<_Float16><<<grid, kBackThreads, 0, s>>>(p, grad);
+    return train_launched("policy loss backward");
+}
+
+}  // extern "C"

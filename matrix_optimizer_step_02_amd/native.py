@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(HERE, "_lib", "libmatopt.so")
 
 OPT_OK, OPT_EINVAL, OPT_ENOWS, OPT_EHIP, OPT_EUNSUPPORTED, OPT_ESTATE = 0, -1, -2, -3, -4, -5
 OPT_F32, OPT_BF16 = 0, 1
+OPT_F16 = 2   # the training-pass operators only
 OPT_FLAG_ROTATED_MOMENTUM = 1
 OPT_FLAG_BF16_ROTATION = 2
 OPT_FLAG_MUON = 4
@@ -33,6 +34,13 @@ EXPORTED = (
     "opt_gemm", "opt_gemm_x6", "opt_gemm_bf16", "opt_orthonormalize_workspace_size", "opt_orthonormalize",
     "opt_partition_dp", "opt_plan_host_ranks", "opt_group_health", "opt_group_reorthonormalize",
     "opt_orthonormalize_static", "opt_group_read_group_timing", "opt_group_workspace_parts",
+)
+
+# include/matopt_train.h: the training-pass operators
+EXPORTED_TRAIN = (
+    "opt_attention_workspace_size", "opt_attention_forward", "opt_attention_backward", "opt_dropout",
+    "opt_layer_norm_forward", "opt_layer_norm_workspace_size", "opt_layer_norm_backward",
+    "opt_policy_loss_workspace_size", "opt_policy_loss_forward", "opt_policy_loss_backward", "opt_policy_loss_step",
 )
 
 
@@ -64,6 +72,37 @@ class opt_health(C.Structure):
         ("orth_U", C.c_double), ("orth_V", C.c_double), ("v_mean_abs", C.c_double), ("v_std", C.c_double),
         ("v_min", C.c_double), ("v_max", C.c_double), ("nonfinite", C.c_int64),
     ]
+
+
+class opt_attention_desc(C.Structure):
+    _fields_ = [
+        ("dtype", C.c_int32), ("batch", C.c_int32), ("heads", C.c_int32), ("kv_heads", C.c_int32),
+        ("head_dim", C.c_int32), ("q_len", C.c_int32), ("k_len", C.c_int32), ("causal", C.c_int32),
+        ("window", C.c_int32), ("scale", C.c_float), ("q_start", C.c_void_p), ("k_start", C.c_void_p),
+        ("q_tokens", C.c_int64), ("k_tokens", C.c_int64), ("q_lens", C.c_void_p), ("k_lens", C.c_void_p),
+    ]
+
+
+class opt_attention_tensor(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("batch_stride", C.c_int64), ("token_stride", C.c_int64),
+                ("head_stride", C.c_int64)]
+
+
+class opt_rng(C.Structure):
+    _fields_ = [("seed", C.c_uint64), ("offset", C.c_uint64), ("device_offset", C.c_void_p)]
+
+
+class opt_policy_desc(C.Structure):
+    _fields_ = [
+        ("dtype", C.c_int32), ("target_i64", C.c_int32), ("rows", C.c_int64), ("vocab", C.c_int64),
+        ("ld", C.c_int64), ("logit_scale", C.c_float), ("clip_low", C.c_float), ("clip_high", C.c_float),
+        ("kl_coef", C.c_float),
+    ]
+
+
+class opt_policy_rows(C.Structure):
+    _fields_ = [("target", C.c_void_p), ("old_logp", C.c_void_p), ("ref_logp", C.c_void_p),
+                ("advantage", C.c_void_p), ("weight", C.c_void_p)]
 
 
 _lib: Optional[C.CDLL] = None
@@ -108,6 +147,23 @@ def load(path: str = LIB_PATH) -> C.CDLL:
                               C.POINTER(i32), C.POINTER(C.c_double)], i32),
         "opt_plan_host_ranks": ([C.POINTER(C.c_double), C.POINTER(u64), i64, i32, u64, C.POINTER(i32),
                                  C.POINTER(i32), C.POINTER(i32), C.POINTER(i32)], i32),
+    }
+    A, T, R = C.POINTER(opt_attention_desc), C.POINTER(opt_attention_tensor), C.POINTER(opt_rng)
+    P, PR = C.POINTER(opt_policy_desc), C.POINTER(opt_policy_rows)
+    sig |= {
+        "opt_attention_workspace_size": ([A, i32, C.POINTER(u64)], i32),
+        "opt_attention_forward": ([A, T, T, T, T, vp, vp, u64, vp], i32),
+        "opt_attention_backward": ([A, T, T, T, T, T, vp, T, T, T, vp, u64, vp], i32),
+        "opt_dropout": ([i64, i64, i32, vp, i64, vp, i64, vp, i64, f32, R, vp], i32),
+        "opt_layer_norm_forward": ([i64, i64, i32, vp, i64, i32, vp, i64, vp, vp, f32, f32, R, vp, i64, vp, i64, vp,
+                                    vp, vp], i32),
+        "opt_layer_norm_workspace_size": ([i64, i64, C.POINTER(u64)], i32),
+        "opt_layer_norm_backward": ([i64, i64, i32, vp, i64, i32, vp, i64, vp, i64, vp, vp, vp, f32, R, vp, i64, vp,
+                                     i64, vp, vp, vp, u64, vp], i32),
+        "opt_policy_loss_workspace_size": ([P, C.POINTER(u64)], i32),
+        "opt_policy_loss_forward": ([P, vp, PR, vp, vp, vp, vp, vp, u64, vp], i32),
+        "opt_policy_loss_backward": ([P, vp, vp, vp, vp, vp, vp, i64, vp], i32),
+        "opt_policy_loss_step": ([P, vp, PR, f32, vp, vp, vp, i64, vp, u64, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -280,3 +336,72 @@ def opt_plan_host_ranks(cost: Sequence[float], nbytes: Sequence[int], ranks: int
     _check(load().opt_plan_host_ranks(c, b, n, ranks, capacity_bytes, order, group_of, host_of,
                                           C.byref(ng)))
     return list(order)[:n], list(group_of)[:n], list(host_of)[:n], ng.value
+
+
+# ------------------------------------------- training-pass operators ----
+
+
+def opt_attention_workspace_size(a: opt_attention_desc, backward: int) -> int:
+    out = C.c_uint64(0)
+    _check(load().opt_attention_workspace_size(a, backward, out))
+    return out.value
+
+
+def opt_attention_forward(a, q, k, v, out, lse: int, workspace: int, workspace_bytes: int, stream_ptr: int):
+    _check(load().opt_attention_forward(a, q, k, v, out, lse, workspace, workspace_bytes, stream_ptr))
+
+
+def opt_attention_backward(a, dout, q, k, v, out, lse: int, dq, dk, dv, workspace: int, workspace_bytes: int,
+                           stream_ptr: int):
+    _check(load().opt_attention_backward(a, dout, q, k, v, out, lse, dq, dk, dv, workspace, workspace_bytes,
+                                         stream_ptr))
+
+
+def opt_dropout(rows: int, cols: int, dtype: int, x: int, ldx: int, residual: int, ldr: int, y: int, ldy: int,
+                p: float, rng: Optional[opt_rng], stream_ptr: int):
+    _check(load().opt_dropout(rows, cols, dtype, x, ldx, residual, ldr, y, ldy, p, rng, stream_ptr))
+
+
+def opt_layer_norm_forward(rows: int, cols: int, dtype: int, x: int, ldx: int, h_dtype: int, residual: int, ldr: int,
+                           weight: int, bias: int, eps: float, p: float, rng: Optional[opt_rng], y: int, ldy: int,
+                           h: int, ldh: int, mean: int, rstd: int, stream_ptr: int):
+    _check(load().opt_layer_norm_forward(rows, cols, dtype, x, ldx, h_dtype, residual, ldr, weight, bias, eps, p,
+                                         rng, y, ldy, h, ldh, mean, rstd, stream_ptr))
+
+
+def opt_layer_norm_workspace_size(rows: int, cols: int) -> int:
+    out = C.c_uint64(0)
+    _check(load().opt_layer_norm_workspace_size(rows, cols, out))
+    return out.value
+
+
+def opt_layer_norm_backward(rows: int, cols: int, dtype: int, dy: int, lddy: int, h_dtype: int, h: int, ldh: int,
+                            dh: int, lddh: int, weight: int, mean: int, rstd: int, p: float, rng: Optional[opt_rng],
+                            dx: int, lddx: int, dres: int, lddres: int, dweight: int, dbias: int, workspace: int,
+                            workspace_bytes: int, stream_ptr: int):
+    _check(load().opt_layer_norm_backward(rows, cols, dtype, dy, lddy, h_dtype, h, ldh, dh, lddh, weight, mean, rstd,
+                                          p, rng, dx, lddx, dres, lddres, dweight, dbias, workspace,
+                                          workspace_bytes, stream_ptr))
+
+
+def opt_policy_loss_workspace_size(a: opt_policy_desc) -> int:
+    out = C.c_uint64(0)
+    _check(load().opt_policy_loss_workspace_size(a, out))
+    return out.value
+
+
+def opt_policy_loss_forward(a, logits: int, rows, loss: int, logp: int, lse: int, slope: int, workspace: int,
+                            workspace_bytes: int, stream_ptr: int):
+    _check(load().opt_policy_loss_forward(a, logits, rows, loss, logp, lse, slope, workspace, workspace_bytes,
+                                          stream_ptr))
+
+
+def opt_policy_loss_backward(a, logits: int, target: int, lse: int, slope: int, grad: int, dlogits: int, ldd: int,
+                             stream_ptr: int):
+    _check(load().opt_policy_loss_backward(a, logits, target, lse, slope, grad, dlogits, ldd, stream_ptr))
+
+
+def opt_policy_loss_step(a, logits: int, rows, grad: float, loss: int, logp: int, dlogits: int, ldd: int,
+                         workspace: int, workspace_bytes: int, stream_ptr: int):
+    _check(load().opt_policy_loss_step(a, logits, rows, grad, loss, logp, dlogits, ldd, workspace, workspace_bytes,
+                                       stream_ptr))

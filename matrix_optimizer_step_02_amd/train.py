@@ -1,0 +1,418 @@
+"""The training pass's operators on torch tensors: attention, layer norm,
+dropout and the clipped policy loss, each with its backward pass.
+
+Functions check their tensors, allocate what they return and call the C entry
+points of include/matopt_train.h on the given stream (default: the current
+one). There is no autograd graph: a backward function is called with what its
+forward function returned, and its results are ordinary tensors (a weight's
+gradient goes into the G of a RotatedAdamGroup). All shapes and argument errors
+raise before anything is launched.
+"""
+
+from __future__ import annotations
+
+import ctypes as C
+import math
+from dataclasses import dataclass
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import native
+
+__all__ = ["Rng", "attention_forward", "attention_backward", "dropout", "dropout_backward", "layer_norm_forward",
+           "layer_norm_backward", "PolicyForward", "policy_loss_forward", "policy_loss_backward", "policy_loss_step"]
+
+_DTYPE = {torch.float32: native.OPT_F32, torch.bfloat16: native.OPT_BF16, torch.float16: native.OPT_F16}
+
+
+@dataclass(frozen=True)
+class Rng:
+    """Where dropout's random bits come from: the same (seed, offset) give the
+    same mask. ``device_offset``: an int64 tensor of one element added to
+    offset on the device, for a step counter that a replayed graph reads."""
+    seed: int
+    offset: int = 0
+    device_offset: Optional[torch.Tensor] = None
+
+    def c(self) -> native.opt_rng:
+        d = self.device_offset
+        if d is not None and (d.dtype != torch.int64 or d.numel() != 1 or d.device.type != "cuda"):
+            raise ValueError("device_offset must be one int64 element on a HIP device")
+        m = (1 << 64) - 1
+        return native.opt_rng(self.seed & m, self.offset & m, d.data_ptr() if d is not None else 0)
+
+
+def _stream(dev, stream):
+    """(handle, stream object when it is not the current one)."""
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on a HIP device")
+    cur = torch.cuda.current_stream(dev)
+    if stream is None or stream.cuda_stream == cur.cuda_stream:
+        return cur.cuda_stream, None
+    return stream.cuda_stream, stream
+
+
+def _used(other, *tensors):
+    """Tensors allocated here but used on another stream than the current one
+    must not be handed out again before that stream is done with them."""
+    if other is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(other)
+
+
+def _is(t, name, device, dtype, shape=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _vector(t, name, device, n, dtype=torch.float32):
+    _is(t, name, device, dtype, (n,))
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _code(t, name):
+    try:
+        return _DTYPE[t.dtype]
+    except KeyError:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {tuple(_DTYPE)}") from None
+
+
+# -------------------------------------------------------------- attention ----
+
+
+def _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens):
+    packed = q_start is not None
+    if packed != (k_start is not None):
+        raise ValueError("q_start and k_start come together")
+    want = 3 if packed else 4
+    dev, dt = q.device, q.dtype
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _is(t, name, dev, dt)
+        if t.dim() != want:
+            raise ValueError(f"{name} must have {want} axes: " + ("(tokens, heads, dim)" if packed else
+                                                                  "(batch, tokens, heads, dim)"))
+    if k.shape != v.shape:
+        raise ValueError("k and v must have the same shape")
+    if dt not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"q has dtype {dt}, expected torch.bfloat16 or torch.float16")
+    heads, dim = q.shape[-2:]
+    kv_heads = k.shape[-2]
+    if k.shape[-1] != dim:
+        raise ValueError("q and k differ in head_dim")
+    a = native.opt_attention_desc()
+    if packed:
+        if q_lens is not None or k_lens is not None:
+            raise ValueError("packed sequences (q_start) have no q_lens or k_lens")
+        if max_q is None or max_k is None:
+            raise ValueError("packed sequences need max_q and max_k")
+        batch = q_start.numel() - 1
+        a.q_start = _vector(q_start, "q_start", dev, batch + 1, torch.int32)
+        a.k_start = _vector(k_start, "k_start", dev, batch + 1, torch.int32)
+        a.q_len, a.k_len = max_q, max_k
+        a.q_tokens, a.k_tokens = q.shape[0], k.shape[0]
+    else:
+        batch = q.shape[0]
+        if k.shape[0] != batch:
+            raise ValueError("q and k differ in batch")
+        a.q_len, a.k_len = q.shape[1], k.shape[1]
+        if q_lens is not None:
+            a.q_lens = _vector(q_lens, "q_lens", dev, batch, torch.int32)
+        if k_lens is not None:
+            a.k_lens = _vector(k_lens, "k_lens", dev, batch, torch.int32)
+    a.dtype, a.batch, a.heads, a.kv_heads, a.head_dim = _DTYPE[dt], batch, heads, kv_heads, dim
+    a.causal, a.window = bool(causal), window
+    a.scale = 1.0 / math.sqrt(dim) if scale is None else scale
+    return a, dev
+
+
+def _bhtd(t, name):
+    s = t.stride()
+    if s[-1] != 1 and t.shape[-1] != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    if len(s) == 3:
+        return native.opt_attention_tensor(t.data_ptr(), 0, s[0], s[1])
+    return native.opt_attention_tensor(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _out(given, name, like, dev):
+    if given is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=dev)
+    _is(given, name, dev, like.dtype, like.shape)
+    return given
+
+
+def _workspace(size, desc, backward, dev):
+    n = size(desc, backward)
+    return (torch.empty(n, dtype=torch.uint8, device=dev) if n else None), n
+
+
+def attention_forward(q, k, v, *, causal=False, window=0, scale=None, q_start=None, k_start=None, max_q=None,
+                      max_k=None, q_lens=None, k_lens=None, out=None, stream=None):
+    """(out, lse) of softmax(scale q k^T) v. q is (batch, tokens, heads, dim);
+    k and v (batch, tokens, kv_heads, dim); any strides with a contiguous last
+    axis. Packed sequences: q, k, v without the batch axis, q_start and k_start
+    int32 offsets of batch + 1, max_q and max_k the longest lengths. Padded
+    batches: q_lens, k_lens int32 lengths. lse is fp32, (heads, all query
+    tokens). scale defaults to dim^-1/2."""
+    a, dev = _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens)
+    st, other = _stream(dev, stream)
+    o = _out(out, "out", q, dev)
+    lse = torch.empty((q.shape[-2], q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]), dtype=torch.float32,
+                      device=dev)
+    ws, n = _workspace(native.opt_attention_workspace_size, a, 0, dev)
+    native.opt_attention_forward(a, _bhtd(q, "q"), _bhtd(k, "k"), _bhtd(v, "v"), _bhtd(o, "out"), lse.data_ptr(),
+                                 ws.data_ptr() if n else 0, n, st)
+    _used(other, o if out is None else None, lse, ws)
+    return o, lse
+
+
+def attention_backward(dout, q, k, v, out, lse, *, causal=False, window=0, scale=None, q_start=None, k_start=None,
+                       max_q=None, max_k=None, q_lens=None, k_lens=None, dq=None, dk=None, dv=None, stream=None):
+    """(dq, dk, dv) from the output's gradient and what attention_forward took
+    and returned. dq, dk, dv may be given, for instance as views of one
+    projection's gradient."""
+    a, dev = _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens)
+    _is(dout, "dout", dev, q.dtype, q.shape)
+    _is(out, "out", dev, q.dtype, q.shape)
+    _is(lse, "lse", dev, torch.float32, (q.shape[-2], q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]))
+    if not lse.is_contiguous():
+        raise ValueError("lse must be contiguous")
+    if dout.stride(-1) != 1:   # an expanded gradient has stride 0
+        dout = dout.contiguous()
+    st, other = _stream(dev, stream)
+    gq, gk, gv = _out(dq, "dq", q, dev), _out(dk, "dk", k, dev), _out(dv, "dv", v, dev)
+    ws, n = _workspace(native.opt_attention_workspace_size, a, 1, dev)
+    native.opt_attention_backward(a, _bhtd(dout, "dout"), _bhtd(q, "q"), _bhtd(k, "k"), _bhtd(v, "v"),
+                                  _bhtd(out, "out"), lse.data_ptr(), _bhtd(gq, "dq"), _bhtd(gk, "dk"),
+                                  _bhtd(gv, "dv"), ws.data_ptr() if n else 0, n, st)
+    _used(other, dout, None if dq is not None else gq, None if dk is not None else gk,
+          None if dv is not None else gv, ws)
+    return gq, gk, gv
+
+
+# ---------------------------------------------------------------- dropout ----
+
+
+def _rows(t, name):
+    """(data pointer, row stride) of a tensor as rows x cols over its last
+    axis; the leading axes must collapse to one stride."""
+    if t.dim() == 2:
+        s0, s1 = t.stride()
+        if s1 != 1 and t.shape[1] > 1:
+            raise ValueError(f"the last axis of {name} must be contiguous")
+        return t.data_ptr(), s0 if t.shape[0] > 1 else max(s0, t.shape[1])
+    if t.dim() < 2 or t.is_contiguous():
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr(), t.shape[-1] if t.dim() else 1
+    try:
+        v = t.view(-1, t.shape[-1])
+    except RuntimeError:
+        raise ValueError(f"the leading axes of {name} must collapse to one stride") from None
+    return _rows(v, name)
+
+
+def _size(t):
+    cols = t.shape[-1] if t.dim() else 1
+    return (t.numel() // cols if cols else 0), cols
+
+
+def _p_rng(p, rng):
+    if p > 0 and rng is None:
+        raise ValueError("dropout needs an rng")
+    return rng.c() if rng is not None and p > 0 else None
+
+
+def dropout(x, p, rng, *, residual=None, out=None, stream=None):
+    """residual + dropout(x) (no residual: dropout(x)); out may be x or
+    residual. The mask depends on rng and on an element's position in x
+    (leading axes as rows, the last axis as columns)."""
+    dev, dt, bits = x.device, _code(x, "x"), _p_rng(p, rng)
+    rows, cols = _size(x)
+    y = _out(out, "out", x, dev)
+    xp, ldx = _rows(x, "x")
+    yp, ldy = _rows(y, "out")
+    rp, ldr = 0, 0
+    if residual is not None:
+        _is(residual, "residual", dev, x.dtype, x.shape)
+        rp, ldr = _rows(residual, "residual")
+    st, other = _stream(dev, stream)
+    native.opt_dropout(rows, cols, dt, xp, ldx, rp, ldr, yp, ldy, p, bits, st)
+    _used(other, y if out is None else None)
+    return y
+
+
+def dropout_backward(dy, p, rng, *, out=None, stream=None):
+    """dropout's gradient with respect to x (the residual's is dy itself)."""
+    return dropout(dy, p, rng, out=out, stream=stream)
+
+
+# ------------------------------------------------------------- layer norm ----
+
+
+def layer_norm_forward(x, weight, bias=None, *, eps=1e-5, residual=None, p=0.0, rng=None, out=None, stream=None):
+    """(y, h, mean, rstd): h = residual + dropout(x) in the residual's type,
+    y its norm over the last axis in x's type. Without residual and dropout h
+    is x. weight and bias are fp32."""
+    dev, dt, bits = x.device, _code(x, "x"), _p_rng(p, rng)
+    rows, cols = _size(x)
+    y = _out(out, "out", x, dev)
+    xp, ldx = _rows(x, "x")
+    yp, ldy = _rows(y, "out")
+    wp = _vector(weight, "weight", dev, cols)
+    bp = _vector(bias, "bias", dev, cols) if bias is not None else 0
+    h, hp, ldh, rp, ldr, hdt = x, 0, 0, 0, 0, dt
+    if residual is not None or p > 0:
+        if residual is not None:
+            hdt = _code(residual, "residual")
+            _is(residual, "residual", dev, residual.dtype, x.shape)
+            rp, ldr = _rows(residual, "residual")
+        h = torch.empty(x.shape, dtype=x.dtype if residual is None else residual.dtype, device=dev)
+        hp, ldh = _rows(h, "h")
+    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev)
+    sp = stats.data_ptr()
+    st, other = _stream(dev, stream)
+    native.opt_layer_norm_forward(rows, cols, dt, xp, ldx, hdt, rp, ldr, wp, bp, eps, p, bits, yp, ldy, hp,
+                                  ldh, sp, sp + 4 * rows, st)
+    _used(other, y if out is None else None, h if hp else None, stats)
+    return y, h, stats[0], stats[1]
+
+
+def layer_norm_backward(dy, h, weight, mean, rstd, *, dh=None, p=0.0, rng=None, residual_grad=True, stream=None):
+    """(dx, dres, dweight, dbias) from y's gradient and what
+    layer_norm_forward returned; dh is the gradient that reaches h past the
+    norm. dres, h's gradient, goes to the residual; without dropout and in the
+    same type it is dx itself. residual_grad=False: dres is None."""
+    dev, dt, bits = dy.device, _code(dy, "dy"), _p_rng(p, rng)
+    rows, cols = _size(dy)
+    hdt = _code(h, "h")
+    _is(h, "h", dev, h.dtype, dy.shape)
+    dyp, lddy = _rows(dy, "dy")
+    hp, ldh = _rows(h, "h")
+    wp = _vector(weight, "weight", dev, cols)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _is(t, name, dev, torch.float32, dy.shape[:-1])
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    dhp, lddh = 0, 0
+    if dh is not None:
+        _is(dh, "dh", dev, h.dtype, dy.shape)
+        dhp, lddh = _rows(dh, "dh")
+    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dev)
+    dres, drp, lddr = None, 0, 0
+    if residual_grad:
+        if p == 0 and h.dtype == dy.dtype:
+            dres = dx
+        else:
+            dres = torch.empty(dy.shape, dtype=h.dtype, device=dev)
+            drp, lddr = _rows(dres, "dres")
+    n = native.opt_layer_norm_workspace_size(rows, cols)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    dwb = torch.empty((2, cols), dtype=torch.float32, device=dev)
+    dp = dwb.data_ptr()
+    st, other = _stream(dev, stream)
+    dxp, lddx = _rows(dx, "dx")
+    native.opt_layer_norm_backward(rows, cols, dt, dyp, lddy, hdt, hp, ldh, dhp, lddh, wp, mean.data_ptr(),
+                                   rstd.data_ptr(), p, bits, dxp, lddx, drp, lddr, dp, dp + 4 * cols,
+                                   ws.data_ptr(), n, st)
+    _used(other, dx, dres, dwb, ws)
+    return dx, dres, dwb[0], dwb[1]
+
+
+# ------------------------------------------------------------ policy loss ----
+
+
+class PolicyForward(NamedTuple):
+    """What policy_loss_forward returns: the loss (a scalar tensor) and per
+    row the target's log probability, the log-sum and d loss / d logp."""
+    loss: torch.Tensor
+    logp: torch.Tensor
+    lse: torch.Tensor
+    slope: torch.Tensor
+
+
+def _policy(logits, target, clip_low, clip_high, kl_coef, logit_scale):
+    if logits.dim() != 2:
+        raise ValueError("logits must have 2 axes (rows, vocab)")
+    dev = logits.device
+    rows, vocab = logits.shape
+    ptr, ld = _rows(logits, "logits")
+    if not isinstance(target, torch.Tensor) or target.dtype not in (torch.int32, torch.int64):
+        raise ValueError("target must be an int32 or int64 tensor")
+    tp = _vector(target, "target", dev, rows, target.dtype)
+    a = native.opt_policy_desc(_code(logits, "logits"), target.dtype == torch.int64, rows, vocab, ld, logit_scale,
+                               clip_low, clip_high, kl_coef)
+    return a, dev, ptr, tp
+
+
+def _policy_rows(tp, dev, n, old_logp, ref_logp, advantage, weight, kl_coef):
+    if ref_logp is None and kl_coef != 0:
+        raise ValueError("kl_coef needs ref_logp")
+    return native.opt_policy_rows(tp, _vector(old_logp, "old_logp", dev, n),
+                                  _vector(ref_logp, "ref_logp", dev, n) if ref_logp is not None else 0,
+                                  _vector(advantage, "advantage", dev, n), _vector(weight, "weight", dev, n))
+
+
+def policy_loss_forward(logits, target, old_logp, advantage, weight, *, ref_logp=None, clip_low=0.2, clip_high=0.2,
+                        kl_coef=0.0, logit_scale=1.0, stream=None):
+    """PolicyForward of the clipped policy loss with a KL term to a reference
+    policy: per row of logits (rows, vocab) a target token, its log
+    probability under the sampling and the reference policy, an advantage and
+    a weight (which holds the normalisation; 0 leaves the row out)."""
+    a, dev, lp, tp = _policy(logits, target, clip_low, clip_high, kl_coef, logit_scale)
+    rows = _policy_rows(tp, dev, a.rows, old_logp, ref_logp, advantage, weight, kl_coef)
+    st, other = _stream(dev, stream)
+    per = torch.empty((3, a.rows), dtype=torch.float32, device=dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    n = native.opt_policy_loss_workspace_size(a)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    native.opt_policy_loss_forward(a, lp, rows, loss.data_ptr(), per[0].data_ptr(), per[1].data_ptr(),
+                                   per[2].data_ptr(), ws.data_ptr(), n, st)
+    _used(other, per, loss, ws)
+    return PolicyForward(loss, per[0], per[1], per[2])
+
+
+def policy_loss_backward(logits, target, fwd, *, grad=None, logit_scale=1.0, out=None, stream=None):
+    """dlogits from policy_loss_forward's result; grad: the loss's gradient, a
+    scalar tensor on the device (None: 1). out may be logits."""
+    a, dev, lp, tp = _policy(logits, target, 0.2, 0.2, 0.0, logit_scale)
+    d = _out(out, "out", logits, dev)
+    dp, ldd = _rows(d, "out")
+    sp, ep = _vector(fwd.slope, "slope", dev, a.rows), _vector(fwd.lse, "lse", dev, a.rows)
+    gp = 0
+    if grad is not None:
+        _is(grad, "grad", dev, torch.float32, ())
+        gp = grad.data_ptr()
+    st, other = _stream(dev, stream)
+    native.opt_policy_loss_backward(a, lp, tp, ep, sp, gp, dp, ldd, st)
+    _used(other, d if out is None else None)
+    return d
+
+
+def policy_loss_step(logits, target, old_logp, advantage, weight, *, ref_logp=None, clip_low=0.2, clip_high=0.2,
+                     kl_coef=0.0, logit_scale=1.0, grad=1.0, out=None, stream=None):
+    """(loss, logp, dlogits) in one pass over the logits, for a loss that is
+    the last operator: grad, the loss's own gradient, is a number. out may be
+    logits."""
+    a, dev, lp, tp = _policy(logits, target, clip_low, clip_high, kl_coef, logit_scale)
+    rows = _policy_rows(tp, dev, a.rows, old_logp, ref_logp, advantage, weight, kl_coef)
+    d = _out(out, "out", logits, dev)
+    dp, ldd = _rows(d, "out")
+    st, other = _stream(dev, stream)
+    logp = torch.empty(a.rows, dtype=torch.float32, device=dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    n = native.opt_policy_loss_workspace_size(a)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    native.opt_policy_loss_step(a, lp, rows, grad, loss.data_ptr(), logp.data_ptr(), dp, ldd, ws.data_ptr(), n, st)
+    _used(other, d if out is None else None, logp, loss, ws)
+    return loss, logp, d

@@ -1,0 +1,185 @@
+"""GPU tests of the clipped policy loss against the fp64 oracle.
+
+The exponentials' arguments carry a relative error of 3 2^-24 of at most 100
+(in base 2), and a sum of V exponentials at most 192 2^-24 of itself (a thread
+adds at most 160 in turn, a tree the rest): lse and logp are within 2e-5,
+probabilities and exp(logp - old) within 5e-5 of themselves, and a gradient
+k (onehot - p) within 2e-4 of |k| (onehot + p) plus the output's rounding u.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import train_ops as T
+
+pytestmark = pytest.mark.gpu
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _train():
+    from matrix_optimizer_step_02_amd import train
+    return train
+
+
+U = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def make(rows, vocab, dtype, seed=0, i64=False, scale=1.0):
+    torch = _torch()
+    dt = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[dtype]
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = (2 * torch.randn(rows, vocab, generator=g, device="cuda")).to(dt)
+    t = torch.randint(0, vocab, (rows,), generator=g, device="cuda", dtype=torch.int64 if i64 else torch.int32)
+    x[torch.arange(rows), t.long()] += 5
+    z = x.double() * scale
+    logp = (z.gather(1, t.long()[:, None])[:, 0] - z.logsumexp(1)).float()
+    gap = torch.tensor([0.0, 0.1, -0.1, 0.5, -0.5, 2.0, -2.0], device="cuda").repeat(rows // 7 + 1)[:rows]
+    old, ref = logp - gap, logp + 0.3 * torch.randn(rows, generator=g, device="cuda")
+    adv = torch.randn(rows, generator=g, device="cuda")
+    w = torch.rand(rows, generator=g, device="cuda") / rows
+    if rows > 3:
+        w[1::5] = 0
+    return x, t, old, ref, adv, w
+
+
+def compare(got, x, t, old, ref, adv, w, dtype, kl, scale, grad=1.0, lo=0.2, hi=0.28):
+    r = T.policy_loss(np64(x), t.cpu().numpy(), np64(old), np64(ref), np64(adv), np64(w), lo, hi, kl, scale, grad)
+    terms = np.abs(r["term"])
+    # a term's own error: r within 5e-5, and the KL term's derivative |1 - e^d| times logp's 2e-5
+    slack = (2e-4 * (terms + np.abs(r["slope"])) + np.abs(np64(w)) * kl * 1e-5).sum() + 1e-12
+    assert abs(float(got["loss"]) - r["loss"]) <= slack
+    assert np.max(np.abs(np64(got["logp"]) - r["logp"])) <= 2e-5
+    if "lse" in got:
+        assert np.max(np.abs(np64(got["lse"]) - r["lse"])) <= 2e-5
+        assert np.max(np.abs(np64(got["slope"]) - r["slope"]) - 2e-4 * (np.abs(r["slope"]) + kl * np.abs(np64(w)))) <= 0
+    d, ref_d = np64(got["dlogits"]), r["dlogits"]
+    n = np.arange(len(t))
+    hot = np.zeros_like(d)
+    hot[n, np.clip(t.cpu().numpy(), 0, d.shape[1] - 1)] = 1
+    k = np.abs(grad * scale) * (np.abs(r["slope"]) + kl * np.abs(np64(w)))[:, None]
+    p = np.exp(scale * np64(x) - r["lse"][:, None])
+    tiny = 2.0 ** -25 if dtype == "f16" else 0
+    assert np.max(np.abs(d - ref_d) - (U[dtype] * np.abs(ref_d) + 2e-4 * k * (hot + p) + tiny + 1e-30)) <= 0
+
+
+SIZES = [(1, 1), (5, 2), (9, 7), (30, 8), (33, 1000), (20, 4096), (11, 4097), (9, 8193), (8, 16385), (6, 32769), (3, 65537),
+         (2, 81921), (3, 131072), (2, 131073), (2, 163841)]
+
+
+@pytest.mark.parametrize("rows,vocab", SIZES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_step_and_forward_backward(rows, vocab, dtype):
+    torch, train = _torch(), _train()
+    print(f"policy {rows}x{vocab} {dtype}", flush=True)
+    kl, scale = (0.1, 0.7) if rows % 2 else (0.0, 1.0)
+    x, t, old, ref, adv, w = make(rows, vocab, dtype, seed=vocab, i64=rows % 3 == 0, scale=scale)
+    how = dict(clip_low=0.2, clip_high=0.28, kl_coef=kl, logit_scale=scale, ref_logp=ref if kl else None)
+    loss, logp, d = train.policy_loss_step(x, t, old, adv, w, grad=2.0, **how)
+    compare({"loss": loss, "logp": logp, "dlogits": d}, x, t, old, ref, adv, w, dtype, kl, scale, grad=2.0)
+    f = train.policy_loss_forward(x, t, old, adv, w, **how)
+    d = train.policy_loss_backward(x, t, f, grad=torch.tensor(0.5, device="cuda"), logit_scale=scale)
+    compare({"loss": f.loss, "logp": f.logp, "lse": f.lse, "slope": f.slope, "dlogits": d}, x, t, old, ref, adv, w, dtype,
+            kl, scale, grad=0.5)
+    assert torch.equal(f.loss, loss) and torch.equal(f.logp, logp)
+
+
+@pytest.mark.parametrize("vocab", [100, 5000, 170001])
+def test_in_place_and_strided(vocab):
+    torch, train = _torch(), _train()
+    print(f"policy in place {vocab}", flush=True)
+    x, t, old, ref, adv, w = make(6, vocab, "bf16")
+    how = dict(ref_logp=ref, kl_coef=0.1)
+    loss, logp, d = train.policy_loss_step(x, t, old, adv, w, **how)
+    wide = torch.full((6, vocab + 13), float("nan"), device="cuda", dtype=torch.bfloat16)
+    v = wide[:, 3:3 + vocab]
+    v.copy_(x)
+    out = torch.full((6, vocab + 5), 7.0, device="cuda", dtype=torch.bfloat16)
+    loss2, logp2, d2 = train.policy_loss_step(v, t, old, adv, w, out=out[:, 2:2 + vocab], **how)
+    assert torch.equal(loss, loss2) and torch.equal(logp, logp2) and torch.equal(d, d2)
+    assert (out[:, :2] == 7).all() and (out[:, 2 + vocab:] == 7).all()
+    f = train.policy_loss_forward(x, t, old, adv, w, **how)
+    y = x.clone()
+    train.policy_loss_backward(y, t, f, out=y)
+    z = x.clone()
+    assert train.policy_loss_step(z, t, old, adv, w, out=z, **how)[2] is z
+    assert torch.equal(z, d)
+    assert (y.float() - d.float()).abs().max() <= 2.0 ** -7 * d.float().abs().max()
+
+
+@pytest.mark.parametrize("vocab", [1000, 40000, 170001])
+def test_rows_left_out_may_hold_anything(vocab):
+    torch, train = _torch(), _train()
+    print(f"policy masked {vocab}", flush=True)
+    x, t, old, ref, adv, w = make(10, vocab, "f32", i64=True)
+    want = train.policy_loss_step(x, t, old, adv, w, ref_logp=ref, kl_coef=0.1)
+    out = w == 0
+    x[out], t[out], old[out], ref[out], adv[out] = float("nan"), -100, float("nan"), float("inf"), float("nan")
+    got = train.policy_loss_step(x, t, old, adv, w, ref_logp=ref, kl_coef=0.1)
+    f = train.policy_loss_forward(x, t, old, adv, w, ref_logp=ref, kl_coef=0.1)
+    d = train.policy_loss_backward(x, t, f)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and (got[2][out] == 0).all()
+    assert torch.equal(f.loss, want[0]) and (d[out] == 0).all() and not d.isnan().any()
+
+
+@pytest.mark.parametrize("vocab", [1000, 170001])
+def test_infinite_logits_and_bad_targets(vocab):
+    """-inf hides a token (gradient 0); NaN, and a target outside the vocabulary, make their rows and the loss NaN."""
+    torch, train = _torch(), _train()
+    print(f"policy infinities {vocab}", flush=True)
+    x, t, old, ref, adv, w = make(4, vocab, "f32")
+    w[:] = 0.25
+    x[:, 5:300] = -float("inf")
+    x[torch.arange(4), t.long()] = 3.0
+    loss, logp, d = train.policy_loss_step(x, t, old, adv, w)
+    compare({"loss": loss, "logp": logp, "dlogits": d}, x, t, old, ref, adv, w, "f32", 0.0, 1.0, hi=0.2)
+    for bad in ("target", "negative", "nan", "all -inf"):
+        y, s = x.clone(), t.clone()
+        if bad == "target":
+            s[2] = vocab
+        elif bad == "negative":
+            s[2] = -1
+        elif bad == "nan":
+            y[2, 7] = float("nan")
+        else:
+            y[2] = -float("inf")
+        f = train.policy_loss_forward(y, s, old, adv, w)
+        g = train.policy_loss_backward(y, s, f)
+        loss, logp, d = train.policy_loss_step(y, s, old, adv, w)
+        for row in range(4):
+            assert bool(logp[row].isnan()) == (row == 2) and bool(f.logp[row].isnan()) == (row == 2), bad
+            assert bool(d[row].isnan().all()) == (row == 2) and bool(g[row].isnan().all()) == (row == 2), bad
+            assert bool(d[row].isnan().any()) == (row == 2), bad
+        assert loss.isnan() and f.loss.isnan()
+
+
+def test_no_rows_and_equal_bits():
+    torch, train = _torch(), _train()
+    print("policy empty, streams, graph", flush=True)
+    v = torch.zeros(0, device="cuda")
+    loss, logp, d = train.policy_loss_step(torch.zeros(0, 9, device="cuda"), torch.zeros(0, device="cuda", dtype=torch.int32), v, v, v)
+    assert float(loss) == 0 and d.shape == (0, 9)
+    x, t, old, ref, adv, w = make(300, 3001, "bf16")
+    how = dict(ref_logp=ref, kl_coef=0.1)
+    first = train.policy_loss_step(x, t, old, adv, w, **how)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = train.policy_loss_step(x, t, old, adv, w, stream=s, **how)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, other))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = train.policy_loss_step(x, t, old, adv, w, **how)
+    for n in range(3):
+        x.copy_(torch.randn_like(x))
+        g.replay()
+        torch.cuda.synchronize()
+        got = [a.clone() for a in held]
+        assert all(torch.equal(a, b) for a, b in zip(got, train.policy_loss_step(x, t, old, adv, w, **how))), n
