@@ -98,6 +98,8 @@ struct Geo {
     static __device__ __forceinline__ int swz(int row) {
         return DB > 2 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
     }
+    // swz(row + i rows of a chunk) ^ swz(row), for a row in the first chunk of a wavefront
+    static __device__ __forceinline__ constexpr int chunk_swz(int i) { return DB > 2 ? i & 3 : (2 * i) & 3; }
 };
 
 // Where one sequence's rows are.
@@ -136,32 +138,36 @@ __device__ __forceinline__ char* rows_of(const Tensor& t, int b, int64_t row0, i
     return t.p + (int64_t)b * t.batch + row0 * t.token + (int64_t)h * t.head;
 }
 
-// Copies 64-row tiles of one tensor into LDS.
-template <int DB>
+// Copies 64-row tiles of one tensor into LDS. Chunk i of a wavefront is 1024
+// bytes of rows; its lanes' rows and groups follow from chunk 0's (rows 1024 /
+// RB further, the swizzle's low slot bits counting chunks), so two registers
+// hold what the eight addresses of a tile need. PIN computes them anew for
+// each tile (a kernel short of registers; the others run 5 % faster with
+// them kept).
+template <int DB, bool PIN = false>
 struct Copy {
     using G = Geo<DB>;
-    uint32_t off[G::PER_WAVE];   // per lane: byte offset of its 16 bytes from the tile's first row
-    int row[G::PER_WAVE];        // its row; past any tile where its columns are past head_dim
+    int row0, group0;   // of chunk 0
     int64_t token;
 
-    __device__ __forceinline__ void init(int64_t token_stride, int head_dim) {
-        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    __device__ __forceinline__ void init(int64_t token_stride) {
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWaves;
         token = token_stride;
-#pragma unroll
-        for (int i = 0; i < G::PER_WAVE; ++i) {
-            row[i] = (wave * G::PER_WAVE + i) * (1024 / G::RB) + lane / G::SLOTS;
-            const int group = (lane % G::SLOTS) ^ G::swz(row[i]);
-            off[i] = (uint32_t)(row[i] * token_stride) + 16 * group;
-            if (8 * group >= head_dim) row[i] = 1 << 30;
-        }
+        row0 = wave * G::PER_WAVE * (1024 / G::RB) + lane / G::SLOTS;
+        group0 = (lane % G::SLOTS) ^ G::swz(row0);
     }
     // rows first .. first + 63 of a sequence of n rows
-    __device__ __forceinline__ void tile(char* lds, const char* base, int first, int n) const {
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    __device__ __forceinline__ void tile(char* lds, const char* base, int first, int n, int head_dim) const {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWaves;
         const char* origin = base + (int64_t)first * token;
+        int r0 = row0, g0 = group0;
+        if constexpr (PIN) asm volatile("" : "+v"(r0), "+v"(g0));
 #pragma unroll
         for (int i = 0; i < G::PER_WAVE; ++i) {
-            const void* src = row[i] < n - first ? (const void*)(origin + off[i]) : (const void*)g_attn_zero;
+            const int row = r0 + i * (1024 / G::RB), group = g0 ^ G::chunk_swz(i);
+            const uint32_t off = (uint32_t)row * (uint32_t)token + 16 * group;
+            const bool in = row < n - first && 8 * group < head_dim;
+            const void* src = in ? (const void*)(origin + off) : (const void*)g_attn_zero;
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                              (__attribute__((address_space(3))) void*)(lds + (wave * G::PER_WAVE + i) * 1024),
                                              16, 0, 0);
@@ -180,37 +186,45 @@ __device__ __forceinline__ void tile_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// A lane's LDS offsets within a tile.
+// A lane's LDS addresses of a tile. The swizzle is an exclusive or and tiles
+// are aligned to 1024 bytes, so one register per kind of read holds them all:
+// k step s flips bits 5 .. 7 of a row's address, the 32-column block d bits 6
+// and 7 of a transposed read's, its second half bit 5. `at` (a multiple of
+// 1024) reaches the tile of another tensor by the instruction's offset.
 template <class T, int DB>
 struct Lane {
     using G = Geo<DB>;
     using F = typename Frag<T>::type;
-    int rowo[2 * DB];   // A operand, k step s: row l % 32, group 2 s + l / 32
-    int tro[DB][2];     // transposed: columns of block db, rows 4 (l / 32) + l % 16 / 4 (+ 8)
+    uint32_t row0;   // A operand, k step 0: row l % 32, group l / 32
+    uint32_t col0;   // transposed, block 0: row 4 (l / 32) + l % 16 / 4
 
     __device__ __forceinline__ void init() {
         const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-#pragma unroll
-        for (int s = 0; s < 2 * DB; ++s) rowo[s] = l32 * G::RB + (((2 * s + h) ^ G::swz(l32)) << 4);
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int row = 8 * p + 4 * h + ((lane & 15) >> 2);
-                const int group = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-                tro[d][p] = row * G::RB + ((group ^ G::swz(row)) << 4) + 8 * (lane & 1);
-            }
+        row0 = l32 * G::RB + ((h ^ G::swz(l32)) << 4);
+        const int row = 4 * h + ((lane & 15) >> 2);
+        const int group = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        col0 = row * G::RB + ((group ^ G::swz(row)) << 4) + 8 * (lane & 1);
     }
+    // The same within the tile at `tile`.
+    __device__ __forceinline__ Lane in(const char* tile) const {
+        const uint32_t t = (uint32_t)(uintptr_t)(lds_char)tile;
+        return {row0 + t, col0 + t};
+    }
+    // Keeps what is derived from the two registers from being computed ahead
+    // and held over the code between (16 registers).
+    __device__ __forceinline__ void pin() { asm volatile("" : "+v"(row0), "+v"(col0)); }
     // rows 32 blk .. of the tile, k step s
-    __device__ __forceinline__ F rows(const char* tile, int blk, int s) const {
-        return *(const F*)(tile + rowo[s] + blk * 32 * G::RB);
+    __device__ __forceinline__ F rows(int at, int blk, int s) const {
+        typedef __attribute__((address_space(3))) const F* ptr;
+        return *(ptr)(lds_char)(uintptr_t)((row0 ^ (uint32_t)(s << 5)) + at + blk * 32 * G::RB);
     }
     // columns 32 d .. as rows of A, tile rows 16 st .. 16 st + 15 as k, in the accumulators' order
-    __device__ __forceinline__ F cols(const char* tile, int st, int d) const {
-        const lds_char t = (lds_char)tile;
+    __device__ __forceinline__ F cols(int at, int st, int d) const {
         typedef __attribute__((address_space(3))) s16x4* ptr;
-        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(t + tro[d][0] + st * 16 * G::RB));
-        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(t + tro[d][1] + st * 16 * G::RB));
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (ptr)(lds_char)(uintptr_t)((col0 ^ (uint32_t)(d << 6)) + at + st * 16 * G::RB));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (ptr)(lds_char)(uintptr_t)((col0 ^ (uint32_t)(d << 6 | 32)) + at + (16 * st + 8) * G::RB));
         return __builtin_bit_cast(F, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
 };
@@ -265,8 +279,8 @@ __device__ __forceinline__ void store_t(const f32x16 (&acc)[DB], float mul, char
 
 // Workgroup id -> (row block, head-and-batch index). Ids go to the XCDs in
 // turn, so id % 8 keeps a head on one XCD, whose L2 then serves its keys to
-// all its row blocks; `heavy_last` runs the blocks from the last to the first
-// (a causal sequence's last queries see the most keys), longest work first.
+// all its row blocks. Blocks run longest work first: `reverse` where that is
+// the last one (a causal sequence's last queries see the most keys).
 __device__ __forceinline__ void locate(int id, int blocks, int pairs, bool reverse, int& blk, int& pair) {
     if (pairs % 8 == 0) {
         const int per = pairs / 8, r = id / 8;
@@ -310,8 +324,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_forward_kernel(AttnArgs a
     F qf[2 * DB];
     load_rows<T, DB>(qf, rows_of(a.q, b, sq.q0, hq), a.q.token, i, sq.nq, a.head_dim);
     Copy<DB> ck, cv;
-    ck.init(a.k.token, a.head_dim);
-    cv.init(a.v.token, a.head_dim);
+    ck.init(a.k.token);
+    cv.init(a.v.token);
     const char* kb = rows_of(a.k, b, sq.k0, hk);
     const char* vb = rows_of(a.v, b, sq.k0, hk);
 
@@ -330,22 +344,23 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_forward_kernel(AttnArgs a
     auto kt = [&](int t) { return smem + (t & 1) * G::BYTES; };
     auto vt = [&](int t) { return smem + (2 + (t & 1)) * G::BYTES; };
     if (first_t < end_t) {
-        ck.tile(kt(first_t), kb, first_t * kTile, sq.nk);
-        cv.tile(vt(first_t), vb, first_t * kTile, sq.nk);
+        ck.tile(kt(first_t), kb, first_t * kTile, sq.nk, a.head_dim);
+        cv.tile(vt(first_t), vb, first_t * kTile, sq.nk, a.head_dim);
     }
     for (int t = first_t; t < end_t; ++t) {
         tile_barrier();
         if (t + 1 < end_t) {
-            ck.tile(kt(t + 1), kb, (t + 1) * kTile, sq.nk);
-            cv.tile(vt(t + 1), vb, (t + 1) * kTile, sq.nk);
+            ck.tile(kt(t + 1), kb, (t + 1) * kTile, sq.nk, a.head_dim);
+            cv.tile(vt(t + 1), vb, (t + 1) * kTile, sq.nk, a.head_dim);
         }
         if (t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
-        const char *kl = kt(t), *vl = vt(t);
+        const Lane<T, DB> at = ln.in(kt(t));
+        constexpr int K = 0, V = 2 * G::BYTES;
         f32x16 s[2] = {};
 #pragma unroll
         for (int ks = 0; ks < 2 * DB; ++ks)
 #pragma unroll
-            for (int n = 0; n < 2; ++n) s[n] = FT::mma(ln.rows(kl, n, ks), qf[ks], s[n]);
+            for (int n = 0; n < 2; ++n) s[n] = FT::mma(at.rows(K, n, ks), qf[ks], s[n]);
         if (t >= full_hi || t < full_lo || w0 + 32 > sq.nq) {
 #pragma unroll
             for (int n = 0; n < 2; ++n)
@@ -382,7 +397,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_forward_kernel(AttnArgs a
         for (int st = 0; st < 4; ++st) {
             const F p = pack8<T>(s[st >> 1], st & 1);
 #pragma unroll
-            for (int d = 0; d < DB; ++d) o[d] = FT::mma(ln.cols(vl, st, d), p, o[d]);
+            for (int d = 0; d < DB; ++d) o[d] = FT::mma(at.cols(V, st, d), p, o[d]);
         }
     }
     if (i >= sq.q_rows) return;
@@ -435,8 +450,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs a, int
         if (h == 0) gptr(a.delta)[at] = D;
     }
     Copy<DB> ck, cv;
-    ck.init(a.k.token, a.head_dim);
-    cv.init(a.v.token, a.head_dim);
+    ck.init(a.k.token);
+    cv.init(a.v.token);
     const char* kb = rows_of(a.k, b, sq.k0, hk);
     const char* vb = rows_of(a.v, b, sq.k0, hk);
     f32x16 dq[DB] = {};
@@ -451,25 +466,26 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs a, int
     auto kt = [&](int t) { return smem + (t & 1) * G::BYTES; };
     auto vt = [&](int t) { return smem + (2 + (t & 1)) * G::BYTES; };
     if (first_t < end_t) {
-        ck.tile(kt(first_t), kb, first_t * kTile, sq.nk);
-        cv.tile(vt(first_t), vb, first_t * kTile, sq.nk);
+        ck.tile(kt(first_t), kb, first_t * kTile, sq.nk, a.head_dim);
+        cv.tile(vt(first_t), vb, first_t * kTile, sq.nk, a.head_dim);
     }
     for (int t = first_t; t < end_t; ++t) {
         tile_barrier();
         if (t + 1 < end_t) {
-            ck.tile(kt(t + 1), kb, (t + 1) * kTile, sq.nk);
-            cv.tile(vt(t + 1), vb, (t + 1) * kTile, sq.nk);
+            ck.tile(kt(t + 1), kb, (t + 1) * kTile, sq.nk, a.head_dim);
+            cv.tile(vt(t + 1), vb, (t + 1) * kTile, sq.nk, a.head_dim);
         }
         if (t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
-        const char *kl = kt(t), *vl = vt(t);
+        const Lane<T, DB> at = ln.in(kt(t));
+        constexpr int K = 0, V = 2 * G::BYTES;
         const bool edge = t >= full_hi || t < full_lo;
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             f32x16 s = {}, dp = {};
 #pragma unroll
             for (int ks = 0; ks < 2 * DB; ++ks) {
-                s = FT::mma(ln.rows(kl, n, ks), qf[ks], s);
-                dp = FT::mma(ln.rows(vl, n, ks), gf[ks], dp);
+                s = FT::mma(at.rows(K, n, ks), qf[ks], s);
+                dp = FT::mma(at.rows(V, n, ks), gf[ks], dp);
             }
             if (edge) {
 #pragma unroll
@@ -484,7 +500,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs a, int
             for (int st = 0; st < 2; ++st) {
                 const F p = pack8<T>(s, st);
 #pragma unroll
-                for (int d = 0; d < DB; ++d) dq[d] = FT::mma(ln.cols(kl, 2 * n + st, d), p, dq[d]);
+                for (int d = 0; d < DB; ++d) dq[d] = FT::mma(at.cols(K, 2 * n + st, d), p, dq[d]);
             }
         }
     }
@@ -493,14 +509,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs a, int
 }
 
 // dK and dV of 128 keys, summed over the queries that see them and over the
-// heads of the group. A lane owns one key.
+// heads of the group. A lane owns one key. The keys' accumulators (128
+// registers at head_dim 128) and operands leave room for two wavefronts a
+// SIMD; two sets of four, each with LDS tiles of its own, take the steps
+// (query tile, head) of the same keys in turn and add their sums through LDS
+// at the end. Two workgroups of one set each would fill the SIMDs as well,
+// but a causal sequence's first keys have twice the mean work, and their
+// workgroup would run on alone at half the rate: 776 us against 600 at 8192
+// tokens, 16 / 8 heads of 128.
 template <class T, int DB>
-__global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnArgs a, int blocks) {
+__global__ __launch_bounds__(2 * 64 * kWaves, 2) void attn_dkv_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
     using FT = Frag<T>;
     using F = typename FT::type;
-    __shared__ __attribute__((aligned(1024))) char smem[4 * G::BYTES];
-    __shared__ __attribute__((aligned(16))) float stat[2][2][kTile];   // [buffer][L, D]
+    __shared__ __attribute__((aligned(1024))) char smem[8 * G::BYTES];
+    __shared__ __attribute__((aligned(16))) float stat[2][2][2][kTile];   // [set][buffer][L, -D]
     int blk, pair;
     locate(blockIdx.x, blocks, a.batch * a.kv_heads, false, blk, pair);
     const int b = pair / a.kv_heads, hk = pair % a.kv_heads, group = a.heads / a.kv_heads;
@@ -508,7 +531,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnArgs a, in
     const int j0 = blk * kRows;
     if (j0 >= sq.k_rows) return;
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % kWaves, set = wave8 / kWaves;
     const int w0 = j0 + 32 * wave, j = w0 + l32;   // the wavefront's first key, the lane's key
     const int off = sq.nk - sq.nq;
 
@@ -517,9 +540,9 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnArgs a, in
     F kf[2 * DB], vf[2 * DB];
     load_rows<T, DB>(kf, rows_of(a.k, b, sq.k0, hk), a.k.token, j, sq.nk, a.head_dim);
     load_rows<T, DB>(vf, rows_of(a.v, b, sq.k0, hk), a.v.token, j, sq.nk, a.head_dim);
-    Copy<DB> cq, cg;
-    cq.init(a.q.token, a.head_dim);
-    cg.init(a.dout.token, a.head_dim);
+    Copy<DB, true> cq, cg;
+    cq.init(a.q.token);
+    cg.init(a.dout.token);
     f32x16 dk[DB] = {}, dv[DB] = {};
     const float c = a.scale * kLog2e;
 
@@ -535,74 +558,114 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_dkv_kernel(AttnArgs a, in
     const int lo = qlo(j), hi = j < sq.nk ? qhi(j) : 0;
     const int full_lo = (qlo(max(wl, w0)) + kTile - 1) / kTile, full_hi = qhi(w0) / kTile;
 
-    auto qt = [&](int t) { return smem + (t & 1) * G::BYTES; };
-    auto gt = [&](int t) { return smem + (2 + (t & 1)) * G::BYTES; };
-    // step n: query tile n % tiles of the group's head n / tiles
-    auto fill = [&](int n) {
+    // buffers of turn r
+    auto qt = [&](int r) { return smem + (4 * set + (r & 1)) * G::BYTES; };
+    auto gt = [&](int r) { return smem + (4 * set + 2 + (r & 1)) * G::BYTES; };
+    // step n: query tile n % tiles of the group's head n / tiles; turn r of a set is step 2 r + set
+    const int steps = tiles * group, turns = (steps + 1) / 2;
+    auto fill = [&](int r) {
+        const int n = 2 * r + set;
+        if (n >= steps) return;
         const int hq = hk * group + n / tiles, first = (first_t + n % tiles) * kTile;
-        cq.tile(qt(n), rows_of(a.q, b, sq.q0, hq), first, sq.nq);
-        cg.tile(gt(n), rows_of(a.dout, b, sq.q0, hq), first, sq.nq);
-        if (threadIdx.x < kTile) {
-            const int i = first + threadIdx.x;
+        cq.tile(qt(r), rows_of(a.q, b, sq.q0, hq), first, sq.nq, a.head_dim);
+        cg.tile(gt(r), rows_of(a.dout, b, sq.q0, hq), first, sq.nq, a.head_dim);
+        if (wave == 0) {
+            const int i = first + lane;
             const int64_t at = (int64_t)hq * a.q_tokens + sq.l0 + i;
             float L = INFINITY, D = 0.f;
             if (i < sq.nq) {
                 L = gptr(a.lse)[at] * kLog2e;
                 if (L == -INFINITY) L = INFINITY;
-                D = gptr(a.delta)[at];
+                D = -gptr(a.delta)[at];
             }
-            stat[n & 1][0][threadIdx.x] = L;
-            stat[n & 1][1][threadIdx.x] = D;
+            stat[set][r & 1][0][lane] = L;
+            stat[set][r & 1][1][lane] = D;
         }
     };
-    const int steps = tiles * group;
-    if (steps > 0) fill(0);
-    for (int n = 0; n < steps; ++n) {
+    fill(0);
+    for (int r = 0; r < turns; ++r) {
         tile_barrier();
-        if (n + 1 < steps) fill(n + 1);
+        fill(r + 1);
+        const int n = 2 * r + set;
+        if (n >= steps) continue;
         const int t = first_t + n % tiles;
         if (t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
-        const char *ql = qt(n), *gl = gt(n);
+        Lane<T, DB> at = ln.in(qt(r));
+        constexpr int Q = 0, O = 2 * G::BYTES;
         const bool edge = t < full_lo || t >= full_hi || w0 + 32 > sq.nk;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            f32x16 s = {}, dp = {};
+            at.pin();
+            if constexpr (DB > 2) __builtin_amdgcn_sched_barrier(0);
+            // dP - D: the product starts from -D of the accumulator's rows
+            f32x16 s = {}, dp;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 D = *(const f32x4*)&stat[set][r & 1][1][32 * u + 8 * g + 4 * h];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dp[4 * g + e] = D[e];
+            }
 #pragma unroll
             for (int ks = 0; ks < 2 * DB; ++ks) {
-                s = FT::mma(ln.rows(ql, u, ks), kf[ks], s);
-                dp = FT::mma(ln.rows(gl, u, ks), vf[ks], dp);
+                s = FT::mma(at.rows(Q, u, ks), kf[ks], s);
+                dp = FT::mma(at.rows(O, u, ks), vf[ks], dp);
             }
             if (edge) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int i = t * kTile + 32 * u + 8 * (r >> 2) + 4 * h + (r & 3);
-                    if (i >= hi || i < lo) s[r] = -INFINITY;
+                for (int e = 0; e < 16; ++e) {
+                    const int i = t * kTile + 32 * u + 8 * (e >> 2) + 4 * h + (e & 3);
+                    if (i >= hi || i < lo) s[e] = -INFINITY;
                 }
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const f32x4 L = *(const f32x4*)&stat[n & 1][0][32 * u + 8 * g + 4 * h];
-                const f32x4 D = *(const f32x4*)&stat[n & 1][1][32 * u + 8 * g + 4 * h];
+                const f32x4 L = *(const f32x4*)&stat[set][r & 1][0][32 * u + 8 * g + 4 * h];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     s[4 * g + e] = __builtin_amdgcn_exp2f(fmaf(s[4 * g + e], c, -L[e]));
-                    dp[4 * g + e] = s[4 * g + e] * (dp[4 * g + e] - D[e]);
+                    dp[4 * g + e] *= s[4 * g + e];
                 }
             }
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
                 const F p = pack8<T>(s, st), ds = pack8<T>(dp, st);
+                if constexpr (DB > 2) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
-                    dv[d] = FT::mma(ln.cols(gl, 2 * u + st, d), p, dv[d]);
-                    dk[d] = FT::mma(ln.cols(ql, 2 * u + st, d), ds, dk[d]);
+                    dv[d] = FT::mma(at.cols(O, 2 * u + st, d), p, dv[d]);
+                    dk[d] = FT::mma(at.cols(Q, 2 * u + st, d), ds, dk[d]);
                 }
             }
         }
     }
+    // set 1's dK and set 0's dV cross over through LDS, and each set stores the sum it then has
+    static_assert(2 * kWaves * DB * 16 * 256 <= sizeof smem, "the accumulators do not fit the tiles' LDS");
+    tile_barrier();
+    float* mine = (float*)smem + (set * kWaves + wave) * DB * 1024 + lane * 4;
+    float* theirs = (float*)smem + ((1 - set) * kWaves + wave) * DB * 1024 + lane * 4;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            f32x4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = set ? dk[d][4 * g + e] : dv[d][4 * g + e];
+            *(f32x4*)(mine + (d * 4 + g) * 256) = x;
+        }
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const f32x4 x = *(const f32x4*)(theirs + (d * 4 + g) * 256);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (set) dv[d][4 * g + e] += x[e];
+                else dk[d][4 * g + e] += x[e];
+        }
     if (j >= sq.k_rows) return;
-    store_t<T, DB>(dk, a.scale, rows_of(a.dk, b, sq.k0, hk) + (int64_t)j * a.dk.token, a.head_dim);
-    store_t<T, DB>(dv, 1.f, rows_of(a.dv, b, sq.k0, hk) + (int64_t)j * a.dv.token, a.head_dim);
+    if (set) store_t<T, DB>(dv, 1.f, rows_of(a.dv, b, sq.k0, hk) + (int64_t)j * a.dv.token, a.head_dim);
+    else store_t<T, DB>(dk, a.scale, rows_of(a.dk, b, sq.k0, hk) + (int64_t)j * a.dk.token, a.head_dim);
 }
 
 // ------------------------------------------------------------------ host ----
@@ -674,7 +737,7 @@ void launch(Kind kind, const AttnArgs& x, hipStream_t s) {
     const dim3 g((uint32_t)grid), n(64 * kWaves);
     if (kind == FORWARD) attn_forward_kernel<T, DB><<<g, n, 0, s>>>(x, blocks);
     else if (kind == DQ) attn_dq_kernel<T, DB><<<g, n, 0, s>>>(x, blocks);
-    else attn_dkv_kernel<T, DB><<<g, n, 0, s>>>(x, blocks);
+    else attn_dkv_kernel<T, DB><<<g, dim3(2 * 64 * kWaves), 0, s>>>(x, blocks);
 }
 template <class T>
 void launch(Kind kind, const AttnArgs& x, hipStream_t s) {
