@@ -61,9 +61,10 @@ struct Tensor {
 struct AttnArgs {
     Tensor q, k, v, o, dout, dq, dk, dv;
     float *lse, *delta;
+    float *part, *part_m, *part_l;   // partial results of key splits (workspace)
     const int32_t *q_start, *k_start, *q_lens, *k_lens;
     int64_t q_tokens, k_tokens;   // rows of lse and delta; packed: the token axes
-    int32_t batch, heads, kv_heads, head_dim, q_len, k_len, causal, window;
+    int32_t batch, heads, kv_heads, head_dim, q_len, k_len, causal, window, splits;
     float scale;
 };
 
@@ -278,13 +279,16 @@ __device__ __forceinline__ void store_t(const f32x16 (&acc)[DB], float mul, char
 }
 
 // Workgroup id -> (row block, head-and-batch index). Ids go to the XCDs in
-// turn, so id % 8 keeps a head on one XCD, whose L2 then serves its keys to
-// all its row blocks. Blocks run longest work first: `reverse` where that is
-// the last one (a causal sequence's last queries see the most keys).
-__device__ __forceinline__ void locate(int id, int blocks, int pairs, bool reverse, int& blk, int& pair) {
+// turn, so id % 8 keeps a key head, with the `group` heads that share it, on
+// one XCD, whose L2 then serves its keys to all their row blocks; the heads of
+// one sequence spread over the XCDs, since sequences may differ in length.
+// Blocks run longest work first: `reverse` where that is the last one (a
+// causal sequence's last queries see the most keys).
+__device__ __forceinline__ void locate(int id, int blocks, int pairs, int group, bool reverse, int& blk, int& pair) {
     if (pairs % 8 == 0) {
-        const int per = pairs / 8, r = id / 8;
-        pair = (r % per) * 8 + id % 8;
+        if (pairs / group % 8) group = 1;
+        const int per = pairs / 8, r = id / 8, c = r % per;
+        pair = (c / group * 8 + id % 8) * group + c % group;
         blk = r / per;
     } else {
         pair = id % pairs;
@@ -300,22 +304,110 @@ struct Sight {
     __device__ __forceinline__ int lo(int i) const { return window ? max(i + off - window + 1, 0) : 0; }
 };
 
+// Why the forward and dQ kernels come with one or two sets of four wavefronts
+// per workgroup, and split the keys over workgroups. Registers leave room for
+// two wavefronts a SIMD, which come from two workgroups (SETS = 1) where the
+// launch has two a CU. Else a workgroup has two sets with LDS tiles of their
+// own, which take the key tiles in turn and join their sums through LDS. Where
+// the launch has fewer workgroups than the GPU has CUs (few queries on a long
+// context), the keys are also split over workgroups, which leave fp32 partial
+// sums in the workspace for a second kernel to join: 509 queries on 8192 keys,
+// 16 / 8 heads of 128, take 49 + 5 us in place of 215.
+struct Block {
+    int b, hq, hk, i0, split;
+};
+__device__ __forceinline__ Block block_of(const AttnArgs& a, int blocks) {
+    const int group = a.heads / a.kv_heads;
+    const int per = blocks * a.batch * a.heads;   // workgroups of one split
+    Block x;
+    x.split = blockIdx.x / per;
+    int blk, pair;
+    locate(blockIdx.x - x.split * per, blocks, a.batch * a.heads, group, a.causal, blk, pair);
+    x.b = pair / a.heads, x.hq = pair % a.heads, x.hk = x.hq / group, x.i0 = blk * kRows;
+    return x;
+}
+
+// Key tiles [first, end) of this workgroup's queries and split.
+__device__ __forceinline__ void tile_range(const AttnArgs& a, const Sight& see, int i0, int nq, int split, int& first, int& end) {
+    first = end = 0;
+    if (i0 >= nq) return;
+    first = see.lo(i0) / kTile;
+    end = (see.hi(min(i0 + kRows, nq) - 1) + kTile - 1) / kTile;
+    if (a.splits > 1) {
+        const int each = (max(end - first, 0) + a.splits - 1) / a.splits;
+        first += split * each;
+        end = min(end, first + each);
+    }
+}
+
+// Row of the partial results: (split, head, row of lse).
+__device__ __forceinline__ int64_t part_row(const AttnArgs& a, int split, int hq, int64_t row) {
+    return ((int64_t)split * a.heads + hq) * a.q_tokens + row;
+}
+
+// Lane's columns of a transposed accumulator as fp32 partial results.
+template <int DB>
+__device__ __forceinline__ void store_part(const f32x16 (&acc)[DB], float* row) {
+    const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = acc[d][4 * g + e];
+            *gptr((f32x4*)(row + 32 * d + 8 * g + 4 * h)) = v;
+        }
+}
+
+// Hands accumulators (and two more values) from set 1 to set 0 through the
+// LDS of the tiles, which every wavefront has left. kWaves * 64 * (16 DB + 2)
+// floats at most.
+template <int DB>
+__device__ __forceinline__ void give(char* smem, int wave, const f32x16 (&acc)[DB], float x, float y) {
+    const int lane = threadIdx.x & 63;
+    float* to = (float*)smem + wave * (DB * 1024 + 128);
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = acc[d][4 * g + e];
+            *(f32x4*)(to + (d * 4 + g) * 256 + lane * 4) = v;
+        }
+    to[DB * 1024 + lane] = x;
+    to[DB * 1024 + 64 + lane] = y;
+}
+template <int DB>
+__device__ __forceinline__ void take(const char* smem, int wave, float mine, float theirs, f32x16 (&acc)[DB]) {
+    const int lane = threadIdx.x & 63;
+    const float* from = (const float*)smem + wave * (DB * 1024 + 128);
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const f32x4 v = *(const f32x4*)(from + (d * 4 + g) * 256 + lane * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[d][4 * g + e] = acc[d][4 * g + e] * mine + v[e] * theirs;
+        }
+}
+
 // --------------------------------------------------------------- forward ----
 
-template <class T, int DB>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_forward_kernel(AttnArgs a, int blocks) {
+template <class T, int DB, int SETS>
+__global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_forward_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
     using FT = Frag<T>;
     using F = typename FT::type;
-    __shared__ __attribute__((aligned(1024))) char smem[4 * G::BYTES];
-    int blk, pair;
-    locate(blockIdx.x, blocks, a.batch * a.heads, a.causal, blk, pair);
-    const int b = pair / a.heads, hq = pair % a.heads, hk = hq / (a.heads / a.kv_heads);
+    __shared__ __attribute__((aligned(1024))) char smem[SETS * 4 * G::BYTES];
+    const Block wg = block_of(a, blocks);
+    const int b = wg.b, hq = wg.hq, hk = wg.hk, i0 = wg.i0;
     const Seq sq = sequence(a, b);
-    const int i0 = blk * kRows;
     if (i0 >= sq.q_rows) return;
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % kWaves;
+    const int set = SETS > 1 ? wave8 / kWaves : 0;
     const int w0 = i0 + 32 * wave, i = w0 + l32;   // the wavefront's first query, the lane's query
     const Sight see = {sq.nk, sq.nk - sq.nq, a.window, a.causal};
 
@@ -332,29 +424,31 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_forward_kernel(AttnArgs a
     f32x16 o[DB] = {};
     float m = kLowest, l = 0.f;
     const float c = a.scale * kLog2e;
-    // keys that any query of the workgroup sees, and of this wavefront
-    const int last = min(i0 + kRows, sq.nq) - 1, wlast = min(w0 + 32, sq.nq) - 1;
-    const int first_t = i0 < sq.nq ? see.lo(i0) / kTile : 0;
-    const int end_t = i0 < sq.nq ? (see.hi(last) + kTile - 1) / kTile : 0;
+    int first_t, end_t;
+    tile_range(a, see, i0, sq.nq, wg.split, first_t, end_t);
+    // keys that any query of this wavefront sees, and the lane's
+    const int wlast = min(w0 + 32, sq.nq) - 1;
     const int whi = w0 < sq.nq ? see.hi(wlast) : 0, wlo = see.lo(w0);
     const int hi = i < sq.nq ? see.hi(i) : 0, lo = see.lo(i);
-    // tiles below this index and at or above that one need no mask
+    // tiles from full_lo up to full_hi need no mask
     const int full_hi = see.hi(w0) / kTile, full_lo = (see.lo(max(wlast, w0)) + kTile - 1) / kTile;
 
-    auto kt = [&](int t) { return smem + (t & 1) * G::BYTES; };
-    auto vt = [&](int t) { return smem + (2 + (t & 1)) * G::BYTES; };
-    if (first_t < end_t) {
-        ck.tile(kt(first_t), kb, first_t * kTile, sq.nk, a.head_dim);
-        cv.tile(vt(first_t), vb, first_t * kTile, sq.nk, a.head_dim);
-    }
-    for (int t = first_t; t < end_t; ++t) {
+    // turn r of a set is tile first_t + SETS r + set, in buffers r & 1
+    auto kt = [&](int r) { return smem + (4 * set + (r & 1)) * G::BYTES; };
+    auto fill = [&](int r) {
+        const int t = first_t + SETS * r + set;
+        if (t >= end_t) return;
+        ck.tile(kt(r), kb, t * kTile, sq.nk, a.head_dim);
+        cv.tile(kt(r) + 2 * G::BYTES, vb, t * kTile, sq.nk, a.head_dim);
+    };
+    const int turns = (end_t - first_t + SETS - 1) / SETS;
+    fill(0);
+    for (int r = 0; r < turns; ++r) {
         tile_barrier();
-        if (t + 1 < end_t) {
-            ck.tile(kt(t + 1), kb, (t + 1) * kTile, sq.nk, a.head_dim);
-            cv.tile(vt(t + 1), vb, (t + 1) * kTile, sq.nk, a.head_dim);
-        }
-        if (t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
-        const Lane<T, DB> at = ln.in(kt(t));
+        fill(r + 1);
+        const int t = first_t + SETS * r + set;
+        if (t >= end_t || t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
+        const Lane<T, DB> at = ln.in(kt(r));
         constexpr int K = 0, V = 2 * G::BYTES;
         f32x16 s[2] = {};
 #pragma unroll
@@ -365,16 +459,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_forward_kernel(AttnArgs a
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int j = t * kTile + 32 * n + 8 * (r >> 2) + 4 * h + (r & 3);
-                    if (j >= hi || j < lo) s[n][r] = -INFINITY;
+                for (int e = 0; e < 16; ++e) {
+                    const int j = t * kTile + 32 * n + 8 * (e >> 2) + 4 * h + (e & 3);
+                    if (j >= hi || j < lo) s[n][e] = -INFINITY;
                 }
         }
         float mx = s[0][0];
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[n][r]);
+            for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[n][e]);
         if (__any(mx * c > m + kGrow)) {
             mx = fmaxf(mx, other_half(mx));
             const float mn = fmaxf(m, mx * c);
@@ -384,14 +478,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_forward_kernel(AttnArgs a
 #pragma unroll
             for (int d = 0; d < DB; ++d)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) o[d][r] *= k;
+                for (int e = 0; e < 16; ++e) o[d][e] *= k;
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                s[n][r] = __builtin_amdgcn_exp2f(fmaf(s[n][r], c, -m));
-                l += s[n][r];
+            for (int e = 0; e < 16; ++e) {
+                s[n][e] = __builtin_amdgcn_exp2f(fmaf(s[n][e], c, -m));
+                l += s[n][e];
             }
 #pragma unroll
         for (int st = 0; st < 4; ++st) {
@@ -400,29 +494,81 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_forward_kernel(AttnArgs a
             for (int d = 0; d < DB; ++d) o[d] = FT::mma(at.cols(V, st, d), p, o[d]);
         }
     }
-    if (i >= sq.q_rows) return;
     l += other_half(l);
+    if constexpr (SETS > 1) {
+        tile_barrier();
+        if (set == 1) give<DB>(smem, wave, o, m, l);
+        __syncthreads();
+        if (set == 1) return;
+        const float* from = (const float*)smem + wave * (DB * 1024 + 128) + DB * 1024 + lane;
+        const float m1 = from[0], l1 = from[64], mn = fmaxf(m, m1);
+        const float k0 = __builtin_amdgcn_exp2f(m - mn), k1 = __builtin_amdgcn_exp2f(m1 - mn);
+        take<DB>(smem, wave, k0, k1, o);
+        l = l * k0 + l1 * k1;
+        m = mn;
+    }
+    if (i >= sq.q_rows) return;
+    if (a.splits > 1) {
+        const int64_t row = part_row(a, wg.split, hq, sq.l0 + i);
+        store_part<DB>(o, a.part + row * (32 * DB));
+        if (h == 0) {
+            gptr(a.part_m)[row] = m;
+            gptr(a.part_l)[row] = l;
+        }
+        return;
+    }
     store_t<T, DB>(o, l == 0.f ? 0.f : 1.f / l, rows_of(a.o, b, sq.q0, hq) + (int64_t)i * a.o.token, a.head_dim);
     if (h == 0) gptr(a.lse)[(int64_t)hq * a.q_tokens + sq.l0 + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// Joins the key splits of one row: out and lse (ML), or the sum of partial
+// gradients times scale. Eight columns a thread, 16 threads a row.
+constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 16;
+template <class T, bool ML>
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int width, int blocks) {
+    const int b = blockIdx.x / blocks / a.heads, hq = blockIdx.x / blocks % a.heads;
+    const Seq sq = sequence(a, b);
+    const int i = blockIdx.x % blocks * kJoinRows + threadIdx.x / 16, col = threadIdx.x % 16 * 8;
+    if (i >= sq.q_rows || col >= a.head_dim) return;
+    float m = kLowest, l = 0.f, x[8] = {};
+    if constexpr (ML)
+        for (int s = 0; s < a.splits; ++s) m = fmaxf(m, gptr(a.part_m)[part_row(a, s, hq, sq.l0 + i)]);
+    for (int s = 0; s < a.splits; ++s) {
+        const int64_t row = part_row(a, s, hq, sq.l0 + i);
+        float v[8], k = 1.f;
+        if constexpr (ML) {
+            k = __builtin_amdgcn_exp2f(gptr(a.part_m)[row] - m);
+            l += gptr(a.part_l)[row] * k;
+        }
+        load8(a.part + row * width + col, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fmaf(v[e], k, x[e]);
+    }
+    const float mul = ML ? (l == 0.f ? 0.f : 1.f / l) : a.scale;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= mul;
+    const Tensor& t = ML ? a.o : a.dq;
+    store8((T*)(rows_of(t, b, sq.q0, hq) + (int64_t)i * t.token) + col, x);
+    if (ML && col == 0)
+        gptr(a.lse)[(int64_t)hq * a.q_tokens + sq.l0 + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // -------------------------------------------------------------- backward ----
 
 // dQ, and D for the other kernel. A lane owns one query, as in the forward pass.
-template <class T, int DB>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs a, int blocks) {
+template <class T, int DB, int SETS>
+__global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dq_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
     using FT = Frag<T>;
     using F = typename FT::type;
-    __shared__ __attribute__((aligned(1024))) char smem[4 * G::BYTES];
-    int blk, pair;
-    locate(blockIdx.x, blocks, a.batch * a.heads, a.causal, blk, pair);
-    const int b = pair / a.heads, hq = pair % a.heads, hk = hq / (a.heads / a.kv_heads);
+    __shared__ __attribute__((aligned(1024))) char smem[SETS * 4 * G::BYTES];
+    const Block wg = block_of(a, blocks);
+    const int b = wg.b, hq = wg.hq, hk = wg.hk, i0 = wg.i0;
     const Seq sq = sequence(a, b);
-    const int i0 = blk * kRows;
     if (i0 >= sq.q_rows) return;
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % kWaves;
+    const int set = SETS > 1 ? wave8 / kWaves : 0;
     const int w0 = i0 + 32 * wave, i = w0 + l32;
     const Sight see = {sq.nk, sq.nk - sq.nq, a.window, a.causal};
 
@@ -441,13 +587,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs a, int
             for (int e = 0; e < 8; ++e) D = fmaf((float)of[s][e], (float)gf[s][e], D);
         D += other_half(D);
     }
-    const int64_t at = (int64_t)hq * a.q_tokens + sq.l0 + i;
+    const int64_t at_row = (int64_t)hq * a.q_tokens + sq.l0 + i;
     // a row that sees no key has L = -inf: with +inf in its place P is 0
     float L2 = INFINITY;
     if (i < sq.nq) {
-        L2 = gptr(a.lse)[at] * kLog2e;
+        L2 = gptr(a.lse)[at_row] * kLog2e;
         if (L2 == -INFINITY) L2 = INFINITY;
-        if (h == 0) gptr(a.delta)[at] = D;
+        if (h == 0 && set == 0 && wg.split == 0) gptr(a.delta)[at_row] = D;
     }
     Copy<DB> ck, cv;
     ck.init(a.k.token);
@@ -456,27 +602,28 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs a, int
     const char* vb = rows_of(a.v, b, sq.k0, hk);
     f32x16 dq[DB] = {};
     const float c = a.scale * kLog2e;
-    const int last = min(i0 + kRows, sq.nq) - 1, wlast = min(w0 + 32, sq.nq) - 1;
-    const int first_t = i0 < sq.nq ? see.lo(i0) / kTile : 0;
-    const int end_t = i0 < sq.nq ? (see.hi(last) + kTile - 1) / kTile : 0;
+    int first_t, end_t;
+    tile_range(a, see, i0, sq.nq, wg.split, first_t, end_t);
+    const int wlast = min(w0 + 32, sq.nq) - 1;
     const int whi = w0 < sq.nq ? see.hi(wlast) : 0, wlo = see.lo(w0);
     const int hi = i < sq.nq ? see.hi(i) : 0, lo = see.lo(i);
     const int full_hi = see.hi(w0) / kTile, full_lo = (see.lo(max(wlast, w0)) + kTile - 1) / kTile;
 
-    auto kt = [&](int t) { return smem + (t & 1) * G::BYTES; };
-    auto vt = [&](int t) { return smem + (2 + (t & 1)) * G::BYTES; };
-    if (first_t < end_t) {
-        ck.tile(kt(first_t), kb, first_t * kTile, sq.nk, a.head_dim);
-        cv.tile(vt(first_t), vb, first_t * kTile, sq.nk, a.head_dim);
-    }
-    for (int t = first_t; t < end_t; ++t) {
+    auto kt = [&](int r) { return smem + (4 * set + (r & 1)) * G::BYTES; };
+    auto fill = [&](int r) {
+        const int t = first_t + SETS * r + set;
+        if (t >= end_t) return;
+        ck.tile(kt(r), kb, t * kTile, sq.nk, a.head_dim);
+        cv.tile(kt(r) + 2 * G::BYTES, vb, t * kTile, sq.nk, a.head_dim);
+    };
+    const int turns = (end_t - first_t + SETS - 1) / SETS;
+    fill(0);
+    for (int r = 0; r < turns; ++r) {
         tile_barrier();
-        if (t + 1 < end_t) {
-            ck.tile(kt(t + 1), kb, (t + 1) * kTile, sq.nk, a.head_dim);
-            cv.tile(vt(t + 1), vb, (t + 1) * kTile, sq.nk, a.head_dim);
-        }
-        if (t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
-        const Lane<T, DB> at = ln.in(kt(t));
+        fill(r + 1);
+        const int t = first_t + SETS * r + set;
+        if (t >= end_t || t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
+        const Lane<T, DB> at = ln.in(kt(r));
         constexpr int K = 0, V = 2 * G::BYTES;
         const bool edge = t >= full_hi || t < full_lo;
 #pragma unroll
@@ -489,13 +636,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs a, int
             }
             if (edge) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int j = t * kTile + 32 * n + 8 * (r >> 2) + 4 * h + (r & 3);
-                    if (j >= hi || j < lo) s[r] = -INFINITY;
+                for (int e = 0; e < 16; ++e) {
+                    const int j = t * kTile + 32 * n + 8 * (e >> 2) + 4 * h + (e & 3);
+                    if (j >= hi || j < lo) s[e] = -INFINITY;
                 }
             }
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -L2)) * (dp[r] - D);
+            for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -L2)) * (dp[e] - D);
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
                 const F p = pack8<T>(s, st);
@@ -504,34 +651,46 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs a, int
             }
         }
     }
-    if (i < sq.q_rows)
+    if constexpr (SETS > 1) {
+        tile_barrier();
+        if (set == 1) give<DB>(smem, wave, dq, 0.f, 0.f);
+        __syncthreads();
+        if (set == 1) return;
+        take<DB>(smem, wave, 1.f, 1.f, dq);
+    }
+    if (i >= sq.q_rows) return;
+    if (a.splits > 1)
+        store_part<DB>(dq, a.part + part_row(a, wg.split, hq, sq.l0 + i) * (32 * DB));
+    else
         store_t<T, DB>(dq, a.scale, rows_of(a.dq, b, sq.q0, hq) + (int64_t)i * a.dq.token, a.head_dim);
 }
 
 // dK and dV of 128 keys, summed over the queries that see them and over the
 // heads of the group. A lane owns one key. The keys' accumulators (128
 // registers at head_dim 128) and operands leave room for two wavefronts a
-// SIMD; two sets of four, each with LDS tiles of its own, take the steps
+// SIMD, which come from two workgroups (SETS = 1), or from two sets of four
+// wavefronts of one, each with LDS tiles of its own, that take the steps
 // (query tile, head) of the same keys in turn and add their sums through LDS
-// at the end. Two workgroups of one set each would fill the SIMDs as well,
-// but a causal sequence's first keys have twice the mean work, and their
-// workgroup would run on alone at half the rate: 776 us against 600 at 8192
-// tokens, 16 / 8 heads of 128.
-template <class T, int DB>
-__global__ __launch_bounds__(2 * 64 * kWaves, 2) void attn_dkv_kernel(AttnArgs a, int blocks) {
+// at the end. The common barrier costs 10 % where all key blocks have equal
+// work (1053 against 1163 us, 4 x 4096 tokens, 16 heads of 128). A causal
+// sequence's first keys have twice the mean work, though, and a workgroup of
+// one set runs on alone at half the rate: 777 against 553 us (8192 tokens, 16 /
+// 8 heads of 128).
+template <class T, int DB, int SETS>
+__global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dkv_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
     using FT = Frag<T>;
     using F = typename FT::type;
-    __shared__ __attribute__((aligned(1024))) char smem[8 * G::BYTES];
-    __shared__ __attribute__((aligned(16))) float stat[2][2][2][kTile];   // [set][buffer][L, -D]
+    __shared__ __attribute__((aligned(1024))) char smem[SETS * 4 * G::BYTES];
+    __shared__ __attribute__((aligned(16))) float stat[SETS][2][2][kTile];   // [set][buffer][L, -D]
     int blk, pair;
-    locate(blockIdx.x, blocks, a.batch * a.kv_heads, false, blk, pair);
+    locate(blockIdx.x, blocks, a.batch * a.kv_heads, 1, false, blk, pair);
     const int b = pair / a.kv_heads, hk = pair % a.kv_heads, group = a.heads / a.kv_heads;
     const Seq sq = sequence(a, b);
     const int j0 = blk * kRows;
     if (j0 >= sq.k_rows) return;
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % kWaves, set = wave8 / kWaves;
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % kWaves, set = SETS > 1 ? wave8 / kWaves : 0;
     const int w0 = j0 + 32 * wave, j = w0 + l32;   // the wavefront's first key, the lane's key
     const int off = sq.nk - sq.nq;
 
@@ -561,10 +720,10 @@ __global__ __launch_bounds__(2 * 64 * kWaves, 2) void attn_dkv_kernel(AttnArgs a
     // buffers of turn r
     auto qt = [&](int r) { return smem + (4 * set + (r & 1)) * G::BYTES; };
     auto gt = [&](int r) { return smem + (4 * set + 2 + (r & 1)) * G::BYTES; };
-    // step n: query tile n % tiles of the group's head n / tiles; turn r of a set is step 2 r + set
-    const int steps = tiles * group, turns = (steps + 1) / 2;
+    // step n: query tile n % tiles of the group's head n / tiles; turn r of a set is step SETS r + set
+    const int steps = tiles * group, turns = (steps + SETS - 1) / SETS;
     auto fill = [&](int r) {
-        const int n = 2 * r + set;
+        const int n = SETS * r + set;
         if (n >= steps) return;
         const int hq = hk * group + n / tiles, first = (first_t + n % tiles) * kTile;
         cq.tile(qt(r), rows_of(a.q, b, sq.q0, hq), first, sq.nq, a.head_dim);
@@ -586,7 +745,7 @@ __global__ __launch_bounds__(2 * 64 * kWaves, 2) void attn_dkv_kernel(AttnArgs a
     for (int r = 0; r < turns; ++r) {
         tile_barrier();
         fill(r + 1);
-        const int n = 2 * r + set;
+        const int n = SETS * r + set;
         if (n >= steps) continue;
         const int t = first_t + n % tiles;
         if (t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
@@ -638,34 +797,38 @@ __global__ __launch_bounds__(2 * 64 * kWaves, 2) void attn_dkv_kernel(AttnArgs a
             }
         }
     }
-    // set 1's dK and set 0's dV cross over through LDS, and each set stores the sum it then has
-    static_assert(2 * kWaves * DB * 16 * 256 <= sizeof smem, "the accumulators do not fit the tiles' LDS");
-    tile_barrier();
-    float* mine = (float*)smem + (set * kWaves + wave) * DB * 1024 + lane * 4;
-    float* theirs = (float*)smem + ((1 - set) * kWaves + wave) * DB * 1024 + lane * 4;
+    if constexpr (SETS > 1) {
+        // set 1's dK and set 0's dV cross over through LDS, and each set stores the sum it then has
+        static_assert(2 * kWaves * DB * 16 * 256 <= sizeof smem, "the accumulators do not fit the tiles' LDS");
+        tile_barrier();
+        float* mine = (float*)smem + (set * kWaves + wave) * DB * 1024 + lane * 4;
+        float* theirs = (float*)smem + ((1 - set) * kWaves + wave) * DB * 1024 + lane * 4;
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            f32x4 x;
+            for (int g = 0; g < 4; ++g) {
+                f32x4 x;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = set ? dk[d][4 * g + e] : dv[d][4 * g + e];
-            *(f32x4*)(mine + (d * 4 + g) * 256) = x;
-        }
-    __syncthreads();
+                for (int e = 0; e < 4; ++e) x[e] = set ? dk[d][4 * g + e] : dv[d][4 * g + e];
+                *(f32x4*)(mine + (d * 4 + g) * 256) = x;
+            }
+        __syncthreads();
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const f32x4 x = *(const f32x4*)(theirs + (d * 4 + g) * 256);
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 x = *(const f32x4*)(theirs + (d * 4 + g) * 256);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (set) dv[d][4 * g + e] += x[e];
-                else dk[d][4 * g + e] += x[e];
-        }
+                for (int e = 0; e < 4; ++e)
+                    if (set) dv[d][4 * g + e] += x[e];
+                    else dk[d][4 * g + e] += x[e];
+            }
+    }
     if (j >= sq.k_rows) return;
-    if (set) store_t<T, DB>(dv, 1.f, rows_of(a.dv, b, sq.k0, hk) + (int64_t)j * a.dv.token, a.head_dim);
-    else store_t<T, DB>(dk, a.scale, rows_of(a.dk, b, sq.k0, hk) + (int64_t)j * a.dk.token, a.head_dim);
+    if (SETS == 1 || set == 0)
+        store_t<T, DB>(dk, a.scale, rows_of(a.dk, b, sq.k0, hk) + (int64_t)j * a.dk.token, a.head_dim);
+    if (SETS == 1 || set == 1)
+        store_t<T, DB>(dv, 1.f, rows_of(a.dv, b, sq.k0, hk) + (int64_t)j * a.dv.token, a.head_dim);
 }
 
 // ------------------------------------------------------------------ host ----
@@ -688,7 +851,7 @@ opt_status check_attention(const opt_attention_desc* a) {
         if (!train_aligned(p, 4)) return fail(OPT_EINVAL, "an offset or length array is not aligned to 4 bytes");
     if (a->q_start && (a->q_tokens < 0 || a->k_tokens < 0)) return fail(OPT_EINVAL, "negative q_tokens or k_tokens");
     const int64_t longest = a->q_len > a->k_len ? a->q_len : a->k_len;
-    if ((longest / kRows + 1) * a->batch * a->heads > INT32_MAX) return fail(OPT_EUNSUPPORTED, "too many row blocks");
+    if ((longest / kJoinRows + 1) * a->batch * a->heads > INT32_MAX) return fail(OPT_EUNSUPPORTED, "too many row blocks");
     return OPT_OK;
 }
 
@@ -727,17 +890,53 @@ AttnArgs attn_args(const opt_attention_desc* a) {
 }
 
 int row_blocks(int len) { return (len + kRows - 1) / kRows; }
+int64_t query_blocks(const AttnArgs& x) { return (int64_t)row_blocks(x.q_len) * x.batch * x.heads; }
+
+// Key splits of the forward and dQ kernels: enough for one workgroup on each
+// of the 256 CUs, of at least eight tiles each, so that the partial sums stay
+// below the keys and values read.
+int key_splits(const AttnArgs& x) {
+    const int64_t wgs = query_blocks(x);
+    if (wgs == 0) return 1;
+    const int64_t most = x.window && x.window + kRows < x.k_len ? x.window + kRows : x.k_len;
+    const int64_t tiles = (most + kTile - 1) / kTile;
+    int64_t s = 256 / wgs;
+    if (s > tiles / 8) s = tiles / 8;
+    return (int)(s < 1 ? 1 : s > 32 ? 32 : s);
+}
+
+// Two sets of wavefronts a workgroup where the launch has too few for two
+// workgroups a CU.
+bool two_sets(int64_t wgs) { return wgs < 512; }
 
 enum Kind { FORWARD, DQ, DKV };
 template <class T, int DB>
-void launch(Kind kind, const AttnArgs& x, hipStream_t s) {
+void launch(Kind kind, AttnArgs x, hipStream_t s) {
     const int blocks = row_blocks(kind == DKV ? x.k_len : x.q_len);
-    const int64_t grid = (int64_t)blocks * x.batch * (kind == DKV ? x.kv_heads : x.heads);
+    int64_t grid = (int64_t)blocks * x.batch * (kind == DKV ? x.kv_heads : x.heads);
     if (grid == 0) return;
-    const dim3 g((uint32_t)grid), n(64 * kWaves);
-    if (kind == FORWARD) attn_forward_kernel<T, DB><<<g, n, 0, s>>>(x, blocks);
-    else if (kind == DQ) attn_dq_kernel<T, DB><<<g, n, 0, s>>>(x, blocks);
-    else attn_dkv_kernel<T, DB><<<g, dim3(2 * 64 * kWaves), 0, s>>>(x, blocks);
+    const dim3 one(64 * kWaves), two(2 * 64 * kWaves);
+    if (kind == DKV) {
+        const dim3 g((uint32_t)grid);
+        if (x.causal || two_sets(grid)) attn_dkv_kernel<T, DB, 2><<<g, two, 0, s>>>(x, blocks);
+        else attn_dkv_kernel<T, DB, 1><<<g, one, 0, s>>>(x, blocks);
+        return;
+    }
+    const dim3 g((uint32_t)(grid * x.splits));
+    const bool sets = two_sets(grid * x.splits);
+    if (kind == FORWARD) {
+        if (sets) attn_forward_kernel<T, DB, 2><<<g, two, 0, s>>>(x, blocks);
+        else attn_forward_kernel<T, DB, 1><<<g, one, 0, s>>>(x, blocks);
+    } else {
+        if (sets) attn_dq_kernel<T, DB, 2><<<g, two, 0, s>>>(x, blocks);
+        else attn_dq_kernel<T, DB, 1><<<g, one, 0, s>>>(x, blocks);
+    }
+    if (x.splits > 1) {
+        const int jb = (x.q_len + kJoinRows - 1) / kJoinRows;
+        const dim3 j((uint32_t)((int64_t)jb * x.batch * x.heads));
+        if (kind == FORWARD) attn_join_kernel<T, true><<<j, kJoinThreads, 0, s>>>(x, 32 * DB, jb);
+        else attn_join_kernel<T, false><<<j, kJoinThreads, 0, s>>>(x, 32 * DB, jb);
+    }
 }
 template <class T>
 void launch(Kind kind, const AttnArgs& x, hipStream_t s) {
@@ -750,10 +949,31 @@ void launch(Kind kind, int32_t dtype, const AttnArgs& x, hipStream_t s) {
     dtype == OPT_BF16 ? launch<__bf16>(kind, x, s) : launch<_Float16>(kind, x, s);
 }
 
-uint64_t attn_bytes(const opt_attention_desc* a, bool backward) {
-    if (!backward) return 0;
-    const AttnArgs x = attn_args(a);
-    return ((uint64_t)x.q_tokens * (uint64_t)x.heads * 4 + 255) / 256 * 256;
+// The workspace: D (backward), then the key splits' partial results.
+struct Space {
+    uint64_t delta, part, part_m, part_l, bytes;
+    int splits;
+};
+Space space_of(const AttnArgs& x, bool backward) {
+    const auto up = [](uint64_t n) { return (n + 255) / 256 * 256; };
+    const uint64_t rows = (uint64_t)x.q_tokens * (uint64_t)x.heads, width = (uint64_t)(x.head_dim + 31) / 32 * 32;
+    Space s = {};
+    s.splits = rows ? key_splits(x) : 1;
+    if (backward) s.bytes += up(rows * 4);
+    if (s.splits > 1) {
+        s.part = s.bytes, s.bytes += up(s.splits * rows * width * 4);
+        if (!backward) {
+            s.part_m = s.bytes, s.bytes += up(s.splits * rows * 4);
+            s.part_l = s.bytes, s.bytes += up(s.splits * rows * 4);
+        }
+    }
+    return s;
+}
+void use_space(AttnArgs& x, const Space& s, void* ws) {
+    char* p = (char*)ws;
+    x.splits = s.splits;
+    x.delta = (float*)(p + s.delta);
+    x.part = (float*)(p + s.part), x.part_m = (float*)(p + s.part_m), x.part_l = (float*)(p + s.part_l);
 }
 
 opt_status check_workspace(const void* ws, uint64_t bytes, uint64_t need) {
@@ -773,7 +993,7 @@ extern "C" {
 opt_status opt_attention_workspace_size(const opt_attention_desc* a, int32_t backward, uint64_t* bytes) {
     if (!bytes) return fail(OPT_EINVAL, "bytes is NULL");
     if (opt_status st = check_attention(a)) return st;
-    *bytes = attn_bytes(a, backward != 0);
+    *bytes = space_of(attn_args(a), backward != 0).bytes;
     return OPT_OK;
 }
 
@@ -789,10 +1009,12 @@ opt_status opt_attention_forward(const opt_attention_desc* a, const opt_attentio
     if (opt_status st = tensor(a, v, "v", no_k || no_q, x.v)) return st;
     if (opt_status st = output(a, out, "out", no_q, a->heads, a->q_len, x.o)) return st;
     if (!no_q && (!lse || !train_aligned(lse, 4))) return fail(OPT_EINVAL, "lse is NULL or not aligned to 4 bytes");
-    if (opt_status st = check_workspace(workspace, workspace_bytes, attn_bytes(a, false))) return st;
+    const Space space = space_of(x, false);
+    if (opt_status st = check_workspace(workspace, workspace_bytes, space.bytes)) return st;
     if (no_q) return OPT_OK;
     if (opt_status st = train_pending()) return st;
     x.lse = lse;
+    use_space(x, space, workspace);
     launch(FORWARD, a->dtype, x, (hipStream_t)stream);
     return train_launched("attention");
 }
@@ -816,11 +1038,12 @@ opt_status opt_attention_backward(const opt_attention_desc* a, const opt_attenti
     if (opt_status st = output(a, dq, "dq", no_q, a->heads, a->q_len, x.dq)) return st;
     if (opt_status st = output(a, dk, "dk", no_k, a->kv_heads, a->k_len, x.dk)) return st;
     if (opt_status st = output(a, dv, "dv", no_k, a->kv_heads, a->k_len, x.dv)) return st;
-    if (opt_status st = check_workspace(workspace, workspace_bytes, attn_bytes(a, true))) return st;
+    const Space space = space_of(x, true);
+    if (opt_status st = check_workspace(workspace, workspace_bytes, space.bytes)) return st;
     if (no_q && no_k) return OPT_OK;
     if (opt_status st = train_pending()) return st;
     x.lse = (float*)lse;
-    x.delta = (float*)workspace;
+    use_space(x, space, workspace);
     if (!no_q) launch(DQ, a->dtype, x, (hipStream_t)stream);
     if (!no_k) launch(DKV, a->dtype, x, (hipStream_t)stream);
     return train_launched("attention backward");

@@ -143,6 +143,38 @@ def test_longer_than_one_workgroup():
     dense(1, 1100, 1100, 2, 1, 128, causal=True, seed=5)
 
 
+@pytest.mark.parametrize("nq,nk,causal,window", [(1, 3000, False, 0), (1, 1025, True, 0), (100, 5000, True, 0), (129, 4100, True, 1500),
+                                                (7, 9000, False, 0), (600, 2000, False, 0), (40, 2000, True, 30)])
+@pytest.mark.parametrize("d", [64, 128, 72])
+def test_few_queries_on_a_long_context(nq, nk, causal, window, d):
+    """The keys of these are split over workgroups and joined."""
+    dense(1, nq, nk, 2, 1, d, causal=causal, window=window, seed=nq + d)
+
+
+@pytest.mark.parametrize("batch,heads,kv,causal", [(16, 16, 8, False), (32, 32, 32, True), (3, 5, 5, True)])
+def test_many_workgroups(batch, heads, kv, causal):
+    """Launches of many even and uneven workgroups, and a head count that does not spread over eight."""
+    dense(batch, 200, 200, heads, kv, 64, causal=causal, seed=batch)
+
+
+def test_packed_sequences_on_long_contexts():
+    torch = _torch()
+    print("attention packed long", flush=True)
+    nq, nk = [3, 0, 90, 1], [4000, 50, 100, 2000]
+    mk = lambda *s: torch.randn(*s, device="cuda").bfloat16()  # noqa: E731
+    q, k, v, dout = mk(sum(nq), 2, 128), mk(sum(nk), 1, 128), mk(sum(nk), 1, 128), mk(sum(nq), 2, 128)
+    st = lambda n: torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device="cuda")  # noqa: E731
+    got = run(q, k, v, dout, causal=True, q_start=st(nq), k_start=st(nk), max_q=max(nq), max_k=max(nk))
+    got = {n: np64(t) for n, t in got.items()}
+    a = c = 0
+    for m, n in zip(nq, nk):
+        one = {x: got[x][a:a + m] for x in ("out", "dq")} | {x: got[x][c:c + n] for x in ("dk", "dv")}
+        one["lse"] = got["lse"][:, a:a + m]
+        check_sequence(np64(q[a:a + m]), np64(k[c:c + n]), np64(v[c:c + n]), np64(dout[a:a + m]), one, 128 ** -0.5,
+                       T.visible(m, n, True), U["bf16"])
+        a, c = a + m, c + n
+
+
 def test_rising_scores_move_the_running_maximum():
     """Keys whose scores grow along the sequence raise the maximum in every tile."""
     torch = _torch()
