@@ -11,8 +11,6 @@ raise before anything is launched.
 
 from __future__ import annotations
 
-import ctypes as C
-import math
 from dataclasses import dataclass
 from typing import NamedTuple, Optional
 
@@ -23,6 +21,7 @@ from . import native
 __all__ = ["Rng", "attention_forward", "attention_backward", "dropout", "dropout_backward", "layer_norm_forward",
            "layer_norm_backward", "PolicyForward", "policy_loss_forward", "policy_loss_backward", "policy_loss_step"]
 
+_HALF = {torch.bfloat16: native.OPT_BF16, torch.float16: native.OPT_F16}
 _DTYPE = {torch.float32: native.OPT_F32, torch.bfloat16: native.OPT_BF16, torch.float16: native.OPT_F16}
 
 
@@ -44,12 +43,13 @@ class Rng:
 
 
 def _stream(dev, stream):
-    """(handle, stream object when it is not the current one)."""
+    """(handle, stream object when it is not the current one). The raw handle
+    of the current stream: the Stream object around it costs 2 us a call."""
     if dev.type != "cuda":
         raise ValueError("tensors must live on a HIP device")
-    cur = torch.cuda.current_stream(dev)
-    if stream is None or stream.cuda_stream == cur.cuda_stream:
-        return cur.cuda_stream, None
+    cur = torch._C._cuda_getCurrentRawStream(dev.index)
+    if stream is None or stream.cuda_stream == cur:
+        return cur, None
     return stream.cuda_stream, stream
 
 
@@ -74,7 +74,8 @@ def _is(t, name, device, dtype, shape=None):
 
 
 def _vector(t, name, device, n, dtype=torch.float32):
-    _is(t, name, device, dtype, (n,))
+    if not (t.__class__ is torch.Tensor and t.dtype == dtype and t.device == device and t.shape == (n,)):
+        _is(t, name, device, dtype, (n,))
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -90,12 +91,10 @@ def _code(t, name):
 # -------------------------------------------------------------- attention ----
 
 
-def _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens):
-    packed = q_start is not None
-    if packed != (k_start is not None):
-        raise ValueError("q_start and k_start come together")
-    want = 3 if packed else 4
+def _refuse_qkv(q, k, v, packed):
+    """Why q, k, v do not go together."""
     dev, dt = q.device, q.dtype
+    want = 3 if packed else 4
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         _is(t, name, dev, dt)
         if t.dim() != want:
@@ -103,36 +102,42 @@ def _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens
                                                                   "(batch, tokens, heads, dim)"))
     if k.shape != v.shape:
         raise ValueError("k and v must have the same shape")
-    if dt not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"q has dtype {dt}, expected torch.bfloat16 or torch.float16")
-    heads, dim = q.shape[-2:]
-    kv_heads = k.shape[-2]
-    if k.shape[-1] != dim:
+    if q.shape[-1] != k.shape[-1]:
         raise ValueError("q and k differ in head_dim")
-    a = native.opt_attention_desc()
+    if not packed and k.shape[0] != q.shape[0]:
+        raise ValueError("q and k differ in batch")
+    raise ValueError(f"q has dtype {dt}, expected torch.bfloat16 or torch.float16")
+
+
+def _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens):
+    packed = q_start is not None
+    if packed != (k_start is not None):
+        raise ValueError("q_start and k_start come together")
+    dev, dt, qs, ks = q.device, q.dtype, q.shape, k.shape
+    code = _HALF.get(dt)
+    if not (code is not None and k.dtype == dt == v.dtype and k.device == dev == v.device and ks == v.shape
+            and len(qs) == len(ks) == (3 if packed else 4) and qs[-1] == ks[-1] and (packed or qs[0] == ks[0])):
+        _refuse_qkv(q, k, v, packed)
     if packed:
         if q_lens is not None or k_lens is not None:
             raise ValueError("packed sequences (q_start) have no q_lens or k_lens")
         if max_q is None or max_k is None:
             raise ValueError("packed sequences need max_q and max_k")
+        nq, heads, dim = qs
         batch = q_start.numel() - 1
-        a.q_start = _vector(q_start, "q_start", dev, batch + 1, torch.int32)
-        a.k_start = _vector(k_start, "k_start", dev, batch + 1, torch.int32)
-        a.q_len, a.k_len = max_q, max_k
-        a.q_tokens, a.k_tokens = q.shape[0], k.shape[0]
-    else:
-        batch = q.shape[0]
-        if k.shape[0] != batch:
-            raise ValueError("q and k differ in batch")
-        a.q_len, a.k_len = q.shape[1], k.shape[1]
-        if q_lens is not None:
-            a.q_lens = _vector(q_lens, "q_lens", dev, batch, torch.int32)
-        if k_lens is not None:
-            a.k_lens = _vector(k_lens, "k_lens", dev, batch, torch.int32)
-    a.dtype, a.batch, a.heads, a.kv_heads, a.head_dim = _DTYPE[dt], batch, heads, kv_heads, dim
-    a.causal, a.window = bool(causal), window
-    a.scale = 1.0 / math.sqrt(dim) if scale is None else scale
-    return a, dev
+        a = native.opt_attention_desc(code, batch, heads, ks[1], dim, max_q, max_k, bool(causal), window,
+                                      dim ** -0.5 if scale is None else scale,
+                                      _vector(q_start, "q_start", dev, batch + 1, torch.int32),
+                                      _vector(k_start, "k_start", dev, batch + 1, torch.int32), nq, ks[0])
+        return a, dev, (heads, nq)
+    batch, nq, heads, dim = qs
+    a = native.opt_attention_desc(code, batch, heads, ks[2], dim, nq, ks[1], bool(causal), window,
+                                  dim ** -0.5 if scale is None else scale)
+    if q_lens is not None:
+        a.q_lens = _vector(q_lens, "q_lens", dev, batch, torch.int32)
+    if k_lens is not None:
+        a.k_lens = _vector(k_lens, "k_lens", dev, batch, torch.int32)
+    return a, dev, (heads, batch * nq)
 
 
 def _bhtd(t, name):
@@ -146,14 +151,13 @@ def _bhtd(t, name):
 
 def _out(given, name, like, dev):
     if given is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=dev)
+        return like.new_empty(like.shape)
     _is(given, name, dev, like.dtype, like.shape)
     return given
 
 
-def _workspace(size, desc, backward, dev):
-    n = size(desc, backward)
-    return (torch.empty(n, dtype=torch.uint8, device=dev) if n else None), n
+def _bytes(like, n):
+    return like.new_empty(n, dtype=torch.uint8) if n else None
 
 
 def attention_forward(q, k, v, *, causal=False, window=0, scale=None, q_start=None, k_start=None, max_q=None,
@@ -164,15 +168,16 @@ def attention_forward(q, k, v, *, causal=False, window=0, scale=None, q_start=No
     int32 offsets of batch + 1, max_q and max_k the longest lengths. Padded
     batches: q_lens, k_lens int32 lengths. lse is fp32, (heads, all query
     tokens). scale defaults to dim^-1/2."""
-    a, dev = _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens)
+    a, dev, per_row = _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens)
     st, other = _stream(dev, stream)
     o = _out(out, "out", q, dev)
-    lse = torch.empty((q.shape[-2], q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]), dtype=torch.float32,
-                      device=dev)
-    ws, n = _workspace(native.opt_attention_workspace_size, a, 0, dev)
+    lse = q.new_empty(per_row, dtype=torch.float32)
+    n = native.opt_attention_workspace_size(a, 0)
+    ws = _bytes(q, n)
     native.opt_attention_forward(a, _bhtd(q, "q"), _bhtd(k, "k"), _bhtd(v, "v"), _bhtd(o, "out"), lse.data_ptr(),
                                  ws.data_ptr() if n else 0, n, st)
-    _used(other, o if out is None else None, lse, ws)
+    if other is not None:
+        _used(other, o if out is None else None, lse, ws)
     return o, lse
 
 
@@ -181,22 +186,25 @@ def attention_backward(dout, q, k, v, out, lse, *, causal=False, window=0, scale
     """(dq, dk, dv) from the output's gradient and what attention_forward took
     and returned. dq, dk, dv may be given, for instance as views of one
     projection's gradient."""
-    a, dev = _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens)
-    _is(dout, "dout", dev, q.dtype, q.shape)
-    _is(out, "out", dev, q.dtype, q.shape)
-    _is(lse, "lse", dev, torch.float32, (q.shape[-2], q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]))
+    a, dev, per_row = _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens)
+    for t, name in ((dout, "dout"), (out, "out")):
+        if not (t.dtype == q.dtype and t.device == dev and t.shape == q.shape):
+            _is(t, name, dev, q.dtype, q.shape)
+    _is(lse, "lse", dev, torch.float32, per_row)
     if not lse.is_contiguous():
         raise ValueError("lse must be contiguous")
     if dout.stride(-1) != 1:   # an expanded gradient has stride 0
         dout = dout.contiguous()
     st, other = _stream(dev, stream)
     gq, gk, gv = _out(dq, "dq", q, dev), _out(dk, "dk", k, dev), _out(dv, "dv", v, dev)
-    ws, n = _workspace(native.opt_attention_workspace_size, a, 1, dev)
+    n = native.opt_attention_workspace_size(a, 1)
+    ws = _bytes(q, n)
     native.opt_attention_backward(a, _bhtd(dout, "dout"), _bhtd(q, "q"), _bhtd(k, "k"), _bhtd(v, "v"),
                                   _bhtd(out, "out"), lse.data_ptr(), _bhtd(gq, "dq"), _bhtd(gk, "dk"),
                                   _bhtd(gv, "dv"), ws.data_ptr() if n else 0, n, st)
-    _used(other, dout, None if dq is not None else gq, None if dk is not None else gk,
-          None if dv is not None else gv, ws)
+    if other is not None:
+        _used(other, dout, None if dq is not None else gq, None if dk is not None else gk,
+              None if dv is not None else gv, ws)
     return gq, gk, gv
 
 
@@ -206,24 +214,28 @@ def attention_backward(dout, q, k, v, out, lse, *, causal=False, window=0, scale
 def _rows(t, name):
     """(data pointer, row stride) of a tensor as rows x cols over its last
     axis; the leading axes must collapse to one stride."""
-    if t.dim() == 2:
+    shape = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1] if shape else 1
+    if len(shape) == 2:
         s0, s1 = t.stride()
-        if s1 != 1 and t.shape[1] > 1:
+        if s1 != 1 and shape[1] > 1:
             raise ValueError(f"the last axis of {name} must be contiguous")
-        return t.data_ptr(), s0 if t.shape[0] > 1 else max(s0, t.shape[1])
-    if t.dim() < 2 or t.is_contiguous():
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr(), t.shape[-1] if t.dim() else 1
+        return t.data_ptr(), s0 if shape[0] > 1 else max(s0, shape[1])
+    if len(shape) < 2:
+        raise ValueError(f"{name} must be contiguous")
     try:
-        v = t.view(-1, t.shape[-1])
+        v = t.view(-1, shape[-1])
     except RuntimeError:
         raise ValueError(f"the leading axes of {name} must collapse to one stride") from None
     return _rows(v, name)
 
 
 def _size(t):
-    cols = t.shape[-1] if t.dim() else 1
+    shape = t.shape
+    if len(shape) == 2:
+        return shape[0], shape[1]
+    cols = shape[-1] if shape else 1
     return (t.numel() // cols if cols else 0), cols
 
 
@@ -248,7 +260,8 @@ def dropout(x, p, rng, *, residual=None, out=None, stream=None):
         rp, ldr = _rows(residual, "residual")
     st, other = _stream(dev, stream)
     native.opt_dropout(rows, cols, dt, xp, ldx, rp, ldr, yp, ldy, p, bits, st)
-    _used(other, y if out is None else None)
+    if other is not None:
+        _used(other, y if out is None else None)
     return y
 
 
@@ -277,15 +290,16 @@ def layer_norm_forward(x, weight, bias=None, *, eps=1e-5, residual=None, p=0.0, 
             hdt = _code(residual, "residual")
             _is(residual, "residual", dev, residual.dtype, x.shape)
             rp, ldr = _rows(residual, "residual")
-        h = torch.empty(x.shape, dtype=x.dtype if residual is None else residual.dtype, device=dev)
-        hp, ldh = _rows(h, "h")
-    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev)
-    sp = stats.data_ptr()
+        h = (x if residual is None else residual).new_empty(x.shape)
+        hp, ldh = h.data_ptr(), cols
+    lead = x.shape[:-1]
+    mean, rstd = weight.new_empty(lead), weight.new_empty(lead)
     st, other = _stream(dev, stream)
-    native.opt_layer_norm_forward(rows, cols, dt, xp, ldx, hdt, rp, ldr, wp, bp, eps, p, bits, yp, ldy, hp,
-                                  ldh, sp, sp + 4 * rows, st)
-    _used(other, y if out is None else None, h if hp else None, stats)
-    return y, h, stats[0], stats[1]
+    native.opt_layer_norm_forward(rows, cols, dt, xp, ldx, hdt, rp, ldr, wp, bp, eps, p, bits, yp, ldy, hp, ldh,
+                                  mean.data_ptr(), rstd.data_ptr(), st)
+    if other is not None:
+        _used(other, y if out is None else None, h if hp else None, mean, rstd)
+    return y, h, mean, rstd
 
 
 def layer_norm_backward(dy, h, weight, mean, rstd, *, dh=None, p=0.0, rng=None, residual_grad=True, stream=None):
@@ -295,38 +309,40 @@ def layer_norm_backward(dy, h, weight, mean, rstd, *, dh=None, p=0.0, rng=None, 
     same type it is dx itself. residual_grad=False: dres is None."""
     dev, dt, bits = dy.device, _code(dy, "dy"), _p_rng(p, rng)
     rows, cols = _size(dy)
-    hdt = _code(h, "h")
-    _is(h, "h", dev, h.dtype, dy.shape)
+    hdt, shape = _code(h, "h"), dy.shape
+    if not (h.device == dev and h.shape == shape):
+        _is(h, "h", dev, h.dtype, shape)
     dyp, lddy = _rows(dy, "dy")
     hp, ldh = _rows(h, "h")
     wp = _vector(weight, "weight", dev, cols)
+    lead = shape[:-1]
     for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _is(t, name, dev, torch.float32, dy.shape[:-1])
+        if not (t.dtype == torch.float32 and t.device == dev and t.shape == lead):
+            _is(t, name, dev, torch.float32, lead)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
     dhp, lddh = 0, 0
     if dh is not None:
-        _is(dh, "dh", dev, h.dtype, dy.shape)
+        _is(dh, "dh", dev, h.dtype, shape)
         dhp, lddh = _rows(dh, "dh")
-    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dev)
+    dx = dy.new_empty(shape)
     dres, drp, lddr = None, 0, 0
     if residual_grad:
         if p == 0 and h.dtype == dy.dtype:
             dres = dx
         else:
-            dres = torch.empty(dy.shape, dtype=h.dtype, device=dev)
-            drp, lddr = _rows(dres, "dres")
+            dres = h.new_empty(shape)
+            drp, lddr = dres.data_ptr(), cols
     n = native.opt_layer_norm_workspace_size(rows, cols)
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    dwb = torch.empty((2, cols), dtype=torch.float32, device=dev)
-    dp = dwb.data_ptr()
+    ws = _bytes(dy, n)
+    dw, db = weight.new_empty(cols), weight.new_empty(cols)
     st, other = _stream(dev, stream)
-    dxp, lddx = _rows(dx, "dx")
     native.opt_layer_norm_backward(rows, cols, dt, dyp, lddy, hdt, hp, ldh, dhp, lddh, wp, mean.data_ptr(),
-                                   rstd.data_ptr(), p, bits, dxp, lddx, drp, lddr, dp, dp + 4 * cols,
-                                   ws.data_ptr(), n, st)
-    _used(other, dx, dres, dwb, ws)
-    return dx, dres, dwb[0], dwb[1]
+                                   rstd.data_ptr(), p, bits, dx.data_ptr(), cols, drp, lddr, dw.data_ptr(),
+                                   db.data_ptr(), ws.data_ptr() if n else 0, n, st)
+    if other is not None:
+        _used(other, dx, dres, dw, db, ws)
+    return dx, dres, dw, db
 
 
 # ------------------------------------------------------------ policy loss ----
@@ -372,14 +388,14 @@ def policy_loss_forward(logits, target, old_logp, advantage, weight, *, ref_logp
     a, dev, lp, tp = _policy(logits, target, clip_low, clip_high, kl_coef, logit_scale)
     rows = _policy_rows(tp, dev, a.rows, old_logp, ref_logp, advantage, weight, kl_coef)
     st, other = _stream(dev, stream)
-    per = torch.empty((3, a.rows), dtype=torch.float32, device=dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
     n = native.opt_policy_loss_workspace_size(a)
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    native.opt_policy_loss_forward(a, lp, rows, loss.data_ptr(), per[0].data_ptr(), per[1].data_ptr(),
-                                   per[2].data_ptr(), ws.data_ptr(), n, st)
-    _used(other, per, loss, ws)
-    return PolicyForward(loss, per[0], per[1], per[2])
+    ws = _bytes(logits, n)
+    loss, logp, lse, slope = (weight.new_empty(s) for s in ((), a.rows, a.rows, a.rows))
+    native.opt_policy_loss_forward(a, lp, rows, loss.data_ptr(), logp.data_ptr(), lse.data_ptr(), slope.data_ptr(),
+                                   ws.data_ptr() if n else 0, n, st)
+    if other is not None:
+        _used(other, loss, logp, lse, slope, ws)
+    return PolicyForward(loss, logp, lse, slope)
 
 
 def policy_loss_backward(logits, target, fwd, *, grad=None, logit_scale=1.0, out=None, stream=None):
@@ -395,7 +411,8 @@ def policy_loss_backward(logits, target, fwd, *, grad=None, logit_scale=1.0, out
         gp = grad.data_ptr()
     st, other = _stream(dev, stream)
     native.opt_policy_loss_backward(a, lp, tp, ep, sp, gp, dp, ldd, st)
-    _used(other, d if out is None else None)
+    if other is not None:
+        _used(other, d if out is None else None)
     return d
 
 
@@ -409,10 +426,11 @@ def policy_loss_step(logits, target, old_logp, advantage, weight, *, ref_logp=No
     d = _out(out, "out", logits, dev)
     dp, ldd = _rows(d, "out")
     st, other = _stream(dev, stream)
-    logp = torch.empty(a.rows, dtype=torch.float32, device=dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
+    logp, loss = weight.new_empty(a.rows), weight.new_empty(())
     n = native.opt_policy_loss_workspace_size(a)
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    native.opt_policy_loss_step(a, lp, rows, grad, loss.data_ptr(), logp.data_ptr(), dp, ldd, ws.data_ptr(), n, st)
-    _used(other, d if out is None else None, logp, loss, ws)
+    ws = _bytes(logits, n)
+    native.opt_policy_loss_step(a, lp, rows, grad, loss.data_ptr(), logp.data_ptr(), dp, ldd,
+                                ws.data_ptr() if n else 0, n, st)
+    if other is not None:
+        _used(other, d if out is None else None, logp, loss, ws)
     return loss, logp, d
