@@ -6,9 +6,10 @@
 //              dx = keep scale g;  dres = g;  dw = sum dy xh;  db = sum dy
 //
 // Every tensor is read once and written once. A row of the norm lives in the
-// registers of one wavefront (up to 1024 columns) or of a workgroup of 256 to
-// 1024 threads (up to 16384), eight or sixteen columns a thread, so mean and
-// variance are two passes over registers: the variance is the sum of squares about the
+// registers of 16, 32 or 64 threads (up to 512 columns) or of a workgroup of
+// 128 to 1024 threads, eight columns a thread (sixteen past 8192 columns: more a
+// thread leaves the backward pass short of registers), so mean and variance
+// are two passes over registers: the variance is the sum of squares about the
 // mean, with no cancellation. The weight's and bias's gradients are column
 // sums: a thread keeps its columns over all rows of its workgroup, each
 // workgroup writes one partial row, and a second kernel adds the partial rows
@@ -102,16 +103,16 @@ void dropout_launch(int64_t rows, int64_t cols, const void* x, int64_t ldx, cons
 
 // ------------------------------------------------------------ layer norm ----
 
-constexpr int kNormMaxBlocks = 1024;   // of the backward pass: partial rows of the column sums
-constexpr int norm_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+constexpr int norm_threads(int tpr) { return tpr <= 64 ? 256 : tpr; }   // of a workgroup
 
-// Sum of one value per thread over the TPR threads of a row: a wavefront or
-// the whole workgroup. The callers rotate `slot`, so one barrier per sum is
-// enough.
+// Sum of one value per thread over the TPR threads of a row: a part of a
+// wavefront, or the whole workgroup. The callers rotate `slot`, so one barrier
+// per sum is enough.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float x, float (*part)[16], int slot) {
-    x = wave_sum(x);
-    if constexpr (TPR == 64) return x;
+#pragma unroll
+    for (int m = (TPR < 64 ? TPR : 64) / 2; m; m >>= 1) x += __shfl_xor(x, m);
+    if constexpr (TPR <= 64) return x;
     if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = x;
     __syncthreads();
     float s = 0.f;
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(norm_threads(TPR)) void norm_forward_kernel(
     __shared__ float part[2][16];
     const int t = threadIdx.x % TPR;
     const uint32_t row = blockIdx.x * (norm_threads(TPR) / TPR) + threadIdx.x / TPR;
-    if (row >= rows) return;   // whole wavefronts; where a row takes the workgroup, none is past the rows
+    if (row >= rows) return;   // all threads of a row; where it takes the workgroup, none is past the rows
     float f[VPT][8];
     int n[VPT];
 #pragma unroll
@@ -214,11 +215,10 @@ __global__ __launch_bounds__(norm_threads(TPR)) void norm_forward_kernel(
     }
 }
 
-// Rows blockIdx.x * R + k, then gridDim.x * R further, with R rows at a time
-// (one per wavefront with TPR = 64). part_w and part_b hold one row of `cols`
+// Rows blockIdx.x * R + k, then gridDim.x * R further, with R rows at a time. part_w and part_b hold one row of `cols`
 // column sums per workgroup.
 template <class T, class H, int TPR, int VPT, bool EIGHTS>
-__global__ __launch_bounds__(norm_threads(TPR)) void norm_backward_kernel(
+__global__ __launch_bounds__(norm_threads(TPR), 4) void norm_backward_kernel(
     uint32_t rows, int cols, const T* dy, int64_t lddy, const H* h, int64_t ldh, const H* dh, int64_t lddh,
     const float* w, const float* mean_in, const float* rstd_in, Drop d, T* dx, int64_t lddx, H* dres, int64_t lddres,
     float* part_w, float* part_b) {
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(norm_threads(TPR)) void norm_backward_kernel(
     // The weight stays in registers over the rows, but for the widest rows,
     // where 128 registers a thread have no room for it and each row reads it
     // again (from L2).
-    constexpr bool KEEP_W = TPR < 1024;
+    constexpr bool KEEP_W = VPT == 1;
     float dw[VPT][8] = {}, db[VPT][8] = {}, wv[KEEP_W ? VPT : 1][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -269,6 +269,7 @@ __global__ __launch_bounds__(norm_threads(TPR)) void norm_backward_kernel(
         slot ^= 2;   // the next row's sums go to the other pair: a slower wavefront may still read this one
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
+            if constexpr (VPT > 1) __builtin_amdgcn_sched_barrier(0);   // one group's values at a time
             if (n[i] == 0) continue;
             const int c = 8 * (t + i * TPR);
             float g[8], q[8];
@@ -285,8 +286,8 @@ __global__ __launch_bounds__(norm_threads(TPR)) void norm_backward_kernel(
             }
         }
     }
-    // one partial row per workgroup: with four wavefronts on different rows
-    // their sums meet in LDS, in wavefront order
+    // one partial row per workgroup: the sums of its R rows' threads meet in
+    // LDS and are added in order
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = 8 * (t + i * TPR);
@@ -310,20 +311,30 @@ __global__ __launch_bounds__(norm_threads(TPR)) void norm_backward_kernel(
     }
 }
 
-// Column sums of the partial rows: 64 columns per workgroup, 16 slices of the
-// rows, added in slice order.
-constexpr int kSumCols = 64, kSumSlices = 16;
+// Column sums of the partial rows: 32 columns per workgroup (a 128-byte line),
+// 32 slices of the rows, eight loads of a slice in flight, added in slice
+// order. For 1024 rows of 2048 columns 4.5 us; 16 columns 6.8, 8 columns 12.5;
+// one load in flight and 16 slices 20.
+constexpr int kSumCols = 32, kSumSlices = 32;
 __global__ __launch_bounds__(kSumCols* kSumSlices) void norm_sum_kernel(int parts, int cols, const float* part_w,
                                                                         const float* part_b, float* dw, float* db) {
     __shared__ float sh[kSumSlices][kSumCols];
     const float* src = blockIdx.y ? part_b : part_w;
     float* dst = blockIdx.y ? db : dw;
-    if (!dst) return;
     const int lane = threadIdx.x % kSumCols, slice = threadIdx.x / kSumCols;
     const int c = blockIdx.x * kSumCols + lane;
     float s = 0.f;
     if (c < cols)
-        for (int r = slice; r < parts; r += kSumSlices) s += gptr(src)[(int64_t)r * cols + c];
+        for (int r0 = slice; r0 < parts; r0 += 8 * kSumSlices) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = r0 + k * kSumSlices;
+                v[k] = r < parts ? gptr(src)[(int64_t)r * cols + c] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += v[k];
+        }
     sh[slice][lane] = s;
     __syncthreads();
     if (slice == 0 && c < cols) {
@@ -333,10 +344,15 @@ __global__ __launch_bounds__(kSumCols* kSumSlices) void norm_sum_kernel(int part
     }
 }
 
+// Workgroups of the backward pass, and partial rows: what the GPU holds at
+// once at 128 registers a thread (1024 threads a CU), so that all run through
+// their rows together.
 int norm_blocks(int64_t rows, int64_t cols) {
-    const int per = cols <= 1024 ? 4 : 1;
-    const int64_t b = (rows + per - 1) / per;
-    return (int)(b < kNormMaxBlocks ? b : kNormMaxBlocks);
+    const int per = cols <= 128 ? 16 : cols <= 256 ? 8 : cols <= 512 ? 4 : 1;
+    int threads = 256;
+    if (cols > 512) threads = cols <= 1024 ? 128 : cols <= 2048 ? 256 : cols <= 4096 ? 512 : 1024;
+    const int64_t b = (rows + per - 1) / per, most = 256 * 1024 / threads;
+    return (int)(b < most ? b : most);
 }
 
 struct NormFwd {
@@ -377,11 +393,13 @@ void run(const NormBwd& a, hipStream_t s) {
 
 template <class T, class H, bool EIGHTS, class A>
 void by_width(const A& a, hipStream_t s) {
-    if (a.cols <= 512) run<T, H, 64, 1, EIGHTS>(a, s);
-    else if (a.cols <= 1024) run<T, H, 64, 2, EIGHTS>(a, s);
+    if (a.cols <= 128) run<T, H, 16, 1, EIGHTS>(a, s);
+    else if (a.cols <= 256) run<T, H, 32, 1, EIGHTS>(a, s);
+    else if (a.cols <= 512) run<T, H, 64, 1, EIGHTS>(a, s);
+    else if (a.cols <= 1024) run<T, H, 128, 1, EIGHTS>(a, s);
     else if (a.cols <= 2048) run<T, H, 256, 1, EIGHTS>(a, s);
-    else if (a.cols <= 4096) run<T, H, 256, 2, EIGHTS>(a, s);
-    else if (a.cols <= 8192) run<T, H, 512, 2, EIGHTS>(a, s);
+    else if (a.cols <= 4096) run<T, H, 512, 1, EIGHTS>(a, s);
+    else if (a.cols <= 8192) run<T, H, 1024, 1, EIGHTS>(a, s);
     else run<T, H, 1024, 2, EIGHTS>(a, s);
 }
 template <class T, class H, class A>

