@@ -61,10 +61,10 @@ struct Tensor {
 struct AttnArgs {
     Tensor q, k, v, o, dout, dq, dk, dv;
     float *lse, *delta;
-    float *part, *part_m, *part_l;   // partial results of key splits (workspace)
+    float *part, *part_v, *part_m, *part_l;   // partial results of splits (workspace)
     const int32_t *q_start, *k_start, *q_lens, *k_lens;
     int64_t q_tokens, k_tokens;   // rows of lse and delta; packed: the token axes
-    int32_t batch, heads, kv_heads, head_dim, q_len, k_len, causal, window, splits;
+    int32_t batch, heads, kv_heads, head_dim, q_len, k_len, causal, window, splits, kv_splits;
     float scale;
 };
 
@@ -684,7 +684,8 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dkv_kernel(AttnArg
     __shared__ __attribute__((aligned(1024))) char smem[SETS * 4 * G::BYTES];
     __shared__ __attribute__((aligned(16))) float stat[SETS][2][2][kTile];   // [set][buffer][L, -D]
     int blk, pair;
-    locate(blockIdx.x, blocks, a.batch * a.kv_heads, 1, false, blk, pair);
+    const int per = blocks * a.batch * a.kv_heads, split = blockIdx.x / per;
+    locate(blockIdx.x - split * per, blocks, a.batch * a.kv_heads, 1, false, blk, pair);
     const int b = pair / a.kv_heads, hk = pair % a.kv_heads, group = a.heads / a.kv_heads;
     const Seq sq = sequence(a, b);
     const int j0 = blk * kRows;
@@ -720,11 +721,13 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dkv_kernel(AttnArg
     // buffers of turn r
     auto qt = [&](int r) { return smem + (4 * set + (r & 1)) * G::BYTES; };
     auto gt = [&](int r) { return smem + (4 * set + 2 + (r & 1)) * G::BYTES; };
-    // step n: query tile n % tiles of the group's head n / tiles; turn r of a set is step SETS r + set
-    const int steps = tiles * group, turns = (steps + SETS - 1) / SETS;
+    // step n: query tile n % tiles of the group's head n / tiles; this split's
+    // steps are [from, to), and turn r of a set is step from + SETS r + set
+    const int steps = tiles * group, each = (steps + a.kv_splits - 1) / a.kv_splits;
+    const int from = split * each, to = min(steps, from + each), turns = (to - from + SETS - 1) / SETS;
     auto fill = [&](int r) {
-        const int n = SETS * r + set;
-        if (n >= steps) return;
+        const int n = from + SETS * r + set;
+        if (n >= to) return;
         const int hq = hk * group + n / tiles, first = (first_t + n % tiles) * kTile;
         cq.tile(qt(r), rows_of(a.q, b, sq.q0, hq), first, sq.nq, a.head_dim);
         cg.tile(gt(r), rows_of(a.dout, b, sq.q0, hq), first, sq.nq, a.head_dim);
@@ -745,8 +748,8 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dkv_kernel(AttnArg
     for (int r = 0; r < turns; ++r) {
         tile_barrier();
         fill(r + 1);
-        const int n = SETS * r + set;
-        if (n >= steps) continue;
+        const int n = from + SETS * r + set;
+        if (n >= to) continue;
         const int t = first_t + n % tiles;
         if (t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
         Lane<T, DB> at = ln.in(qt(r));
@@ -825,10 +828,40 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dkv_kernel(AttnArg
             }
     }
     if (j >= sq.k_rows) return;
+    if (a.kv_splits > 1) {
+        const int64_t row = (((int64_t)split * a.kv_heads + hk) * a.k_tokens + (a.q_start ? sq.k0 : (int64_t)b * a.k_len) + j) * (32 * DB);
+        if (SETS == 1 || set == 0) store_part<DB>(dk, a.part + row);
+        if (SETS == 1 || set == 1) store_part<DB>(dv, a.part_v + row);
+        return;
+    }
     if (SETS == 1 || set == 0)
         store_t<T, DB>(dk, a.scale, rows_of(a.dk, b, sq.k0, hk) + (int64_t)j * a.dk.token, a.head_dim);
     if (SETS == 1 || set == 1)
         store_t<T, DB>(dv, 1.f, rows_of(a.dv, b, sq.k0, hk) + (int64_t)j * a.dv.token, a.head_dim);
+}
+
+// Adds the splits of dK and dV: eight columns a thread, 16 threads a row.
+template <class T>
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kv_kernel(AttnArgs a, int width, int blocks) {
+    const int b = blockIdx.x / blocks / a.kv_heads, hk = blockIdx.x / blocks % a.kv_heads;
+    const Seq sq = sequence(a, b);
+    const int j = blockIdx.x % blocks * kJoinRows + threadIdx.x / 16, col = threadIdx.x % 16 * 8;
+    if (j >= sq.k_rows || col >= a.head_dim) return;
+    const bool v_part = blockIdx.y;
+    const float* part = v_part ? a.part_v : a.part;
+    const int64_t row = (a.q_start ? sq.k0 : (int64_t)b * a.k_len) + j;
+    float x[8] = {};
+    for (int s = 0; s < a.kv_splits; ++s) {
+        float v[8];
+        load8(part + (((int64_t)s * a.kv_heads + hk) * a.k_tokens + row) * width + col, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] += v[e];
+    }
+    const float mul = v_part ? 1.f : a.scale;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= mul;
+    const Tensor& t = v_part ? a.dv : a.dk;
+    store8((T*)(rows_of(t, b, sq.k0, hk) + (int64_t)j * t.token) + col, x);
 }
 
 // ------------------------------------------------------------------ host ----
@@ -892,22 +925,32 @@ AttnArgs attn_args(const opt_attention_desc* a) {
 int row_blocks(int len) { return (len + kRows - 1) / kRows; }
 int64_t query_blocks(const AttnArgs& x) { return (int64_t)row_blocks(x.q_len) * x.batch * x.heads; }
 
-// Key splits of the forward and dQ kernels: enough for one workgroup on each
-// of the 256 CUs, of at least eight tiles each, so that the partial sums stay
-// below the keys and values read.
-int key_splits(const AttnArgs& x) {
-    const int64_t wgs = query_blocks(x);
+// Parts to split `steps` of 64 rows into, for a launch of `wgs` workgroups:
+// enough for one on each of the 256 CUs, or two where a causal bound leaves
+// them uneven, but at least eight steps each, so that the partial sums stay
+// below what is read.
+int split_steps(int64_t wgs, int64_t steps, bool causal) {
     if (wgs == 0) return 1;
-    const int64_t most = x.window && x.window + kRows < x.k_len ? x.window + kRows : x.k_len;
-    const int64_t tiles = (most + kTile - 1) / kTile;
-    int64_t s = 256 / wgs;
-    if (s > tiles / 8) s = tiles / 8;
+    int64_t s = (causal ? 512 : 256) / wgs;
+    if (s > steps / 8) s = steps / 8;
     return (int)(s < 1 ? 1 : s > 32 ? 32 : s);
+}
+int64_t tiles_of(int len, const AttnArgs& x) {
+    const int64_t n = x.window && x.window + kRows < len ? x.window + kRows : len;
+    return (n + kTile - 1) / kTile;
+}
+int key_splits(const AttnArgs& x) { return split_steps(query_blocks(x), tiles_of(x.k_len, x), x.causal); }
+int query_splits(const AttnArgs& x) {
+    const int64_t wgs = (int64_t)row_blocks(x.k_len) * x.batch * x.kv_heads;
+    return split_steps(wgs, tiles_of(x.q_len, x) * (x.heads / x.kv_heads), x.causal);
 }
 
 // Two sets of wavefronts a workgroup where the launch has too few for two
-// workgroups a CU.
-bool two_sets(int64_t wgs) { return wgs < 512; }
+// workgroups a CU. Between 256 and 512 of even work, some CUs with two
+// workgroups of one set are done sooner than all with one or two of two sets
+// (81 against 93 us, 320 workgroups); of uneven work they are not (104
+// against 76 us, 448).
+bool two_sets(int64_t wgs, bool causal) { return wgs <= 256 || (causal && wgs < 512); }
 
 enum Kind { FORWARD, DQ, DKV };
 template <class T, int DB>
@@ -917,13 +960,18 @@ void launch(Kind kind, AttnArgs x, hipStream_t s) {
     if (grid == 0) return;
     const dim3 one(64 * kWaves), two(2 * 64 * kWaves);
     if (kind == DKV) {
-        const dim3 g((uint32_t)grid);
-        if (x.causal || two_sets(grid)) attn_dkv_kernel<T, DB, 2><<<g, two, 0, s>>>(x, blocks);
+        const dim3 g((uint32_t)(grid * x.kv_splits));
+        if (x.causal || two_sets(grid * x.kv_splits, false)) attn_dkv_kernel<T, DB, 2><<<g, two, 0, s>>>(x, blocks);
         else attn_dkv_kernel<T, DB, 1><<<g, one, 0, s>>>(x, blocks);
+        if (x.kv_splits > 1) {
+            const int jb = (x.k_len + kJoinRows - 1) / kJoinRows;
+            const dim3 j((uint32_t)((int64_t)jb * x.batch * x.kv_heads), 2);
+            attn_join_kv_kernel<T><<<j, kJoinThreads, 0, s>>>(x, 32 * DB, jb);
+        }
         return;
     }
     const dim3 g((uint32_t)(grid * x.splits));
-    const bool sets = two_sets(grid * x.splits);
+    const bool sets = two_sets(grid * x.splits, x.causal);
     if (kind == FORWARD) {
         if (sets) attn_forward_kernel<T, DB, 2><<<g, two, 0, s>>>(x, blocks);
         else attn_forward_kernel<T, DB, 1><<<g, one, 0, s>>>(x, blocks);
@@ -949,31 +997,39 @@ void launch(Kind kind, int32_t dtype, const AttnArgs& x, hipStream_t s) {
     dtype == OPT_BF16 ? launch<__bf16>(kind, x, s) : launch<_Float16>(kind, x, s);
 }
 
-// The workspace: D (backward), then the key splits' partial results.
+// The workspace: D (backward), then the splits' partial results. dQ's are
+// joined before dK's and dV's are written, in the same place.
 struct Space {
-    uint64_t delta, part, part_m, part_l, bytes;
-    int splits;
+    uint64_t delta, part, part_v, part_m, part_l, bytes;
+    int splits, kv_splits;
 };
 Space space_of(const AttnArgs& x, bool backward) {
     const auto up = [](uint64_t n) { return (n + 255) / 256 * 256; };
     const uint64_t rows = (uint64_t)x.q_tokens * (uint64_t)x.heads, width = (uint64_t)(x.head_dim + 31) / 32 * 32;
+    const uint64_t k_rows = (uint64_t)x.k_tokens * (uint64_t)x.kv_heads;
     Space s = {};
     s.splits = rows ? key_splits(x) : 1;
+    s.kv_splits = backward && k_rows ? query_splits(x) : 1;
     if (backward) s.bytes += up(rows * 4);
-    if (s.splits > 1) {
-        s.part = s.bytes, s.bytes += up(s.splits * rows * width * 4);
-        if (!backward) {
-            s.part_m = s.bytes, s.bytes += up(s.splits * rows * 4);
-            s.part_l = s.bytes, s.bytes += up(s.splits * rows * 4);
-        }
+    s.part = s.bytes;
+    const uint64_t q_part = s.splits > 1 ? up(s.splits * rows * width * 4) : 0;
+    if (backward) {
+        const uint64_t k_part = s.kv_splits > 1 ? up(s.kv_splits * k_rows * width * 4) : 0;
+        s.part_v = s.part + k_part;
+        s.bytes += q_part > 2 * k_part ? q_part : 2 * k_part;
+    } else if (s.splits > 1) {
+        s.bytes += q_part;
+        s.part_m = s.bytes, s.bytes += up(s.splits * rows * 4);
+        s.part_l = s.bytes, s.bytes += up(s.splits * rows * 4);
     }
     return s;
 }
 void use_space(AttnArgs& x, const Space& s, void* ws) {
     char* p = (char*)ws;
-    x.splits = s.splits;
+    x.splits = s.splits, x.kv_splits = s.kv_splits;
     x.delta = (float*)(p + s.delta);
-    x.part = (float*)(p + s.part), x.part_m = (float*)(p + s.part_m), x.part_l = (float*)(p + s.part_l);
+    x.part = (float*)(p + s.part), x.part_v = (float*)(p + s.part_v);
+    x.part_m = (float*)(p + s.part_m), x.part_l = (float*)(p + s.part_l);
 }
 
 opt_status check_workspace(const void* ws, uint64_t bytes, uint64_t need) {
