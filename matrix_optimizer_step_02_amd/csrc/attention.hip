@@ -44,8 +44,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTile = 64;       // rows of an LDS tile
-constexpr int kWaves = 4;       // wavefronts of a workgroup, each with 32 rows of its own
-constexpr int kRows = 32 * kWaves;
 // A running maximum is raised only where it would grow by more than this
 // (in powers of two): P stays below 2^8, far from any overflow, its relative
 // rounding is unchanged, and the accumulators are rescaled in the first tile
@@ -95,7 +93,6 @@ struct Geo {
     static constexpr int SLOTS = RB / 16;
     static constexpr int BYTES = kTile * RB;
     static constexpr int CHUNKS = BYTES / 1024;     // 1 KiB per wavefront and copy instruction
-    static constexpr int PER_WAVE = CHUNKS / kWaves;
     static __device__ __forceinline__ int swz(int row) {
         return DB > 2 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
     }
@@ -145,32 +142,33 @@ __device__ __forceinline__ char* rows_of(const Tensor& t, int b, int64_t row0, i
 // hold what the eight addresses of a tile need. PIN computes them anew for
 // each tile (a kernel short of registers; the others run 5 % faster with
 // them kept).
-template <int DB, bool PIN = false>
+template <int DB, int W, bool PIN = false>
 struct Copy {
     using G = Geo<DB>;
+    static constexpr int PER_WAVE = G::CHUNKS / W;   // of W wavefronts
     int row0, group0;   // of chunk 0
     int64_t token;
 
     __device__ __forceinline__ void init(int64_t token_stride) {
-        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWaves;
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % W;
         token = token_stride;
-        row0 = wave * G::PER_WAVE * (1024 / G::RB) + lane / G::SLOTS;
+        row0 = wave * PER_WAVE * (1024 / G::RB) + lane / G::SLOTS;
         group0 = (lane % G::SLOTS) ^ G::swz(row0);
     }
     // rows first .. first + 63 of a sequence of n rows
     __device__ __forceinline__ void tile(char* lds, const char* base, int first, int n, int head_dim) const {
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWaves;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % W;
         const char* origin = base + (int64_t)first * token;
         int r0 = row0, g0 = group0;
         if constexpr (PIN) asm volatile("" : "+v"(r0), "+v"(g0));
 #pragma unroll
-        for (int i = 0; i < G::PER_WAVE; ++i) {
+        for (int i = 0; i < PER_WAVE; ++i) {
             const int row = r0 + i * (1024 / G::RB), group = g0 ^ G::chunk_swz(i);
             const uint32_t off = (uint32_t)row * (uint32_t)token + 16 * group;
             const bool in = row < n - first && 8 * group < head_dim;
             const void* src = in ? (const void*)(origin + off) : (const void*)g_attn_zero;
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                             (__attribute__((address_space(3))) void*)(lds + (wave * G::PER_WAVE + i) * 1024),
+                                             (__attribute__((address_space(3))) void*)(lds + (wave * PER_WAVE + i) * 1024),
                                              16, 0, 0);
         }
     }
@@ -304,35 +302,35 @@ struct Sight {
     __device__ __forceinline__ int lo(int i) const { return window ? max(i + off - window + 1, 0) : 0; }
 };
 
-// Why the forward and dQ kernels come with one or two sets of four wavefronts
-// per workgroup, and split the keys over workgroups. Registers leave room for
-// two wavefronts a SIMD, which come from two workgroups (SETS = 1) where the
-// launch has two a CU. Else a workgroup has two sets with LDS tiles of their
-// own, which take the key tiles in turn and join their sums through LDS. Where
-// the launch has fewer workgroups than the GPU has CUs (few queries on a long
-// context), the keys are also split over workgroups, which leave fp32 partial
-// sums in the workspace for a second kernel to join: 509 queries on 8192 keys,
-// 16 / 8 heads of 128, take 49 + 5 us in place of 215.
+// Workgroups come in three shapes: four wavefronts (128 rows), eight (256
+// rows) that share the same tiles, or two sets of four (128 rows) with LDS
+// tiles of their own, which take the tiles in turn and join their sums through
+// LDS. Registers leave room for two wavefronts a SIMD: two workgroups a CU of
+// the first shape, one of the others. Where the launch has fewer workgroups
+// than the GPU has CUs (few queries on a long context), the tiles are also
+// split over workgroups, which leave fp32 partial sums in the workspace for a
+// second kernel to join: 509 queries on 8192 keys, 16 / 8 heads of 128, take
+// 49 + 5 us in place of 215. The host chooses (shape_of, splits_of).
 struct Block {
     int b, hq, hk, i0, split;
 };
-__device__ __forceinline__ Block block_of(const AttnArgs& a, int blocks) {
+__device__ __forceinline__ Block block_of(const AttnArgs& a, int blocks, int rows) {
     const int group = a.heads / a.kv_heads;
     const int per = blocks * a.batch * a.heads;   // workgroups of one split
     Block x;
     x.split = blockIdx.x / per;
     int blk, pair;
     locate(blockIdx.x - x.split * per, blocks, a.batch * a.heads, group, a.causal, blk, pair);
-    x.b = pair / a.heads, x.hq = pair % a.heads, x.hk = x.hq / group, x.i0 = blk * kRows;
+    x.b = pair / a.heads, x.hq = pair % a.heads, x.hk = x.hq / group, x.i0 = blk * rows;
     return x;
 }
 
 // Key tiles [first, end) of this workgroup's queries and split.
-__device__ __forceinline__ void tile_range(const AttnArgs& a, const Sight& see, int i0, int nq, int split, int& first, int& end) {
+__device__ __forceinline__ void tile_range(const AttnArgs& a, const Sight& see, int i0, int rows, int nq, int split, int& first, int& end) {
     first = end = 0;
     if (i0 >= nq) return;
     first = see.lo(i0) / kTile;
-    end = (see.hi(min(i0 + kRows, nq) - 1) + kTile - 1) / kTile;
+    end = (see.hi(min(i0 + rows, nq) - 1) + kTile - 1) / kTile;
     if (a.splits > 1) {
         const int each = (max(end - first, 0) + a.splits - 1) / a.splits;
         first += split * each;
@@ -361,8 +359,8 @@ __device__ __forceinline__ void store_part(const f32x16 (&acc)[DB], float* row) 
 }
 
 // Hands accumulators (and two more values) from set 1 to set 0 through the
-// LDS of the tiles, which every wavefront has left. kWaves * 64 * (16 DB + 2)
-// floats at most.
+// LDS of the tiles, which every wavefront has left: 64 (16 DB + 2) floats of
+// each wavefront.
 template <int DB>
 __device__ __forceinline__ void give(char* smem, int wave, const f32x16 (&acc)[DB], float x, float y) {
     const int lane = threadIdx.x & 63;
@@ -395,19 +393,19 @@ __device__ __forceinline__ void take(const char* smem, int wave, float mine, flo
 
 // --------------------------------------------------------------- forward ----
 
-template <class T, int DB, int SETS>
-__global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_forward_kernel(AttnArgs a, int blocks) {
+template <class T, int DB, int W, int SETS>
+__global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
     using FT = Frag<T>;
     using F = typename FT::type;
     __shared__ __attribute__((aligned(1024))) char smem[SETS * 4 * G::BYTES];
-    const Block wg = block_of(a, blocks);
+    const Block wg = block_of(a, blocks, 32 * W);
     const int b = wg.b, hq = wg.hq, hk = wg.hk, i0 = wg.i0;
     const Seq sq = sequence(a, b);
     if (i0 >= sq.q_rows) return;
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % kWaves;
-    const int set = SETS > 1 ? wave8 / kWaves : 0;
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % W;
+    const int set = SETS > 1 ? wave8 / W : 0;
     const int w0 = i0 + 32 * wave, i = w0 + l32;   // the wavefront's first query, the lane's query
     const Sight see = {sq.nk, sq.nk - sq.nq, a.window, a.causal};
 
@@ -415,7 +413,7 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_forward_kernel(Att
     ln.init();
     F qf[2 * DB];
     load_rows<T, DB>(qf, rows_of(a.q, b, sq.q0, hq), a.q.token, i, sq.nq, a.head_dim);
-    Copy<DB> ck, cv;
+    Copy<DB, W> ck, cv;
     ck.init(a.k.token);
     cv.init(a.v.token);
     const char* kb = rows_of(a.k, b, sq.k0, hk);
@@ -425,7 +423,7 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_forward_kernel(Att
     float m = kLowest, l = 0.f;
     const float c = a.scale * kLog2e;
     int first_t, end_t;
-    tile_range(a, see, i0, sq.nq, wg.split, first_t, end_t);
+    tile_range(a, see, i0, 32 * W, sq.nq, wg.split, first_t, end_t);
     // keys that any query of this wavefront sees, and the lane's
     const int wlast = min(w0 + 32, sq.nq) - 1;
     const int whi = w0 < sq.nq ? see.hi(wlast) : 0, wlo = see.lo(w0);
@@ -556,19 +554,19 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
 // -------------------------------------------------------------- backward ----
 
 // dQ, and D for the other kernel. A lane owns one query, as in the forward pass.
-template <class T, int DB, int SETS>
-__global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dq_kernel(AttnArgs a, int blocks) {
+template <class T, int DB, int W, int SETS>
+__global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
     using FT = Frag<T>;
     using F = typename FT::type;
     __shared__ __attribute__((aligned(1024))) char smem[SETS * 4 * G::BYTES];
-    const Block wg = block_of(a, blocks);
+    const Block wg = block_of(a, blocks, 32 * W);
     const int b = wg.b, hq = wg.hq, hk = wg.hk, i0 = wg.i0;
     const Seq sq = sequence(a, b);
     if (i0 >= sq.q_rows) return;
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % kWaves;
-    const int set = SETS > 1 ? wave8 / kWaves : 0;
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % W;
+    const int set = SETS > 1 ? wave8 / W : 0;
     const int w0 = i0 + 32 * wave, i = w0 + l32;
     const Sight see = {sq.nk, sq.nk - sq.nq, a.window, a.causal};
 
@@ -581,11 +579,17 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dq_kernel(AttnArgs
         load_rows<T, DB>(of, rows_of(a.o, b, sq.q0, hq), a.o.token, i, sq.nq, a.head_dim);
         load_rows<T, DB>(gf, rows_of(a.dout, b, sq.q0, hq), a.dout.token, i, sq.nq, a.head_dim);
         load_rows<T, DB>(qf, rows_of(a.q, b, sq.q0, hq), a.q.token, i, sq.nq, a.head_dim);
+        // D is the diagonal of O dO^T, by the products that form dP = V dO^T:
+        // where a row sees one key, O is that key's V to the bit, dP - D is
+        // zero, and so are its gradients
+        f32x16 x = {};
 #pragma unroll
-        for (int s = 0; s < 2 * DB; ++s)
+        for (int s = 0; s < 2 * DB; ++s) x = FT::mma(of[s], gf[s], x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) D = fmaf((float)of[s][e], (float)gf[s][e], D);
-        D += other_half(D);
+        for (int r = 0; r < 16; ++r)
+            if (8 * (r >> 2) + 4 * h + (r & 3) == l32) D = x[r];
+        const float y = other_half(D);
+        D = ((l32 >> 2) & 1) == h ? D : y;   // the half that holds it
     }
     const int64_t at_row = (int64_t)hq * a.q_tokens + sq.l0 + i;
     // a row that sees no key has L = -inf: with +inf in its place P is 0
@@ -595,7 +599,7 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dq_kernel(AttnArgs
         if (L2 == -INFINITY) L2 = INFINITY;
         if (h == 0 && set == 0 && wg.split == 0) gptr(a.delta)[at_row] = D;
     }
-    Copy<DB> ck, cv;
+    Copy<DB, W> ck, cv;
     ck.init(a.k.token);
     cv.init(a.v.token);
     const char* kb = rows_of(a.k, b, sq.k0, hk);
@@ -603,7 +607,7 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dq_kernel(AttnArgs
     f32x16 dq[DB] = {};
     const float c = a.scale * kLog2e;
     int first_t, end_t;
-    tile_range(a, see, i0, sq.nq, wg.split, first_t, end_t);
+    tile_range(a, see, i0, 32 * W, sq.nq, wg.split, first_t, end_t);
     const int wlast = min(w0 + 32, sq.nq) - 1;
     const int whi = w0 < sq.nq ? see.hi(wlast) : 0, wlo = see.lo(w0);
     const int hi = i < sq.nq ? see.hi(i) : 0, lo = see.lo(i);
@@ -665,33 +669,27 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dq_kernel(AttnArgs
         store_t<T, DB>(dq, a.scale, rows_of(a.dq, b, sq.q0, hq) + (int64_t)i * a.dq.token, a.head_dim);
 }
 
-// dK and dV of 128 keys, summed over the queries that see them and over the
-// heads of the group. A lane owns one key. The keys' accumulators (128
-// registers at head_dim 128) and operands leave room for two wavefronts a
-// SIMD, which come from two workgroups (SETS = 1), or from two sets of four
-// wavefronts of one, each with LDS tiles of its own, that take the steps
-// (query tile, head) of the same keys in turn and add their sums through LDS
-// at the end. The common barrier costs 10 % where all key blocks have equal
-// work (1053 against 1163 us, 4 x 4096 tokens, 16 heads of 128). A causal
-// sequence's first keys have twice the mean work, though, and a workgroup of
-// one set runs on alone at half the rate: 777 against 553 us (8192 tokens, 16 /
-// 8 heads of 128).
-template <class T, int DB, int SETS>
-__global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dkv_kernel(AttnArgs a, int blocks) {
+// dK and dV of 32 W keys, summed over the queries that see them and over the
+// heads of the group; the steps are (head, query tile). A lane owns one key.
+// The keys' accumulators (128 registers at head_dim 128) and operands (64)
+// leave little of the 256 registers that two wavefronts a SIMD have, so the
+// addresses are computed where they are used.
+template <class T, int DB, int W, int SETS>
+__global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dkv_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
     using FT = Frag<T>;
     using F = typename FT::type;
     __shared__ __attribute__((aligned(1024))) char smem[SETS * 4 * G::BYTES];
-    __shared__ __attribute__((aligned(16))) float stat[SETS][2][2][kTile];   // [set][buffer][L, -D]
+    __shared__ __attribute__((aligned(16))) float stat[SETS][2][2][kTile];   // [set][buffer][L, D]
     int blk, pair;
     const int per = blocks * a.batch * a.kv_heads, split = blockIdx.x / per;
     locate(blockIdx.x - split * per, blocks, a.batch * a.kv_heads, 1, false, blk, pair);
     const int b = pair / a.kv_heads, hk = pair % a.kv_heads, group = a.heads / a.kv_heads;
     const Seq sq = sequence(a, b);
-    const int j0 = blk * kRows;
+    const int j0 = blk * 32 * W;
     if (j0 >= sq.k_rows) return;
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % kWaves, set = SETS > 1 ? wave8 / kWaves : 0;
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % W, set = SETS > 1 ? wave8 / W : 0;
     const int w0 = j0 + 32 * wave, j = w0 + l32;   // the wavefront's first key, the lane's key
     const int off = sq.nk - sq.nq;
 
@@ -700,7 +698,7 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dkv_kernel(AttnArg
     F kf[2 * DB], vf[2 * DB];
     load_rows<T, DB>(kf, rows_of(a.k, b, sq.k0, hk), a.k.token, j, sq.nk, a.head_dim);
     load_rows<T, DB>(vf, rows_of(a.v, b, sq.k0, hk), a.v.token, j, sq.nk, a.head_dim);
-    Copy<DB, true> cq, cg;
+    Copy<DB, W, true> cq, cg;
     cq.init(a.q.token);
     cg.init(a.dout.token);
     f32x16 dk[DB] = {}, dv[DB] = {};
@@ -709,7 +707,7 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dkv_kernel(AttnArg
     // queries [lo, hi) that see key j: j <= i + off, and j > i + off - window
     auto qlo = [&](int key) { return a.causal ? clampi(key - off, 0, sq.nq) : 0; };
     auto qhi = [&](int key) { return a.window ? clampi(key - off + a.window, 0, sq.nq) : sq.nq; };
-    const int jl = min(j0 + kRows, sq.nk) - 1, wl = min(w0 + 32, sq.nk) - 1;
+    const int jl = min(j0 + 32 * W, sq.nk) - 1, wl = min(w0 + 32, sq.nk) - 1;
     const bool any = j0 < sq.nk;
     const int first_t = any ? qlo(j0) / kTile : 0;
     const int end_t = any ? (qhi(jl) + kTile - 1) / kTile : 0;
@@ -738,7 +736,7 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dkv_kernel(AttnArg
             if (i < sq.nq) {
                 L = gptr(a.lse)[at] * kLog2e;
                 if (L == -INFINITY) L = INFINITY;
-                D = -gptr(a.delta)[at];
+                D = gptr(a.delta)[at];
             }
             stat[set][r & 1][0][lane] = L;
             stat[set][r & 1][1][lane] = D;
@@ -759,14 +757,7 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dkv_kernel(AttnArg
         for (int u = 0; u < 2; ++u) {
             at.pin();
             if constexpr (DB > 2) __builtin_amdgcn_sched_barrier(0);
-            // dP - D: the product starts from -D of the accumulator's rows
-            f32x16 s = {}, dp;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const f32x4 D = *(const f32x4*)&stat[set][r & 1][1][32 * u + 8 * g + 4 * h];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dp[4 * g + e] = D[e];
-            }
+            f32x16 s = {}, dp = {};
 #pragma unroll
             for (int ks = 0; ks < 2 * DB; ++ks) {
                 s = FT::mma(at.rows(Q, u, ks), kf[ks], s);
@@ -782,10 +773,11 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dkv_kernel(AttnArg
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const f32x4 L = *(const f32x4*)&stat[set][r & 1][0][32 * u + 8 * g + 4 * h];
+                const f32x4 D = *(const f32x4*)&stat[set][r & 1][1][32 * u + 8 * g + 4 * h];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     s[4 * g + e] = __builtin_amdgcn_exp2f(fmaf(s[4 * g + e], c, -L[e]));
-                    dp[4 * g + e] *= s[4 * g + e];
+                    dp[4 * g + e] = s[4 * g + e] * (dp[4 * g + e] - D[e]);
                 }
             }
 #pragma unroll
@@ -802,10 +794,10 @@ __global__ __launch_bounds__(SETS * 64 * kWaves, 2) void attn_dkv_kernel(AttnArg
     }
     if constexpr (SETS > 1) {
         // set 1's dK and set 0's dV cross over through LDS, and each set stores the sum it then has
-        static_assert(2 * kWaves * DB * 16 * 256 <= sizeof smem, "the accumulators do not fit the tiles' LDS");
+        static_assert(2 * W * DB * 16 * 256 <= sizeof smem, "the accumulators do not fit the tiles' LDS");
         tile_barrier();
-        float* mine = (float*)smem + (set * kWaves + wave) * DB * 1024 + lane * 4;
-        float* theirs = (float*)smem + ((1 - set) * kWaves + wave) * DB * 1024 + lane * 4;
+        float* mine = (float*)smem + (set * W + wave) * DB * 1024 + lane * 4;
+        float* theirs = (float*)smem + ((1 - set) * W + wave) * DB * 1024 + lane * 4;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -922,68 +914,86 @@ AttnArgs attn_args(const opt_attention_desc* a) {
     return x;
 }
 
-int row_blocks(int len) { return (len + kRows - 1) / kRows; }
-int64_t query_blocks(const AttnArgs& x) { return (int64_t)row_blocks(x.q_len) * x.batch * x.heads; }
+int64_t row_blocks(int len, int rows) { return (len + rows - 1) / rows; }
 
-// Parts to split `steps` of 64 rows into, for a launch of `wgs` workgroups:
-// enough for one on each of the 256 CUs, or two where a causal bound leaves
-// them uneven, but at least eight steps each, so that the partial sums stay
-// below what is read.
-int split_steps(int64_t wgs, int64_t steps, bool causal) {
+// Blocks of 128 rows with work to do. Packed sequences: the launch covers the
+// longest for each, the blocks past a shorter one's end leave at once.
+int64_t busy_blocks(const AttnArgs& x, bool keys) {
+    const int64_t n = row_blocks(keys ? x.k_len : x.q_len, 128) * x.batch;
+    const int64_t packed = (keys ? x.k_tokens : x.q_tokens) / 128 + x.batch;
+    return (x.q_start && packed < n ? packed : n) * (keys ? x.kv_heads : x.heads);
+}
+// Tiles of 64 keys a block of queries steps through (or of queries a block of
+// keys, over the heads of its group).
+int64_t block_steps(const AttnArgs& x, bool keys) {
+    const int len = keys ? x.q_len : x.k_len;
+    const int64_t n = x.window && x.window + 128 < len ? x.window + 128 : len;
+    return (n + kTile - 1) / kTile * (keys ? x.heads / x.kv_heads : 1);
+}
+
+// Parts to split a block's steps into, over workgroups: enough for `fill`
+// workgroups, but at least eight steps each, so that the partial sums stay
+// below what is read. One workgroup a CU; two for the keys of a causal
+// sequence, whose blocks are uneven (4096 tokens, 16 / 8 heads of 128: dK and
+// dV 232 us without, 185 with two). Two for its queries gained nothing (46
+// against 42 us, 2048 tokens).
+int splits_of(const AttnArgs& x, bool keys) {
+    const int64_t wgs = busy_blocks(x, keys), steps = block_steps(x, keys);
     if (wgs == 0) return 1;
-    int64_t s = (causal ? 512 : 256) / wgs;
+    int64_t s = (keys && x.causal ? 512 : 256) / wgs;
     if (s > steps / 8) s = steps / 8;
     return (int)(s < 1 ? 1 : s > 32 ? 32 : s);
 }
-int64_t tiles_of(int len, const AttnArgs& x) {
-    const int64_t n = x.window && x.window + kRows < len ? x.window + kRows : len;
-    return (n + kTile - 1) / kTile;
-}
-int key_splits(const AttnArgs& x) { return split_steps(query_blocks(x), tiles_of(x.k_len, x), x.causal); }
-int query_splits(const AttnArgs& x) {
-    const int64_t wgs = (int64_t)row_blocks(x.k_len) * x.batch * x.kv_heads;
-    return split_steps(wgs, tiles_of(x.q_len, x) * (x.heads / x.kv_heads), x.causal);
-}
-
-// Two sets of wavefronts a workgroup where the launch has too few for two
-// workgroups a CU. Between 256 and 512 of even work, some CUs with two
-// workgroups of one set are done sooner than all with one or two of two sets
-// (81 against 93 us, 320 workgroups); of uneven work they are not (104
-// against 76 us, 448).
-bool two_sets(int64_t wgs, bool causal) { return wgs <= 256 || (causal && wgs < 512); }
 
 enum Kind { FORWARD, DQ, DKV };
+
+// Wavefronts and sets of a workgroup. `wgs`: workgroups of 128 rows with work.
+//  - Up to one a CU: two sets. Also while there are few and uneven ones, the
+//    longest of which would run on alone: causal, below 1024 (keys, with twice
+//    the work at their uneven end: 2048), of 32 steps at least. Forward, us,
+//    two sets against one: 76 / 104 (3500 tokens, 16 heads of 128), 83 / 101
+//    (4096); short ones 28 / 23 (8 x 512), 37 / 33 (4 x 1024). dK and dV with dQ: 946 / 1182 (8192
+//    tokens, 8 key heads), but 1095 / 1020 (4 x 4096, 16 key heads).
+//  - Plenty: eight wavefronts share each tile. Half the copies into LDS, which
+//    cost power, and the clock follows the power drawn: 277 us against 298 of
+//    four (forward, 8192 tokens), 521 / 534 (not causal); few ones are left
+//    with a part-filled last round: 51 / 46 (6 x 1000, 16 heads of 64).
+//  - Else one set of four, two workgroups a CU.
+enum Shape { W4S2, W4S1, W8S1 };
+Shape shape_of(const AttnArgs& x, Kind kind) {
+    const bool keys = kind == DKV;
+    const int splits = keys ? x.kv_splits : x.splits;
+    const int64_t wgs = busy_blocks(x, keys) * splits, steps = block_steps(x, keys) / splits;
+    if (wgs <= 256 || (x.causal && wgs < (keys ? 2048 : 1024) && steps >= 32)) return W4S2;
+    return wgs >= 1024 ? W8S1 : W4S1;
+}
+
+template <class T, int DB, int W, int SETS>
+void launch_shape(Kind kind, const AttnArgs& x, hipStream_t s) {
+    const int blocks = (int)row_blocks(kind == DKV ? x.k_len : x.q_len, 32 * W);
+    const int64_t grid = (int64_t)blocks * x.batch * (kind == DKV ? (int64_t)x.kv_heads * x.kv_splits
+                                                                  : (int64_t)x.heads * x.splits);
+    const dim3 g((uint32_t)grid), n(SETS * 64 * W);
+    if (kind == FORWARD) attn_forward_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, blocks);
+    else if (kind == DQ) attn_dq_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, blocks);
+    else attn_dkv_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, blocks);
+}
+
 template <class T, int DB>
-void launch(Kind kind, AttnArgs x, hipStream_t s) {
-    const int blocks = row_blocks(kind == DKV ? x.k_len : x.q_len);
-    int64_t grid = (int64_t)blocks * x.batch * (kind == DKV ? x.kv_heads : x.heads);
-    if (grid == 0) return;
-    const dim3 one(64 * kWaves), two(2 * 64 * kWaves);
-    if (kind == DKV) {
-        const dim3 g((uint32_t)(grid * x.kv_splits));
-        if (x.causal || two_sets(grid * x.kv_splits, false)) attn_dkv_kernel<T, DB, 2><<<g, two, 0, s>>>(x, blocks);
-        else attn_dkv_kernel<T, DB, 1><<<g, one, 0, s>>>(x, blocks);
-        if (x.kv_splits > 1) {
-            const int jb = (x.k_len + kJoinRows - 1) / kJoinRows;
-            const dim3 j((uint32_t)((int64_t)jb * x.batch * x.kv_heads), 2);
-            attn_join_kv_kernel<T><<<j, kJoinThreads, 0, s>>>(x, 32 * DB, jb);
-        }
-        return;
+void launch(Kind kind, const AttnArgs& x, hipStream_t s) {
+    if ((kind == DKV ? x.k_len : x.q_len) == 0 || x.batch == 0) return;
+    switch (shape_of(x, kind)) {
+        case W4S2: launch_shape<T, DB, 4, 2>(kind, x, s); break;
+        case W4S1: launch_shape<T, DB, 4, 1>(kind, x, s); break;
+        case W8S1: launch_shape<T, DB, 8, 1>(kind, x, s); break;
     }
-    const dim3 g((uint32_t)(grid * x.splits));
-    const bool sets = two_sets(grid * x.splits, x.causal);
-    if (kind == FORWARD) {
-        if (sets) attn_forward_kernel<T, DB, 2><<<g, two, 0, s>>>(x, blocks);
-        else attn_forward_kernel<T, DB, 1><<<g, one, 0, s>>>(x, blocks);
-    } else {
-        if (sets) attn_dq_kernel<T, DB, 2><<<g, two, 0, s>>>(x, blocks);
-        else attn_dq_kernel<T, DB, 1><<<g, one, 0, s>>>(x, blocks);
-    }
-    if (x.splits > 1) {
-        const int jb = (x.q_len + kJoinRows - 1) / kJoinRows;
-        const dim3 j((uint32_t)((int64_t)jb * x.batch * x.heads));
+    if (kind == DKV ? x.kv_splits > 1 : x.splits > 1) {
+        const int jb = (int)row_blocks(kind == DKV ? x.k_len : x.q_len, kJoinRows);
+        const int64_t n = (int64_t)jb * x.batch * (kind == DKV ? x.kv_heads : x.heads);
+        const dim3 j((uint32_t)n, kind == DKV ? 2 : 1);
         if (kind == FORWARD) attn_join_kernel<T, true><<<j, kJoinThreads, 0, s>>>(x, 32 * DB, jb);
-        else attn_join_kernel<T, false><<<j, kJoinThreads, 0, s>>>(x, 32 * DB, jb);
+        else if (kind == DQ) attn_join_kernel<T, false><<<j, kJoinThreads, 0, s>>>(x, 32 * DB, jb);
+        else attn_join_kv_kernel<T><<<j, kJoinThreads, 0, s>>>(x, 32 * DB, jb);
     }
 }
 template <class T>
@@ -1008,8 +1018,8 @@ Space space_of(const AttnArgs& x, bool backward) {
     const uint64_t rows = (uint64_t)x.q_tokens * (uint64_t)x.heads, width = (uint64_t)(x.head_dim + 31) / 32 * 32;
     const uint64_t k_rows = (uint64_t)x.k_tokens * (uint64_t)x.kv_heads;
     Space s = {};
-    s.splits = rows ? key_splits(x) : 1;
-    s.kv_splits = backward && k_rows ? query_splits(x) : 1;
+    s.splits = rows ? splits_of(x, false) : 1;
+    s.kv_splits = backward && k_rows ? splits_of(x, true) : 1;
     if (backward) s.bytes += up(rows * 4);
     s.part = s.bytes;
     const uint64_t q_part = s.splits > 1 ? up(s.splits * rows * width * 4) : 0;

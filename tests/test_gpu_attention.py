@@ -133,6 +133,22 @@ def test_windows(window):
     dense(1, 130, 300, 2, 1, 128, causal=True, window=window, seed=window)
 
 
+@pytest.mark.parametrize("nq,nk,causal,window", [(1, 1, True, 0), (130, 1, False, 0), (200, 200, True, 1), (40, 300, True, 1)])
+@pytest.mark.parametrize("d", [32, 64, 88, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_one_visible_key_has_no_score_gradient(nq, nk, causal, window, d, dtype):
+    """softmax over one key is 1 whatever the score: dq and dk are zero, not round-off, and out is the value."""
+    torch = _torch()
+    print(f"attention one key {nq} {nk} {d} {dtype}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(nq + d)
+    mk = lambda *s: torch.randn(*s, generator=g, device="cuda").to(_dt(dtype))  # noqa: E731
+    q, k, v, dout = mk(2, nq, 4, d), mk(2, nk, 2, d), mk(2, nk, 2, d), mk(2, nq, 4, d)
+    got = run(q, k, v, dout, causal=causal, window=window)
+    j = torch.arange(nq, device="cuda") + nk - nq if causal else torch.zeros(nq, dtype=torch.int64, device="cuda")
+    assert torch.equal(got["out"], v[:, j].repeat_interleave(2, dim=2))
+    assert (got["dq"] == 0).all() and (got["dk"] == 0).all()
+
+
 def test_large_scores_and_scales():
     dense(1, 200, 200, 2, 1, 128, spread=30.0, seed=1)
     dense(1, 200, 200, 2, 1, 64, scale=1.0, seed=2)
