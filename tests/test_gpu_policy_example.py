@@ -1,0 +1,75 @@
+"""GPU tests of examples/policy_step.py: the operators together, as a training
+step uses them. The whole model's gradients are compared with automatic
+differentiation of the same model in float64 on the CPU, from the same weights
+rounded to bfloat16; activations in bfloat16 are rounded about 8 times per
+block, each at most 2^-8, so gradients stay within 5 % in norm."""
+
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(model, tokens, target, old, ref, adv, w, kl):
+    """Loss and {name: gradient} in float64."""
+    import torch
+    W = {n: (s["W"] if n == "embed" else s["W"].bfloat16()).double().cpu().requires_grad_() for n, s in model.state.items()}
+    norms = [n for pair in model.norms for n in pair] + [model.last]
+    nw = [n.weight.double().cpu().requires_grad_() for n in norms]
+    nb = [n.bias.double().cpu().requires_grad_() for n in norms]
+    ln = lambda h, i: torch.nn.functional.layer_norm(h, h.shape[-1:], nw[i], nb[i], 1e-5)  # noqa: E731
+    b, t = tokens.shape
+    h = W["embed"][tokens.cpu()]
+    hide = torch.ones(t, t).triu(1).bool()
+    for n in range(len(model.norms)):
+        q, k, v = (ln(h, 2 * n) @ W[f"qkv{n}"]).view(b, t, -1, model.dim).split([model.heads, model.kv, model.kv], 2)
+        k, v = (x.repeat_interleave(model.heads // model.kv, 2) for x in (k, v))
+        s = torch.einsum("bihd,bjhd->bhij", q, k) / math.sqrt(model.dim)
+        p = s.masked_fill(hide, -math.inf).softmax(-1)
+        h = h + torch.einsum("bhij,bjhd->bihd", p, v).reshape(b, t, -1) @ W[f"o{n}"]
+        h = h + (ln(h, 2 * n + 1) @ W[f"up{n}"]).relu() @ W[f"down{n}"]
+    z = (ln(h, len(norms) - 1) @ W["head"]).view(b * t, -1)
+    logp = z.log_softmax(-1).gather(1, target.cpu()[:, None])[:, 0]
+    old, ref, adv, w = (x.double().cpu() for x in (old, ref, adv, w))
+    r, d = (logp - old).exp(), ref - logp
+    loss = (w * (torch.maximum(-adv * r, -adv * r.clip(0.8, 1.2)) + kl * (d.exp() - d - 1))).sum()
+    loss.backward()
+    return loss, {n: x.grad for n, x in W.items()}, [x.grad for x in nw], [x.grad for x in nb]
+
+
+def test_gradients_of_the_whole_model():
+    import torch
+    from examples import policy_step
+    from matrix_optimizer_step_02_amd import train
+    print("policy model gradients", flush=True)
+    torch.manual_seed(0)
+    model = policy_step.Policy(vocab=40, hidden=96, heads=6, kv_heads=2, ffn=200, layers=2, dropout=0.0)
+    tokens = torch.randint(0, 40, (4, 30), device="cuda")
+    n = tokens.numel()
+    target = torch.randint(0, 40, (n,), device="cuda")
+    logits = model.forward(tokens)
+    logp = logits.double().log_softmax(-1).gather(1, target[:, None])[:, 0].float()
+    # ratios away from the clip's borders by more than the activations' rounding
+    old = logp - torch.tensor([0.0, 0.5, -0.5, 0.05], device="cuda").repeat(n // 4)
+    ref, adv, w = logp + 0.2, torch.randn(n, device="cuda"), torch.rand(n, device="cuda") / n
+    loss, _, dlogits = train.policy_loss_step(logits, target, old, adv, w, ref_logp=ref, kl_coef=0.1)
+    model.backward(dlogits)
+    torch.cuda.synchronize()
+    want, grads, nw, nb = reference(model, tokens, target, old, ref, adv, w, 0.1)
+    assert abs(float(loss) - float(want)) <= 0.05 * float(w.sum())
+    near = lambda a, b: float((a.double().cpu() - b).norm() / b.norm())  # noqa: E731
+    off = {x: near(model.state[x]["G"], g) for x, g in grads.items()}
+    norms = [x for pair in model.norms for x in pair] + [model.last]
+    off |= {f"norm{i}": max(near(x.dweight, nw[i]), near(x.dbias, nb[i])) for i, x in enumerate(norms)}
+    print({k: round(v, 4) for k, v in off.items()}, flush=True)
+    assert max(off.values()) <= 0.05, off
+
+
+def test_training_learns_the_task():
+    """16 tokens to choose from: chance is 1/16; the mean reward of the last steps is several times that."""
+    from examples import policy_step
+    print("policy training", flush=True)
+    rewards = policy_step.train_policy(steps=60, vocab=16, log=lambda s: print(s, flush=True))
+    last = sum(rewards[-10:]) / 10
+    assert rewards[0] < 0.2 and last > 0.5, (rewards[0], last)
