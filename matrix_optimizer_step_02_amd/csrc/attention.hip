@@ -63,6 +63,7 @@ struct AttnArgs {
     const int32_t *q_start, *k_start, *q_lens, *k_lens;
     int64_t q_tokens, k_tokens;   // rows of lse and delta; packed: the token axes
     int32_t batch, heads, kv_heads, head_dim, q_len, k_len, causal, window, splits, kv_splits;
+    int32_t listed;   // packed: row blocks are found by their place in a list (block_of_list)
     float scale;
 };
 
@@ -109,18 +110,22 @@ struct Seq {
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
 
+// First row and length of packed sequence b: offsets that do not ascend, or
+// leave the token axis, cannot make an access leave it.
+__device__ __forceinline__ int64_t packed(const int32_t* start, int64_t tokens, int most, int b, int& n) {
+    const int64_t from = min(max((int64_t)gptr(start)[b], (int64_t)0), tokens);
+    const int64_t to = min(max((int64_t)gptr(start)[b + 1], from), tokens);
+    n = (int)min(to - from, (int64_t)most);
+    return from;
+}
+
 __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
     Seq s;
     if (a.q_start) {
-        // offsets that do not ascend, or leave the token axis, cannot make an access leave it
-        const int64_t qb = min(max((int64_t)gptr(a.q_start)[b], (int64_t)0), a.q_tokens);
-        const int64_t qe = min(max((int64_t)gptr(a.q_start)[b + 1], qb), a.q_tokens);
-        const int64_t kb = min(max((int64_t)gptr(a.k_start)[b], (int64_t)0), a.k_tokens);
-        const int64_t ke = min(max((int64_t)gptr(a.k_start)[b + 1], kb), a.k_tokens);
-        s.nq = s.q_rows = (int)min(qe - qb, (int64_t)a.q_len);
-        s.nk = s.k_rows = (int)min(ke - kb, (int64_t)a.k_len);
-        s.q0 = s.l0 = qb;
-        s.k0 = kb;
+        s.q0 = s.l0 = packed(a.q_start, a.q_tokens, a.q_len, b, s.nq);
+        s.k0 = packed(a.k_start, a.k_tokens, a.k_len, b, s.nk);
+        s.q_rows = s.nq;
+        s.k_rows = s.nk;
     } else {
         s.nq = a.q_lens ? clampi(gptr(a.q_lens)[b], 0, a.q_len) : a.q_len;
         s.nk = a.k_lens ? clampi(gptr(a.k_lens)[b], 0, a.k_len) : a.k_len;
@@ -311,18 +316,75 @@ struct Sight {
 // split over workgroups, which leave fp32 partial sums in the workspace for a
 // second kernel to join: 509 queries on 8192 keys, 16 / 8 heads of 128, take
 // 49 + 5 us in place of 215. The host chooses (shape_of, splits_of).
+// Row blocks of packed sequences, as a list without the blocks that a shorter
+// sequence lacks (a launch that covers the longest one for each sequence would
+// be mostly of those; 4 to 12 % at 13 sequences of 8192 tokens): entry `at` of the list of all (sequence, level) with
+// level below the sequence's number of blocks, highest level first, so that
+// the longest sequences' far blocks come first. Each wavefront finds it by
+// bisection over the levels, a sequence per lane. false: past the list's end.
+constexpr int kListed = 256;   // sequences at most: four turns of 64 per step
+__device__ __forceinline__ bool find_listed(const int32_t* start, int64_t tokens, int most, int batch, int rows, int at,
+                                            int& seq, int& level, int& levels) {
+    const int lane = threadIdx.x & 63;
+    int n[kListed / 64];
+#pragma unroll
+    for (int c = 0; c < kListed / 64; ++c) {
+        const int b = 64 * c + lane;
+        int len = 0;
+        if (b < batch) packed(start, tokens, most, b, len);
+        n[c] = (len + rows - 1) / rows;
+    }
+    const auto above = [&](int x) {   // entries of levels x and higher
+        int s = 0;
+#pragma unroll
+        for (int c = 0; c < kListed / 64; ++c) s += max(n[c] - x, 0);
+#pragma unroll
+        for (int m = 32; m; m >>= 1) s += __shfl_xor(s, m);
+        return __builtin_amdgcn_readfirstlane(s);
+    };
+    if (at >= above(0)) return false;
+    int lo = 0, hi = (most + rows - 1) / rows;   // above(lo) > at >= above(hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (above(mid) > at) lo = mid;
+        else hi = mid;
+    }
+    level = lo;
+    int left = at - above(lo + 1);   // which of the sequences that have this level
+#pragma unroll
+    for (int c = 0; c < kListed / 64; ++c) {
+        uint64_t has = __ballot(n[c] > lo);
+        const int k = __popcll(has);
+        if (left >= 0 && left < k) {
+            for (; left; --left) has &= has - 1;
+            const int l = __ffsll((unsigned long long)has) - 1;
+            seq = 64 * c + l;
+            levels = __builtin_amdgcn_readlane(n[c], l);
+            left = -1;
+        } else if (left >= 0) {
+            left -= k;
+        }
+    }
+    return true;
+}
+
 struct Block {
     int b, hq, hk, i0, split;
 };
-__device__ __forceinline__ Block block_of(const AttnArgs& a, int blocks, int rows) {
+// false: no rows here.
+__device__ __forceinline__ bool block_of(const AttnArgs& a, int blocks, int rows, Block& x) {
     const int group = a.heads / a.kv_heads;
-    const int per = blocks * a.batch * a.heads;   // workgroups of one split
-    Block x;
+    const int pairs = a.listed ? a.heads : a.batch * a.heads, per = blocks * pairs;   // workgroups of one split
     x.split = blockIdx.x / per;
     int blk, pair;
-    locate(blockIdx.x - x.split * per, blocks, a.batch * a.heads, group, a.causal, blk, pair);
-    x.b = pair / a.heads, x.hq = pair % a.heads, x.hk = x.hq / group, x.i0 = blk * rows;
-    return x;
+    locate(blockIdx.x - x.split * per, blocks, pairs, group, a.causal && !a.listed, blk, pair);
+    x.b = pair / a.heads, x.hq = pair % a.heads, x.hk = x.hq / group;
+    if (a.listed) {
+        int levels;
+        if (!find_listed(a.q_start, a.q_tokens, a.q_len, a.batch, rows, blk, x.b, blk, levels)) return false;
+    }
+    x.i0 = blk * rows;
+    return true;
 }
 
 // Key tiles [first, end) of this workgroup's queries and split.
@@ -399,7 +461,8 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs
     using FT = Frag<T>;
     using F = typename FT::type;
     __shared__ __attribute__((aligned(1024))) char smem[SETS * 4 * G::BYTES];
-    const Block wg = block_of(a, blocks, 32 * W);
+    Block wg;
+    if (!block_of(a, blocks, 32 * W, wg)) return;
     const int b = wg.b, hq = wg.hq, hk = wg.hk, i0 = wg.i0;
     const Seq sq = sequence(a, b);
     if (i0 >= sq.q_rows) return;
@@ -560,7 +623,8 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
     using FT = Frag<T>;
     using F = typename FT::type;
     __shared__ __attribute__((aligned(1024))) char smem[SETS * 4 * G::BYTES];
-    const Block wg = block_of(a, blocks, 32 * W);
+    Block wg;
+    if (!block_of(a, blocks, 32 * W, wg)) return;
     const int b = wg.b, hq = wg.hq, hk = wg.hk, i0 = wg.i0;
     const Seq sq = sequence(a, b);
     if (i0 >= sq.q_rows) return;
@@ -682,9 +746,15 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dkv_kernel(AttnArgs a, 
     __shared__ __attribute__((aligned(1024))) char smem[SETS * 4 * G::BYTES];
     __shared__ __attribute__((aligned(16))) float stat[SETS][2][2][kTile];   // [set][buffer][L, D]
     int blk, pair;
-    const int per = blocks * a.batch * a.kv_heads, split = blockIdx.x / per;
-    locate(blockIdx.x - split * per, blocks, a.batch * a.kv_heads, 1, false, blk, pair);
-    const int b = pair / a.kv_heads, hk = pair % a.kv_heads, group = a.heads / a.kv_heads;
+    const int pairs = a.listed ? a.kv_heads : a.batch * a.kv_heads, per = blocks * pairs, split = blockIdx.x / per;
+    locate(blockIdx.x - split * per, blocks, pairs, 1, false, blk, pair);
+    const int hk = pair % a.kv_heads, group = a.heads / a.kv_heads;
+    int b = pair / a.kv_heads;
+    if (a.listed) {
+        int level, levels;
+        if (!find_listed(a.k_start, a.k_tokens, a.k_len, a.batch, 32 * W, blk, b, level, levels)) return;
+        blk = a.causal ? levels - 1 - level : level;   // the first keys of a causal sequence have the most queries
+    }
     const Seq sq = sequence(a, b);
     const int j0 = blk * 32 * W;
     if (j0 >= sq.k_rows) return;
@@ -953,7 +1023,8 @@ enum Kind { FORWARD, DQ, DKV };
 //    the work at their uneven end: 2048), of 32 steps at least. Forward, us,
 //    two sets against one: 76 / 104 (3500 tokens, 16 heads of 128), 83 / 101
 //    (4096); short ones 28 / 23 (8 x 512), 37 / 33 (4 x 1024). dK and dV with dQ: 946 / 1182 (8192
-//    tokens, 8 key heads), but 1095 / 1020 (4 x 4096, 16 key heads).
+//    tokens, 8 key heads), but 1095 / 1020 (4 x 4096, 16 key heads). A batch of
+//    8192 packed tokens, the longest sequence 4194: 80 / 110 at head_dim 64.
 //  - Plenty: eight wavefronts share each tile. Half the copies into LDS, which
 //    cost power, and the clock follows the power drawn: 277 us against 298 of
 //    four (forward, 8192 tokens), 521 / 534 (not causal); few ones are left
@@ -964,19 +1035,24 @@ Shape shape_of(const AttnArgs& x, Kind kind) {
     const bool keys = kind == DKV;
     const int splits = keys ? x.kv_splits : x.splits;
     const int64_t wgs = busy_blocks(x, keys) * splits, steps = block_steps(x, keys) / splits;
-    if (wgs <= 256 || (x.causal && wgs < (keys ? 2048 : 1024) && steps >= 32)) return W4S2;
+    const bool many = x.q_start && x.head_dim <= 64;   // two such workgroups a CU, and sequences uneven among themselves
+    if (wgs <= 256 || (x.causal && wgs < (keys || many ? 2048 : 1024) && steps >= 32)) return W4S2;
     return wgs >= 1024 ? W8S1 : W4S1;
 }
 
 template <class T, int DB, int W, int SETS>
-void launch_shape(Kind kind, const AttnArgs& x, hipStream_t s) {
-    const int blocks = (int)row_blocks(kind == DKV ? x.k_len : x.q_len, 32 * W);
-    const int64_t grid = (int64_t)blocks * x.batch * (kind == DKV ? (int64_t)x.kv_heads * x.kv_splits
-                                                                  : (int64_t)x.heads * x.splits);
+void launch_shape(Kind kind, AttnArgs x, hipStream_t s) {
+    const bool keys = kind == DKV;
+    int64_t blocks = row_blocks(keys ? x.k_len : x.q_len, 32 * W), sequences = x.batch;
+    // the list where it is shorter than a block of every sequence for each of the longest one's
+    const int64_t list = (keys ? x.k_tokens : x.q_tokens) / (32 * W) + x.batch;
+    x.listed = x.q_start && x.batch <= kListed && list < blocks * sequences;
+    if (x.listed) blocks = list, sequences = 1;
+    const int64_t grid = blocks * sequences * (keys ? (int64_t)x.kv_heads * x.kv_splits : (int64_t)x.heads * x.splits);
     const dim3 g((uint32_t)grid), n(SETS * 64 * W);
-    if (kind == FORWARD) attn_forward_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, blocks);
-    else if (kind == DQ) attn_dq_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, blocks);
-    else attn_dkv_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, blocks);
+    if (kind == FORWARD) attn_forward_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, (int)blocks);
+    else if (kind == DQ) attn_dq_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, (int)blocks);
+    else attn_dkv_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, (int)blocks);
 }
 
 template <class T, int DB>

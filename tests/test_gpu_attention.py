@@ -191,6 +191,28 @@ def test_packed_sequences_on_long_contexts():
         a, c = a + m, c + n
 
 
+@pytest.mark.parametrize("count", [64, 65, 200, 256, 300])
+def test_many_packed_sequences(count):
+    """More sequences than a wavefront has lanes, and than the list of blocks takes."""
+    torch = _torch()
+    print(f"attention packed {count}", flush=True)
+    rng = np.random.default_rng(count)
+    lens = [int(x) for x in rng.integers(0, 9, count)]
+    lens[count // 2], lens[-1], lens[3] = 300, 140, 0
+    mk = lambda h: torch.randn(sum(lens), h, 32, device="cuda").bfloat16()  # noqa: E731
+    q, k, v, dout = mk(2), mk(1), mk(1), mk(2)
+    st = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    for causal in (True, False):
+        got = {n: np64(t) for n, t in run(q, k, v, dout, causal=causal, q_start=st, k_start=st, max_q=300, max_k=300).items()}
+        a = 0
+        for m in lens:
+            one = {x: got[x][a:a + m] for x in ("out", "dq", "dk", "dv")} | {"lse": got["lse"][:, a:a + m]}
+            if m:
+                check_sequence(np64(q[a:a + m]), np64(k[a:a + m]), np64(v[a:a + m]), np64(dout[a:a + m]), one, 32 ** -0.5,
+                               T.visible(m, m, causal), U["bf16"])
+            a += m
+
+
 def test_rising_scores_move_the_running_maximum():
     """Keys whose scores grow along the sequence raise the maximum in every tile."""
     torch = _torch()
