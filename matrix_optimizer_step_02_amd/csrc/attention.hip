@@ -234,17 +234,18 @@ struct Lane {
 };
 
 // B operand fragments of 32 rows in registers: row l % 32 (of n), k 16 s + 8 (l / 32) ..
+// What is outside is read from the zeros, so that all loads go out at once.
 template <class T, int DB>
 __device__ __forceinline__ void load_rows(typename Frag<T>::type (&f)[2 * DB], const char* base, int64_t token, int row,
                                           int n, int head_dim) {
     const int h = (threadIdx.x & 63) >> 5;
     const char* p = base + (int64_t)row * token;
+    const char* zero = (const char*)g_attn_zero;
 #pragma unroll
     for (int s = 0; s < 2 * DB; ++s) {
         const int c = 16 * s + 8 * h;
-        u32x4 w = {0, 0, 0, 0};
-        if (row < n && c < head_dim) w = *gptr((const u32x4*)(p + 2 * c));
-        f[s] = __builtin_bit_cast(typename Frag<T>::type, w);
+        const char* q = row < n && c < head_dim ? p + 2 * c : zero;
+        f[s] = __builtin_bit_cast(typename Frag<T>::type, *gptr((const u32x4*)q));
     }
 }
 
@@ -1001,18 +1002,20 @@ int64_t block_steps(const AttnArgs& x, bool keys) {
     return (n + kTile - 1) / kTile * (keys ? x.heads / x.kv_heads : 1);
 }
 
-// Parts to split a block's steps into, over workgroups: enough for `fill`
-// workgroups, but at least eight steps each, so that the partial sums stay
-// below what is read. One workgroup a CU; two for the keys of a causal
-// sequence, whose blocks are uneven (4096 tokens, 16 / 8 heads of 128: dK and
-// dV 232 us without, 185 with two). Two for its queries gained nothing (46
-// against 42 us, 2048 tokens).
+// Parts to split a block's steps into, over workgroups: enough for one on each
+// CU, but at least eight steps each, so that the partial sums stay below what
+// is read. Twice as many for the keys of a causal sequence, whose blocks are
+// uneven, if 32 steps are left to each (dK and dV of 4096 tokens, 16 / 8 heads
+// of 128: 232 us without, 181 with; 4 x 1024: 69 and 87). For its queries
+// twice as many gained nothing (46 against 42 us, 2048 tokens).
 int splits_of(const AttnArgs& x, bool keys) {
     const int64_t wgs = busy_blocks(x, keys), steps = block_steps(x, keys);
     if (wgs == 0) return 1;
-    int64_t s = (keys && x.causal ? 512 : 256) / wgs;
+    int64_t s = 256 / wgs;
     if (s > steps / 8) s = steps / 8;
-    return (int)(s < 1 ? 1 : s > 32 ? 32 : s);
+    if (s < 1) s = 1;
+    if (keys && x.causal && wgs * s <= 256 && steps >= 64 * s) s *= 2;
+    return (int)(s > 32 ? 32 : s);
 }
 
 enum Kind { FORWARD, DQ, DKV };

@@ -11,7 +11,6 @@ raise before anything is launched.
 
 from __future__ import annotations
 
-from dataclasses import dataclass
 from typing import NamedTuple, Optional
 
 import torch
@@ -25,8 +24,7 @@ _HALF = {torch.bfloat16: native.OPT_BF16, torch.float16: native.OPT_F16}
 _DTYPE = {torch.float32: native.OPT_F32, torch.bfloat16: native.OPT_BF16, torch.float16: native.OPT_F16}
 
 
-@dataclass(frozen=True)
-class Rng:
+class Rng(NamedTuple):
     """Where dropout's random bits come from: the same (seed, offset) give the
     same mask. ``device_offset``: an int64 tensor of one element added to
     offset on the device, for a step counter that a replayed graph reads."""
