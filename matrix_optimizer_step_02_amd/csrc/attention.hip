@@ -738,9 +738,11 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
 // heads of the group; the steps are (head, query tile). A lane owns one key.
 // The keys' accumulators (128 registers at head_dim 128) and operands (64)
 // leave little of the 256 registers that two wavefronts a SIMD have, so the
-// addresses are computed where they are used.
+// addresses are computed where they are used. At head_dim <= 64 a workgroup of
+// four is held to 168 registers, three wavefronts a SIMD: 68 us against 78 (6 x
+// 1000 tokens, 16 heads of 64).
 template <class T, int DB, int W, int SETS>
-__global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dkv_kernel(AttnArgs a, int blocks) {
+__global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) void attn_dkv_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
     using FT = Frag<T>;
     using F = typename FT::type;
@@ -1022,25 +1024,28 @@ enum Kind { FORWARD, DQ, DKV };
 
 // Wavefronts and sets of a workgroup. `wgs`: workgroups of 128 rows with work.
 //  - Up to one a CU: two sets. Also while there are few and uneven ones, the
-//    longest of which would run on alone: causal, below 1024 (keys, with twice
-//    the work at their uneven end: 2048), of 32 steps at least. Forward, us,
-//    two sets against one: 76 / 104 (3500 tokens, 16 heads of 128), 83 / 101
-//    (4096); short ones 28 / 23 (8 x 512), 37 / 33 (4 x 1024). dK and dV with dQ: 946 / 1182 (8192
-//    tokens, 8 key heads), but 1095 / 1020 (4 x 4096, 16 key heads). A batch of
-//    8192 packed tokens, the longest sequence 4194: 80 / 110 at head_dim 64.
+//    longest of which would run on alone: causal, below 1024, of 32 steps at
+//    least. Forward, us, two sets against one: 76 / 104 (3500 tokens, 16 heads
+//    of 128), 83 / 101 (4096), but 37 / 33 (4 x 1024), 327 / 287 (4 x 4096).
+//    dK and dV with dQ: 946 / 1182 (8192 tokens, 8 key heads), but 440 / 428
+//    (2 x 4096, 16 of 96). The forward pass of packed sequences, which are
+//    uneven among themselves, up to 2048 where two such workgroups fit a CU:
+//    77 / 105 (8192 tokens, the longest sequence 4194, 16 heads of 64).
 //  - Plenty: eight wavefronts share each tile. Half the copies into LDS, which
 //    cost power, and the clock follows the power drawn: 277 us against 298 of
 //    four (forward, 8192 tokens), 521 / 534 (not causal); few ones are left
-//    with a part-filled last round: 51 / 46 (6 x 1000, 16 heads of 64).
-//  - Else one set of four, two workgroups a CU.
+//    with a part-filled last round: 51 / 46 (6 x 1000, 16 heads of 64). Not
+//    for the keys at head_dim <= 64, where three workgroups of four fit a CU:
+//    1072 / 1026.
+//  - Else one set of four.
 enum Shape { W4S2, W4S1, W8S1 };
 Shape shape_of(const AttnArgs& x, Kind kind) {
-    const bool keys = kind == DKV;
+    const bool keys = kind == DKV, narrow = x.head_dim <= 64;
     const int splits = keys ? x.kv_splits : x.splits;
     const int64_t wgs = busy_blocks(x, keys) * splits, steps = block_steps(x, keys) / splits;
-    const bool many = x.q_start && x.head_dim <= 64;   // two such workgroups a CU, and sequences uneven among themselves
-    if (wgs <= 256 || (x.causal && wgs < (keys || many ? 2048 : 1024) && steps >= 32)) return W4S2;
-    return wgs >= 1024 ? W8S1 : W4S1;
+    const int64_t few = x.q_start && narrow && kind == FORWARD ? 2048 : 1024;
+    if (wgs <= 256 || (x.causal && wgs < few && steps >= 32)) return W4S2;
+    return wgs >= 1024 && !(keys && narrow) ? W8S1 : W4S1;
 }
 
 template <class T, int DB, int W, int SETS>
