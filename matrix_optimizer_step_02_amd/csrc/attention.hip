@@ -948,7 +948,9 @@ opt_status check_attention(const opt_attention_desc* a) {
     for (const int32_t* p : {a->q_start, a->k_start, a->q_lens, a->k_lens})
         if (!train_aligned(p, 4)) return fail(OPT_EINVAL, "an offset or length array is not aligned to 4 bytes");
     if (a->q_start && (a->q_tokens < 0 || a->k_tokens < 0)) return fail(OPT_EINVAL, "negative q_tokens or k_tokens");
-    const int64_t longest = a->q_len > a->k_len ? a->q_len : a->k_len;
+    if (a->q_start && (a->q_tokens > int64_t(1) << 40 || a->k_tokens > int64_t(1) << 40))
+        return fail(OPT_EUNSUPPORTED, "too many packed tokens");
+    const double longest = a->q_len > a->k_len ? a->q_len : a->k_len;
     if ((longest / kJoinRows + 1) * a->batch * a->heads > INT32_MAX) return fail(OPT_EUNSUPPORTED, "too many row blocks");
     return OPT_OK;
 }
