@@ -56,7 +56,7 @@ typedef struct {
     int32_t dtype;            /* OPT_BF16 or OPT_F16: every tensor but lse */
     int32_t batch, heads, kv_heads;   /* heads a multiple of kv_heads */
     int32_t head_dim;         /* a multiple of 8, at most 128 */
-    int32_t q_len, k_len;     /* tokens per sequence; packed: the longest sequence */
+    int32_t q_len, k_len;     /* tokens per sequence; packed: the longest sequence; at most 2^29 */
     int32_t causal, window;   /* window: 0 for none */
     float scale;
     /* Packed sequences: batch + 1 ascending device offsets into the token

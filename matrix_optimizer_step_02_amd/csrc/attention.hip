@@ -63,7 +63,7 @@ struct AttnArgs {
     const int32_t *q_start, *k_start, *q_lens, *k_lens;
     int64_t q_tokens, k_tokens;   // rows of lse and delta; packed: the token axes
     int32_t batch, heads, kv_heads, head_dim, q_len, k_len, causal, window, splits, kv_splits;
-    int32_t listed;   // packed: row blocks are found by their place in a list (block_of_list)
+    int32_t listed;   // packed: row blocks are found by their place in a list (find_listed)
     float scale;
 };
 
@@ -311,18 +311,21 @@ struct Sight {
 // Workgroups come in three shapes: four wavefronts (128 rows), eight (256
 // rows) that share the same tiles, or two sets of four (128 rows) with LDS
 // tiles of their own, which take the tiles in turn and join their sums through
-// LDS. Registers leave room for two wavefronts a SIMD: two workgroups a CU of
-// the first shape, one of the others. Where the launch has fewer workgroups
-// than the GPU has CUs (few queries on a long context), the tiles are also
-// split over workgroups, which leave fp32 partial sums in the workspace for a
-// second kernel to join: 509 queries on 8192 keys, 16 / 8 heads of 128, take
-// 49 + 5 us in place of 215. The host chooses (shape_of, splits_of).
+// LDS. Registers leave room for two wavefronts a SIMD (three for dK and dV at
+// head_dim <= 64): two workgroups a CU of the first shape, one of the others.
+// Where the launch has fewer workgroups than the GPU has CUs (few queries on a
+// long context), the tiles are also split over workgroups, which leave fp32
+// partial sums in the workspace for a second kernel to join: 509 queries on
+// 8192 keys, 16 / 8 heads of 128, take 49 + 5 us in place of 215. The host
+// chooses (shape_of, splits_of).
+
 // Row blocks of packed sequences, as a list without the blocks that a shorter
 // sequence lacks (a launch that covers the longest one for each sequence would
-// be mostly of those; 4 to 12 % at 13 sequences of 8192 tokens): entry `at` of the list of all (sequence, level) with
-// level below the sequence's number of blocks, highest level first, so that
-// the longest sequences' far blocks come first. Each wavefront finds it by
-// bisection over the levels, a sequence per lane. false: past the list's end.
+// be mostly of those: 4 to 12 % of the time at 13 sequences of 8192 tokens).
+// Finds entry `at` of the list of all (sequence, level) with level below the
+// sequence's number of blocks, highest level first, so that the longest
+// sequences' far blocks come first: a bisection over the levels in each
+// wavefront, a sequence per lane. false: past the list's end.
 constexpr int kListed = 256;   // sequences at most: four turns of 64 per step
 __device__ __forceinline__ bool find_listed(const int32_t* start, int64_t tokens, int most, int batch, int rows, int at,
                                             int& seq, int& level, int& levels) {
@@ -939,7 +942,8 @@ opt_status check_attention(const opt_attention_desc* a) {
         return fail(OPT_EINVAL, "heads must be a positive multiple of kv_heads");
     if (a->head_dim < 8 || a->head_dim % 8) return fail(OPT_EINVAL, "head_dim must be a positive multiple of 8");
     if (a->head_dim > 128) return fail(OPT_EUNSUPPORTED, "head_dim must be <= 128");
-    if (a->q_len > (1 << 30) || a->k_len > (1 << 30)) return fail(OPT_EUNSUPPORTED, "sequence too long");
+    // the sums of a length, an offset between lengths and a window fit in 32 bits
+    if (a->q_len > (1 << 29) || a->k_len > (1 << 29)) return fail(OPT_EUNSUPPORTED, "sequence too long");
     if (a->window < 0) return fail(OPT_EINVAL, "window must be >= 0");
     if (a->window > 0 && !a->causal) return fail(OPT_EUNSUPPORTED, "a window needs causal");
     if (!(a->scale > 0.f) || !(a->scale < INFINITY)) return fail(OPT_EINVAL, "scale must be positive and finite");
@@ -985,7 +989,8 @@ AttnArgs attn_args(const opt_attention_desc* a) {
     x.q_tokens = a->q_start ? a->q_tokens : (int64_t)a->batch * a->q_len;
     x.k_tokens = a->q_start ? a->k_tokens : (int64_t)a->batch * a->k_len;
     x.batch = a->batch, x.heads = a->heads, x.kv_heads = a->kv_heads, x.head_dim = a->head_dim;
-    x.q_len = a->q_len, x.k_len = a->k_len, x.causal = a->causal != 0, x.window = a->window, x.scale = a->scale;
+    x.q_len = a->q_len, x.k_len = a->k_len, x.causal = a->causal != 0, x.scale = a->scale;
+    x.window = a->window < a->k_len ? a->window : 0;   // as long as the keys: it hides none
     return x;
 }
 

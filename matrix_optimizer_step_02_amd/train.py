@@ -2,8 +2,8 @@
 dropout and the clipped policy loss, each with its backward pass.
 
 Functions check their tensors, allocate what they return and call the C entry
-points of include/matopt_train.h on the given stream (default: the current
-one). There is no autograd graph: a backward function is called with what its
+points of include/matopt_train.h on the current stream, or on the one given as
+``stream``. There is no autograd graph: a backward function is called with what its
 forward function returned, and its results are ordinary tensors (a weight's
 gradient goes into the G of a RotatedAdamGroup). All shapes and argument errors
 raise before anything is launched.
@@ -11,6 +11,7 @@ raise before anything is launched.
 
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -40,24 +41,25 @@ class Rng(NamedTuple):
         return native.opt_rng(self.seed & m, self.offset & m, d.data_ptr() if d is not None else 0)
 
 
-def _stream(dev, stream):
-    """(handle, stream object when it is not the current one). The raw handle
-    of the current stream: the Stream object around it costs 2 us a call."""
+def _streamed(fn):
+    """Gives fn a ``stream`` argument. Everything of the call happens there:
+    the kernels, the copies it may need, and the allocation of what it returns
+    (so that no memory is taken that the current stream may still be using)."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _stream(dev):
+    """The raw handle of the current stream: the Stream object around it costs
+    2 us a call."""
     if dev.type != "cuda":
         raise ValueError("tensors must live on a HIP device")
-    cur = torch._C._cuda_getCurrentRawStream(dev.index)
-    if stream is None or stream.cuda_stream == cur:
-        return cur, None
-    return stream.cuda_stream, stream
-
-
-def _used(other, *tensors):
-    """Tensors allocated here but used on another stream than the current one
-    must not be handed out again before that stream is done with them."""
-    if other is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(other)
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _is(t, name, device, dtype, shape=None):
@@ -158,8 +160,9 @@ def _bytes(like, n):
     return like.new_empty(n, dtype=torch.uint8) if n else None
 
 
+@_streamed
 def attention_forward(q, k, v, *, causal=False, window=0, scale=None, q_start=None, k_start=None, max_q=None,
-                      max_k=None, q_lens=None, k_lens=None, out=None, stream=None):
+                      max_k=None, q_lens=None, k_lens=None, out=None):
     """(out, lse) of softmax(scale q k^T) v. q is (batch, tokens, heads, dim);
     k and v (batch, tokens, kv_heads, dim); any strides with a contiguous last
     axis. Packed sequences: q, k, v without the batch axis, q_start and k_start
@@ -167,20 +170,19 @@ def attention_forward(q, k, v, *, causal=False, window=0, scale=None, q_start=No
     batches: q_lens, k_lens int32 lengths. lse is fp32, (heads, all query
     tokens). scale defaults to dim^-1/2."""
     a, dev, per_row = _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens)
-    st, other = _stream(dev, stream)
+    st = _stream(dev)
     o = _out(out, "out", q, dev)
     lse = q.new_empty(per_row, dtype=torch.float32)
     n = native.opt_attention_workspace_size(a, 0)
     ws = _bytes(q, n)
     native.opt_attention_forward(a, _bhtd(q, "q"), _bhtd(k, "k"), _bhtd(v, "v"), _bhtd(o, "out"), lse.data_ptr(),
                                  ws.data_ptr() if n else 0, n, st)
-    if other is not None:
-        _used(other, o if out is None else None, lse, ws)
     return o, lse
 
 
+@_streamed
 def attention_backward(dout, q, k, v, out, lse, *, causal=False, window=0, scale=None, q_start=None, k_start=None,
-                       max_q=None, max_k=None, q_lens=None, k_lens=None, dq=None, dk=None, dv=None, stream=None):
+                       max_q=None, max_k=None, q_lens=None, k_lens=None, dq=None, dk=None, dv=None):
     """(dq, dk, dv) from the output's gradient and what attention_forward took
     and returned. dq, dk, dv may be given, for instance as views of one
     projection's gradient."""
@@ -193,16 +195,13 @@ def attention_backward(dout, q, k, v, out, lse, *, causal=False, window=0, scale
         raise ValueError("lse must be contiguous")
     if dout.stride(-1) != 1:   # an expanded gradient has stride 0
         dout = dout.contiguous()
-    st, other = _stream(dev, stream)
+    st = _stream(dev)
     gq, gk, gv = _out(dq, "dq", q, dev), _out(dk, "dk", k, dev), _out(dv, "dv", v, dev)
     n = native.opt_attention_workspace_size(a, 1)
     ws = _bytes(q, n)
     native.opt_attention_backward(a, _bhtd(dout, "dout"), _bhtd(q, "q"), _bhtd(k, "k"), _bhtd(v, "v"),
                                   _bhtd(out, "out"), lse.data_ptr(), _bhtd(gq, "dq"), _bhtd(gk, "dk"),
                                   _bhtd(gv, "dv"), ws.data_ptr() if n else 0, n, st)
-    if other is not None:
-        _used(other, dout, None if dq is not None else gq, None if dk is not None else gk,
-              None if dv is not None else gv, ws)
     return gq, gk, gv
 
 
@@ -243,7 +242,8 @@ def _p_rng(p, rng):
     return rng.c() if rng is not None and p > 0 else None
 
 
-def dropout(x, p, rng, *, residual=None, out=None, stream=None):
+@_streamed
+def dropout(x, p, rng, *, residual=None, out=None):
     """residual + dropout(x) (no residual: dropout(x)); out may be x or
     residual. The mask depends on rng and on an element's position in x
     (leading axes as rows, the last axis as columns)."""
@@ -256,22 +256,22 @@ def dropout(x, p, rng, *, residual=None, out=None, stream=None):
     if residual is not None:
         _is(residual, "residual", dev, x.dtype, x.shape)
         rp, ldr = _rows(residual, "residual")
-    st, other = _stream(dev, stream)
+    st = _stream(dev)
     native.opt_dropout(rows, cols, dt, xp, ldx, rp, ldr, yp, ldy, p, bits, st)
-    if other is not None:
-        _used(other, y if out is None else None)
     return y
 
 
-def dropout_backward(dy, p, rng, *, out=None, stream=None):
+@_streamed
+def dropout_backward(dy, p, rng, *, out=None):
     """dropout's gradient with respect to x (the residual's is dy itself)."""
-    return dropout(dy, p, rng, out=out, stream=stream)
+    return dropout(dy, p, rng, out=out)
 
 
 # ------------------------------------------------------------- layer norm ----
 
 
-def layer_norm_forward(x, weight, bias=None, *, eps=1e-5, residual=None, p=0.0, rng=None, out=None, stream=None):
+@_streamed
+def layer_norm_forward(x, weight, bias=None, *, eps=1e-5, residual=None, p=0.0, rng=None, out=None):
     """(y, h, mean, rstd): h = residual + dropout(x) in the residual's type,
     y its norm over the last axis in x's type. Without residual and dropout h
     is x. weight and bias are fp32."""
@@ -292,15 +292,14 @@ def layer_norm_forward(x, weight, bias=None, *, eps=1e-5, residual=None, p=0.0, 
         hp, ldh = h.data_ptr(), cols
     lead = x.shape[:-1]
     mean, rstd = weight.new_empty(lead), weight.new_empty(lead)
-    st, other = _stream(dev, stream)
+    st = _stream(dev)
     native.opt_layer_norm_forward(rows, cols, dt, xp, ldx, hdt, rp, ldr, wp, bp, eps, p, bits, yp, ldy, hp, ldh,
                                   mean.data_ptr(), rstd.data_ptr(), st)
-    if other is not None:
-        _used(other, y if out is None else None, h if hp else None, mean, rstd)
     return y, h, mean, rstd
 
 
-def layer_norm_backward(dy, h, weight, mean, rstd, *, dh=None, p=0.0, rng=None, residual_grad=True, stream=None):
+@_streamed
+def layer_norm_backward(dy, h, weight, mean, rstd, *, dh=None, p=0.0, rng=None, residual_grad=True):
     """(dx, dres, dweight, dbias) from y's gradient and what
     layer_norm_forward returned; dh is the gradient that reaches h past the
     norm. dres, h's gradient, goes to the residual; without dropout and in the
@@ -334,12 +333,10 @@ def layer_norm_backward(dy, h, weight, mean, rstd, *, dh=None, p=0.0, rng=None, 
     n = native.opt_layer_norm_workspace_size(rows, cols)
     ws = _bytes(dy, n)
     dw, db = weight.new_empty(cols), weight.new_empty(cols)
-    st, other = _stream(dev, stream)
+    st = _stream(dev)
     native.opt_layer_norm_backward(rows, cols, dt, dyp, lddy, hdt, hp, ldh, dhp, lddh, wp, mean.data_ptr(),
                                    rstd.data_ptr(), p, bits, dx.data_ptr(), cols, drp, lddr, dw.data_ptr(),
                                    db.data_ptr(), ws.data_ptr() if n else 0, n, st)
-    if other is not None:
-        _used(other, dx, dres, dw, db, ws)
     return dx, dres, dw, db
 
 
@@ -377,26 +374,26 @@ def _policy_rows(tp, dev, n, old_logp, ref_logp, advantage, weight, kl_coef):
                                   _vector(advantage, "advantage", dev, n), _vector(weight, "weight", dev, n))
 
 
+@_streamed
 def policy_loss_forward(logits, target, old_logp, advantage, weight, *, ref_logp=None, clip_low=0.2, clip_high=0.2,
-                        kl_coef=0.0, logit_scale=1.0, stream=None):
+                        kl_coef=0.0, logit_scale=1.0):
     """PolicyForward of the clipped policy loss with a KL term to a reference
     policy: per row of logits (rows, vocab) a target token, its log
     probability under the sampling and the reference policy, an advantage and
     a weight (which holds the normalisation; 0 leaves the row out)."""
     a, dev, lp, tp = _policy(logits, target, clip_low, clip_high, kl_coef, logit_scale)
     rows = _policy_rows(tp, dev, a.rows, old_logp, ref_logp, advantage, weight, kl_coef)
-    st, other = _stream(dev, stream)
+    st = _stream(dev)
     n = native.opt_policy_loss_workspace_size(a)
     ws = _bytes(logits, n)
     loss, logp, lse, slope = (weight.new_empty(s) for s in ((), a.rows, a.rows, a.rows))
     native.opt_policy_loss_forward(a, lp, rows, loss.data_ptr(), logp.data_ptr(), lse.data_ptr(), slope.data_ptr(),
                                    ws.data_ptr() if n else 0, n, st)
-    if other is not None:
-        _used(other, loss, logp, lse, slope, ws)
     return PolicyForward(loss, logp, lse, slope)
 
 
-def policy_loss_backward(logits, target, fwd, *, grad=None, logit_scale=1.0, out=None, stream=None):
+@_streamed
+def policy_loss_backward(logits, target, fwd, *, grad=None, logit_scale=1.0, out=None):
     """dlogits from policy_loss_forward's result; grad: the loss's gradient, a
     scalar tensor on the device (None: 1). out may be logits."""
     a, dev, lp, tp = _policy(logits, target, 0.2, 0.2, 0.0, logit_scale)
@@ -407,15 +404,14 @@ def policy_loss_backward(logits, target, fwd, *, grad=None, logit_scale=1.0, out
     if grad is not None:
         _is(grad, "grad", dev, torch.float32, ())
         gp = grad.data_ptr()
-    st, other = _stream(dev, stream)
+    st = _stream(dev)
     native.opt_policy_loss_backward(a, lp, tp, ep, sp, gp, dp, ldd, st)
-    if other is not None:
-        _used(other, d if out is None else None)
     return d
 
 
+@_streamed
 def policy_loss_step(logits, target, old_logp, advantage, weight, *, ref_logp=None, clip_low=0.2, clip_high=0.2,
-                     kl_coef=0.0, logit_scale=1.0, grad=1.0, out=None, stream=None):
+                     kl_coef=0.0, logit_scale=1.0, grad=1.0, out=None):
     """(loss, logp, dlogits) in one pass over the logits, for a loss that is
     the last operator: grad, the loss's own gradient, is a number. out may be
     logits."""
@@ -423,12 +419,10 @@ def policy_loss_step(logits, target, old_logp, advantage, weight, *, ref_logp=No
     rows = _policy_rows(tp, dev, a.rows, old_logp, ref_logp, advantage, weight, kl_coef)
     d = _out(out, "out", logits, dev)
     dp, ldd = _rows(d, "out")
-    st, other = _stream(dev, stream)
+    st = _stream(dev)
     logp, loss = weight.new_empty(a.rows), weight.new_empty(())
     n = native.opt_policy_loss_workspace_size(a)
     ws = _bytes(logits, n)
     native.opt_policy_loss_step(a, lp, rows, grad, loss.data_ptr(), logp.data_ptr(), dp, ldd,
                                 ws.data_ptr() if n else 0, n, st)
-    if other is not None:
-        _used(other, d if out is None else None, logp, loss, ws)
     return loss, logp, d

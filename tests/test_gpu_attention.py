@@ -308,6 +308,32 @@ def test_expanded_gradient():
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+def test_expanded_gradient_on_another_stream():
+    """The copy that an expanded gradient needs is made on the stream of the call."""
+    torch, train = _torch(), _train()
+    print("attention expanded, stream", flush=True)
+    q = torch.randn(2, 1500, 4, 64, device="cuda").bfloat16()
+    out, lse = train.attention_forward(q, q, q)
+    one = torch.ones((), device="cuda", dtype=torch.bfloat16).expand(q.shape)
+    want = train.attention_backward(one, q, q, q, out, lse)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    busy = torch.randn(4096, 4096, device="cuda")
+    for _ in range(10):
+        busy = busy @ busy / 64   # the current stream is not done when the call is made
+    got = train.attention_backward(one, q, q, q, out, lse, stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_windows_past_the_keys():
+    dense(1, 70, 100, 2, 1, 64, causal=True, window=100, seed=8)
+    torch, train = _torch(), _train()
+    q = torch.randn(1, 90, 1, 64, device="cuda").bfloat16()
+    assert torch.equal(train.attention_forward(q, q, q, causal=True, window=2 ** 31 - 1)[0],
+                       train.attention_forward(q, q, q, causal=True)[0])
+
+
 def test_bad_offsets_stay_inside():
     """Offsets that descend or leave the token axis give defined, in-bounds work: no row outside is written."""
     torch, train = _torch(), _train()
