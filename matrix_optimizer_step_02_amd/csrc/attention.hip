@@ -424,6 +424,16 @@ __device__ __forceinline__ void store_part(const f32x16 (&acc)[DB], float* row) 
         }
 }
 
+// A row that sees nothing holds sums of 0 times what it does not see, which
+// are NaN where that is not finite.
+template <int DB>
+__device__ __forceinline__ void clear(f32x16 (&acc)[DB]) {
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
+}
+
 // Hands accumulators (and two more values) from set 1 to set 0 through the
 // LDS of the tiles, which every wavefront has left: 64 (16 DB + 2) floats of
 // each wavefront.
@@ -572,6 +582,7 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs
         l = l * k0 + l1 * k1;
         m = mn;
     }
+    if (l == 0.f) clear(o);
     if (i >= sq.q_rows) return;
     if (a.splits > 1) {
         const int64_t row = part_row(a, wg.split, hq, sq.l0 + i);
@@ -730,6 +741,7 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
         if (set == 1) return;
         take<DB>(smem, wave, 1.f, 1.f, dq);
     }
+    if (hi <= lo) clear(dq);
     if (i >= sq.q_rows) return;
     if (a.splits > 1)
         store_part<DB>(dq, a.part + part_row(a, wg.split, hq, sq.l0 + i) * (32 * DB));
@@ -895,6 +907,7 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
                     else dk[d][4 * g + e] += x[e];
             }
     }
+    if (hi <= lo) clear(dk), clear(dv);
     if (j >= sq.k_rows) return;
     if (a.kv_splits > 1) {
         const int64_t row = (((int64_t)split * a.kv_heads + hk) * a.k_tokens + (a.q_start ? sq.k0 : (int64_t)b * a.k_len) + j) * (32 * DB);

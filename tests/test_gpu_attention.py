@@ -275,6 +275,35 @@ def test_padding_is_never_read(causal):
             assert (got["dk"][b] == 0).all() and (got["dv"][b] == 0).all()
 
 
+@pytest.mark.parametrize("tokens", [1, 2])   # 1: one workgroup's rows; 2: workgroups of two sets and splits
+def test_rows_and_keys_that_see_nothing_among_values_that_are_not_finite(tokens):
+    """Rows without a key, queries past their length and keys without a query
+    share tiles with values that are not finite."""
+    torch, train = _torch(), _train()
+    print("attention nothing visible", tokens, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(14)
+    mk = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    ti = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    nk = 8 if tokens == 1 else 700
+    nq = nk + 40                       # causal: the first 40 queries see no key
+    q, k, v, dout = mk(1, nq, 2, 64), mk(1, nk, 1, 64), mk(1, nk, 1, 64), mk(1, nq, 2, 64)
+    k[:, ::3], v[:, ::2] = float("nan"), float("inf")
+    got = run(q, k, v, dout, causal=True)
+    assert not got["out"][:, :40].any() and not got["dq"][:, :40].any()
+    assert got["lse"][:, :40].isneginf().all()
+    lens = [30, 0]                     # not causal: queries past 30 are padding, and a whole sequence of them
+    q, k, v, dout = mk(2, 60, 2, 64), mk(2, nk, 1, 64), mk(2, nk, 1, 64), mk(2, 60, 2, 64)
+    k[:, ::3], v[:, ::2] = float("inf"), float("nan")
+    got = run(q, k, v, dout, q_lens=ti(lens))
+    for b, n in enumerate(lens):
+        assert not got["out"][b, n:].any() and not got["dq"][b, n:].any()
+    q, k, v, dout = mk(1, 20, 2, 64), mk(1, nk + 60, 1, 64), mk(1, nk + 60, 1, 64), mk(1, 20, 2, 64)
+    q[:, ::3], dout[:, ::2] = float("nan"), float("inf")
+    out, lse = train.attention_forward(q, k, v, causal=True, window=4)   # the last 23 keys have queries
+    _, dk, dv = train.attention_backward(dout, q, k, v, out, lse, causal=True, window=4)
+    assert not dk[:, :-23].any() and not dv[:, :-23].any()
+
+
 def test_strided_views_and_given_outputs():
     """q, k, v are views of one projection, their gradients views of another, and out is head-major."""
     torch, train = _torch(), _train()
