@@ -63,6 +63,7 @@ struct AttnArgs {
     const int32_t *q_start, *k_start, *q_lens, *k_lens;
     int64_t q_tokens, k_tokens;   // rows of lse and delta; packed: the token axes
     int32_t batch, heads, kv_heads, head_dim, q_len, k_len, causal, window, splits, kv_splits;
+    uint32_t first;   // of the workgroups, this launch's first
     int32_t listed;   // packed: row blocks are found by their place in a list (find_listed)
     float scale;
 };
@@ -379,9 +380,10 @@ struct Block {
 __device__ __forceinline__ bool block_of(const AttnArgs& a, int blocks, int rows, Block& x) {
     const int group = a.heads / a.kv_heads;
     const int pairs = a.listed ? a.heads : a.batch * a.heads, per = blocks * pairs;   // workgroups of one split
-    x.split = blockIdx.x / per;
+    const int at = a.first + blockIdx.x;
+    x.split = at / per;
     int blk, pair;
-    locate(blockIdx.x - x.split * per, blocks, pairs, group, a.causal && !a.listed, blk, pair);
+    locate(at - x.split * per, blocks, pairs, group, a.causal && !a.listed, blk, pair);
     x.b = pair / a.heads, x.hq = pair % a.heads, x.hk = x.hq / group;
     if (a.listed) {
         int levels;
@@ -764,8 +766,8 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
     __shared__ __attribute__((aligned(1024))) char smem[SETS * 4 * G::BYTES];
     __shared__ __attribute__((aligned(16))) float stat[SETS][2][2][kTile];   // [set][buffer][L, D]
     int blk, pair;
-    const int pairs = a.listed ? a.kv_heads : a.batch * a.kv_heads, per = blocks * pairs, split = blockIdx.x / per;
-    locate(blockIdx.x - split * per, blocks, pairs, 1, false, blk, pair);
+    const int pairs = a.listed ? a.kv_heads : a.batch * a.kv_heads, per = blocks * pairs, wg = a.first + blockIdx.x, split = wg / per;
+    locate(wg - split * per, blocks, pairs, 1, false, blk, pair);
     const int hk = pair % a.kv_heads, group = a.heads / a.kv_heads;
     int b = pair / a.kv_heads;
     if (a.listed) {
@@ -967,8 +969,10 @@ opt_status check_attention(const opt_attention_desc* a) {
     if (a->q_start && (a->q_tokens < 0 || a->k_tokens < 0)) return fail(OPT_EINVAL, "negative q_tokens or k_tokens");
     if (a->q_start && (a->q_tokens > int64_t(1) << 40 || a->k_tokens > int64_t(1) << 40))
         return fail(OPT_EUNSUPPORTED, "too many packed tokens");
+    // workgroups of all launches are counted in 31 bits
     const double longest = a->q_len > a->k_len ? a->q_len : a->k_len;
-    if ((longest / kJoinRows + 1) * a->batch * a->heads > INT32_MAX) return fail(OPT_EUNSUPPORTED, "too many row blocks");
+    if ((longest / kJoinRows + 1) * a->batch * a->heads > INT32_MAX)
+        return fail(OPT_EUNSUPPORTED, "too many row blocks");
     return OPT_OK;
 }
 
@@ -1002,8 +1006,10 @@ AttnArgs attn_args(const opt_attention_desc* a) {
     x.q_tokens = a->q_start ? a->q_tokens : (int64_t)a->batch * a->q_len;
     x.k_tokens = a->q_start ? a->k_tokens : (int64_t)a->batch * a->k_len;
     x.batch = a->batch, x.heads = a->heads, x.kv_heads = a->kv_heads, x.head_dim = a->head_dim;
-    x.q_len = a->q_len, x.k_len = a->k_len, x.causal = a->causal != 0, x.scale = a->scale;
-    x.window = a->window < a->k_len ? a->window : 0;   // as long as the keys: it hides none
+    x.q_len = a->q_start && a->q_tokens < a->q_len ? (int32_t)a->q_tokens : a->q_len;   // no sequence is longer than all
+    x.k_len = a->q_start && a->k_tokens < a->k_len ? (int32_t)a->k_tokens : a->k_len;
+    x.causal = a->causal != 0, x.scale = a->scale;
+    x.window = a->window < x.k_len ? a->window : 0;   // as long as the keys: it hides none
     return x;
 }
 
@@ -1077,10 +1083,14 @@ void launch_shape(Kind kind, AttnArgs x, hipStream_t s) {
     x.listed = x.q_start && x.batch <= kListed && list < blocks * sequences;
     if (x.listed) blocks = list, sequences = 1;
     const int64_t grid = blocks * sequences * (keys ? (int64_t)x.kv_heads * x.kv_splits : (int64_t)x.heads * x.splits);
-    const dim3 g((uint32_t)grid), n(SETS * 64 * W);
-    if (kind == FORWARD) attn_forward_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, (int)blocks);
-    else if (kind == DQ) attn_dq_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, (int)blocks);
-    else attn_dkv_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, (int)blocks);
+    constexpr int64_t most = most_blocks(SETS * 64 * W);
+    for (int64_t first = 0; first < grid; first += most) {
+        const dim3 g((uint32_t)(grid - first < most ? grid - first : most)), n(SETS * 64 * W);
+        x.first = (uint32_t)first;
+        if (kind == FORWARD) attn_forward_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, (int)blocks);
+        else if (kind == DQ) attn_dq_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, (int)blocks);
+        else attn_dkv_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, (int)blocks);
+    }
 }
 
 template <class T, int DB>

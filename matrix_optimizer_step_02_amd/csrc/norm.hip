@@ -149,10 +149,10 @@ __device__ __forceinline__ void store_g(T* p, int n, const float (&f)[8]) {
 template <class T, class H, int TPR, int VPT, bool EIGHTS>
 __global__ __launch_bounds__(norm_threads(TPR)) void norm_forward_kernel(
     uint32_t rows, int cols, const T* x, int64_t ldx, const H* res, int64_t ldr, const float* w, const float* b,
-    float eps, Drop d, T* y, int64_t ldy, H* h, int64_t ldh, float* mean_out, float* rstd_out) {
+    float eps, Drop d, T* y, int64_t ldy, H* h, int64_t ldh, float* mean_out, float* rstd_out, uint32_t first) {
     __shared__ float part[2][16];
     const int t = threadIdx.x % TPR;
-    const uint32_t row = blockIdx.x * (norm_threads(TPR) / TPR) + threadIdx.x / TPR;
+    const uint32_t row = first + blockIdx.x * (norm_threads(TPR) / TPR) + threadIdx.x / TPR;
     if (row >= rows) return;   // all threads of a row; where it takes the workgroup, none is past the rows
     float f[VPT][8];
     int n[VPT];
@@ -383,10 +383,14 @@ struct NormBwd {
 
 template <class T, class H, int TPR, int VPT, bool EIGHTS>
 void run(const NormFwd& a, hipStream_t s) {
-    constexpr int R = norm_threads(TPR) / TPR;
-    norm_forward_kernel<T, H, TPR, VPT, EIGHTS><<<dim3((a.rows + R - 1) / R), norm_threads(TPR), 0, s>>>(
-        a.rows, a.cols, (const T*)a.x, a.ldx, (const H*)a.res, a.ldr, a.w, a.b, a.eps, a.d, (T*)a.y, a.ldy, (H*)a.h,
-        a.ldh, a.mean, a.rstd);
+    constexpr int64_t R = norm_threads(TPR) / TPR, most = most_blocks(norm_threads(TPR));
+    for (int64_t first = 0; first < a.rows; first += most * R) {
+        const int64_t blocks = (a.rows - first + R - 1) / R;
+        norm_forward_kernel<T, H, TPR, VPT, EIGHTS>
+            <<<dim3((uint32_t)(blocks < most ? blocks : most)), norm_threads(TPR), 0, s>>>(
+                a.rows, a.cols, (const T*)a.x, a.ldx, (const H*)a.res, a.ldr, a.w, a.b, a.eps, a.d, (T*)a.y, a.ldy,
+                (H*)a.h, a.ldh, a.mean, a.rstd, (uint32_t)first);
+    }
 }
 template <class T, class H, int TPR, int VPT, bool EIGHTS>
 void run(const NormBwd& a, hipStream_t s) {

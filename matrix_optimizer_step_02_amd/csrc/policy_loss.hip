@@ -33,6 +33,7 @@ struct PolicyArgs {
     void* dlogits;                      // NULL: forward only
     int64_t ld, ldd;
     int32_t vocab, target_i64;
+    uint32_t first;                     // row of the launch's first workgroup
     float scale, lo, hi, kl, grad;
 };
 
@@ -117,7 +118,7 @@ __device__ __forceinline__ void row_loss(const PolicyArgs& a, uint32_t row, floa
 template <class T, int NT, int NV>
 __global__ __launch_bounds__(NT) void policy_row_kernel(PolicyArgs a) {
     __shared__ float part[2][NT / 64];
-    const uint32_t row = blockIdx.x;
+    const uint32_t row = a.first + blockIdx.x;
     const int tid = threadIdx.x, V = a.vocab, G = (V + 7) >> 3;
     const T* x = (const T*)a.logits + (int64_t)row * a.ld;
     T* dx = a.dlogits ? (T*)a.dlogits + (int64_t)row * a.ldd : nullptr;
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(NT) void policy_row_kernel(PolicyArgs a) {
 constexpr int kBackThreads = 256, kBackPer = 4;
 template <class T>
 __global__ __launch_bounds__(kBackThreads) void policy_backward_kernel(PolicyArgs a, const float* grad) {
-    const uint32_t row = blockIdx.x;
+    const uint32_t row = a.first + blockIdx.x;
     const int V = a.vocab, G = (V + 7) >> 3, g0 = blockIdx.y * (kBackThreads * kBackPer) + threadIdx.x;
     const T* x = (const T*)a.logits + (int64_t)row * a.ld;
     T* dx = (T*)a.dlogits + (int64_t)row * a.ldd;
@@ -268,7 +269,13 @@ constexpr int kLossThreads = 1024;
 __global__ __launch_bounds__(kLossThreads) void policy_sum_kernel(int64_t rows, const float* term, float* loss) {
     __shared__ double part[kLossThreads / 64];
     double s = 0.0;
-    for (int64_t r = threadIdx.x; r < rows; r += kLossThreads) s += gptr(term)[r];
+    for (int64_t r0 = threadIdx.x; r0 < rows; r0 += 8 * kLossThreads) {
+        float v[8];   // eight loads in flight
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = r0 + k * kLossThreads < rows ? gptr(term)[r0 + k * kLossThreads] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += v[k];
+    }
 #pragma unroll
     for (int m = 32; m; m >>= 1) s += __shfl_xor(s, m);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
@@ -281,19 +288,36 @@ __global__ __launch_bounds__(kLossThreads) void policy_sum_kernel(int64_t rows, 
 
 // Small vocabularies take small workgroups, so that several rows share a CU;
 // past what 1024 threads hold in 80 registers the row is streamed.
+template <class T, int NT, int NV>
+void launch_rows(PolicyArgs a, int64_t rows, hipStream_t s) {
+    constexpr int64_t most = most_blocks(NT);
+    for (int64_t r = 0; r < rows; r += most) {
+        a.first = (uint32_t)r;
+        policy_row_kernel<T, NT, NV><<<dim3((uint32_t)(rows - r < most ? rows - r : most)), NT, 0, s>>>(a);
+    }
+}
 template <class T>
 void launch_rows(const PolicyArgs& a, int64_t rows, hipStream_t s) {
-    const dim3 grid((uint32_t)rows);
     const int64_t v = a.vocab;
     constexpr int K = 4 / sizeof(T);   // logits per register
-    if (v <= 8 * 256 * 2) policy_row_kernel<T, 256, 2><<<grid, 256, 0, s>>>(a);
-    else if (v <= 8 * 256 * 4) policy_row_kernel<T, 256, 4><<<grid, 256, 0, s>>>(a);
-    else if (v <= 8 * 1024 * 2) policy_row_kernel<T, 1024, 2><<<grid, 1024, 0, s>>>(a);
-    else if (v <= 8 * 1024 * 4) policy_row_kernel<T, 1024, 4><<<grid, 1024, 0, s>>>(a);
-    else if (v <= 8 * 1024 * 8) policy_row_kernel<T, 1024, 8><<<grid, 1024, 0, s>>>(a);
-    else if (v <= 8 * 1024 * 8 * K) policy_row_kernel<T, 1024, 8 * K><<<grid, 1024, 0, s>>>(a);
-    else if (v <= 8 * 1024 * 10 * K) policy_row_kernel<T, 1024, 10 * K><<<grid, 1024, 0, s>>>(a);
-    else policy_row_kernel<T, 1024, 0><<<grid, 1024, 0, s>>>(a);
+    if (v <= 8 * 256 * 2) launch_rows<T, 256, 2>(a, rows, s);
+    else if (v <= 8 * 256 * 4) launch_rows<T, 256, 4>(a, rows, s);
+    else if (v <= 8 * 1024 * 2) launch_rows<T, 1024, 2>(a, rows, s);
+    else if (v <= 8 * 1024 * 4) launch_rows<T, 1024, 4>(a, rows, s);
+    else if (v <= 8 * 1024 * 8) launch_rows<T, 1024, 8>(a, rows, s);
+    else if (v <= 8 * 1024 * 8 * K) launch_rows<T, 1024, 8 * K>(a, rows, s);
+    else if (v <= 8 * 1024 * 10 * K) launch_rows<T, 1024, 10 * K>(a, rows, s);
+    else launch_rows<T, 1024, 0>(a, rows, s);
+}
+
+template <class T>
+void launch_backward(PolicyArgs a, int64_t rows, int64_t chunks, const float* grad, hipStream_t s) {
+    const int64_t most = most_blocks(kBackThreads) / chunks;
+    for (int64_t r = 0; r < rows; r += most) {
+        a.first = (uint32_t)r;
+        const dim3 grid((uint32_t)(rows - r < most ? rows - r : most), (uint32_t)chunks);
+        policy_backward_kernel<T><<<grid, kBackThreads, 0, s>>>(a, grad);
+    }
 }
 
 opt_status check_policy(const opt_policy_desc* a) {
@@ -424,11 +448,10 @@ opt_status opt_policy_loss_backward(const opt_policy_desc* a, const void* logits
     if (opt_status st = train_pending()) return st;
     PolicyArgs p = policy_args(a, logits, nullptr);
     p.target = target, p.lse = (float*)lse, p.slope = (float*)slope, p.dlogits = dlogits, p.ldd = ldd;
-    const dim3 grid((uint32_t)a->rows, (uint32_t)chunks);
     const hipStream_t s = (hipStream_t)stream;
-    if (a->dtype == OPT_F32) policy_backward_kernel<float><<<grid, kBackThreads, 0, s>>>(p, grad);
-    else if (a->dtype == OPT_BF16) policy_backward_kernel<__bf16><<<grid, kBackThreads, 0, s>>>(p, grad);
-    else policy_backward_kernel<_Float16><<<grid, kBackThreads, 0, s>>>(p, grad);
+    if (a->dtype == OPT_F32) launch_backward<float>(p, a->rows, chunks, grad, s);
+    else if (a->dtype == OPT_BF16) launch_backward<__bf16>(p, a->rows, chunks, grad, s);
+    else launch_backward<_Float16>(p, a->rows, chunks, grad, s);
     return train_launched("policy loss backward");
 }
 

@@ -22,6 +22,9 @@ inline opt_status train_pending() {
     return e == hipSuccess ? OPT_OK : fail(OPT_EHIP, "pending HIP error: %s", hipGetErrorString(e));
 }
 
+// Workgroups of `threads` in one launch: its threads are counted in 32 bits.
+constexpr int64_t most_blocks(int threads) { return (int64_t(1) << 31) / threads; }
+
 inline bool train_dtype(int32_t d) { return d == OPT_F32 || d == OPT_BF16 || d == OPT_F16; }
 inline int64_t train_bytes(int32_t d) { return d == OPT_F32 ? 4 : 2; }
 inline bool train_aligned(const void* p, uintptr_t a) { return (uintptr_t)p % a == 0; }

@@ -304,6 +304,23 @@ def test_rows_and_keys_that_see_nothing_among_values_that_are_not_finite(tokens)
     assert not dk[:, :-23].any() and not dv[:, :-23].any()
 
 
+def test_more_workgroups_than_one_launch_holds():
+    """Past 2^31 threads the row blocks take several launches. One token a
+    sequence: its output is its value."""
+    torch, train = _torch(), _train()
+    batch, heads = 2 ** 17 + 3, 64
+    print("attention workgroups", batch * heads, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(15)
+    q, k, v, dout = (torch.randn(batch, 1, heads, 8, generator=g, device="cuda").bfloat16() for _ in range(4))
+    out, lse = train.attention_forward(q, k, v, scale=0.25)
+    dq, dk, dv = train.attention_backward(dout, q, k, v, out, lse, scale=0.25)
+    assert torch.equal(out, v) and torch.equal(dv, dout) and not dq.any() and not dk.any()
+    s = 0.25 * (q.double() * k.double()).sum(-1)[:, 0].t()
+    # eight products of 24 bits added in 24, the scaling and the change of base: 16 roundings of the largest sum
+    most = 0.25 * (q.double() * k.double()).abs().sum(-1)[:, 0].t()
+    assert ((lse.reshape(heads, batch) - s).abs() <= 16 * 2.0 ** -24 * most + 1e-30).all()
+
+
 def test_strided_views_and_given_outputs():
     """q, k, v are views of one projection, their gradients views of another, and out is head-major."""
     torch, train = _torch(), _train()

@@ -235,3 +235,17 @@ def test_equal_bits_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         got = [t.clone() for t in held]
         assert all(torch.equal(a, b) for a, b in zip(got, both())), n
+
+
+def test_more_rows_than_one_launch_holds():
+    """Past 2^31 threads the rows take several launches, and the dropped bits
+    go on from one to the next."""
+    torch, train = _torch(), _train()
+    rows, cols, part = 2 ** 27 + 3, 8, 2 ** 20
+    print("norm rows", rows, flush=True)
+    x = torch.randn(part, cols, device="cuda").bfloat16().repeat(rows // part + 1, 1)[:rows]
+    w = torch.randn(cols, device="cuda")
+    y, h, mean, rstd = train.layer_norm_forward(x, w, p=0.25, rng=train.Rng(5, 9))
+    assert torch.equal(h, train.dropout(x, 0.25, train.Rng(5, 9)))
+    y2, _, mean2, rstd2 = train.layer_norm_forward(h[-part:].contiguous(), w)
+    assert torch.equal(y[-part:], y2) and torch.equal(mean[-part:], mean2) and torch.equal(rstd[-part:], rstd2)

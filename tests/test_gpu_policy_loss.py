@@ -183,3 +183,25 @@ def test_no_rows_and_equal_bits():
         torch.cuda.synchronize()
         got = [a.clone() for a in held]
         assert all(torch.equal(a, b) for a, b in zip(got, train.policy_loss_step(x, t, old, adv, w, **how))), n
+
+
+def test_more_rows_than_one_launch_holds():
+    """Past 2^31 threads the rows take several launches: the last rows are as
+    they are alone, and so are the first."""
+    torch, train = _torch(), _train()
+    rows, vocab = 2 ** 23 + 5, 9
+    print("policy rows", rows, flush=True)
+    x, t, old, _, adv, w = (a[:4096] if a is not None else None for a in make(4096, vocab, "bf16"))
+    often = lambda a: a.repeat(rows // 4096 + 1, *[1] * (a.dim() - 1))[:rows]  # noqa: E731
+    many = [often(a) for a in (x, t, old, adv, w)]
+    few = train.policy_loss_step(x, t, old, adv, w)
+    loss, logp, d = train.policy_loss_step(*many)
+    f = train.policy_loss_forward(*many)
+    g = train.policy_loss_backward(many[0], many[1], f)
+    for a in (logp, f.logp):
+        assert torch.equal(a, often(few[1]))
+    assert torch.equal(d, often(few[2]))
+    # the two calls' probabilities are the same to the bit, their gradients to two roundings
+    assert torch.equal(g[-5:], g[:5]) and torch.equal(g, often(g[:4096]))
+    want = float(few[0]) * (rows // 4096) + float(train.policy_loss_step(x[:5], t[:5], old[:5], adv[:5], w[:5])[0])
+    assert abs(float(loss) - want) <= 2 ** -22 * abs(want) + 1e-30 and torch.equal(loss, f.loss)

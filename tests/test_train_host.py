@@ -63,6 +63,19 @@ def test_attention_descriptions_refused(N, kw, unsupported):
     refused(N, N.OPT_EUNSUPPORTED if unsupported else N.OPT_EINVAL, N.opt_attention_workspace_size, desc(N, **kw), 1)
 
 
+@pytest.mark.parametrize("kw,fits", [
+    (dict(batch=1 << 25, heads=8, kv_heads=8, q_len=1, k_len=1), True),   # several launches
+    (dict(q_len=1 << 29, k_len=1 << 29, heads=1, kv_heads=1, batch=1), True),
+    (dict(q_len=(1 << 29) + 1, k_len=8, heads=1, kv_heads=1, batch=1), False),
+    (dict(q_len=1 << 29, k_len=1 << 29, heads=64, kv_heads=8, batch=1), False),
+])
+def test_attention_limits(N, kw, fits):
+    if fits:
+        N.opt_attention_workspace_size(desc(N, **kw), 1)
+    else:
+        refused(N, N.OPT_EUNSUPPORTED, N.opt_attention_workspace_size, desc(N, **kw), 1)
+
+
 @pytest.mark.parametrize("bad", [
     dict(data=0), dict(data=BASE + 8), dict(t=255), dict(h=60), dict(b=7), dict(t=-256),
 ])
