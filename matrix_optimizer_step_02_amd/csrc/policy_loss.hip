@@ -6,8 +6,9 @@
 //   slope = w ((-A r where that is the larger or equal) + kl (1 - exp(d)))
 //   dx_j  = grad scale slope ([j = t] - exp(z_j - lse))
 //
-// One workgroup per row. The row is read once: each thread keeps its groups
-// of eight logits in registers as they are stored (up to 80 registers of 1024
+// One workgroup per row, of 256 or 1024 threads, or one wavefront for up to
+// 2048 logits. The row is read once: each thread keeps its groups of eight
+// logits in registers as they are stored (up to 80 registers of 1024
 // threads: 163840 16-bit or 81920 32-bit logits, more than half of a CU's
 // register file), takes the maximum, the sum of exponentials and the gradient
 // from there, so a pass moves one read and one write of the logits: 4096 rows
@@ -17,8 +18,8 @@
 // us that way, 270 from registers). The exponentials are taken
 // in base 2, with log2(e) folded into the scale.
 //
-// The loss is the sum of the rows' terms, which a second kernel adds in
-// 64 bits in a fixed order.
+// The loss is the sum of the rows' terms, which a second kernel (past 16384
+// rows a third) adds in 64 bits in a fixed order.
 #include "train.h"
 
 namespace matopt {
@@ -33,7 +34,7 @@ struct PolicyArgs {
     void* dlogits;                      // NULL: forward only
     int64_t ld, ldd;
     int32_t vocab, target_i64;
-    uint32_t first;                     // row of the launch's first workgroup
+    uint32_t rows, first;               // first: row of the launch's first workgroup
     float scale, lo, hi, kl, grad;
 };
 
@@ -80,9 +81,13 @@ struct Raw8 {
     }
 };
 
+constexpr int row_threads(int nt) { return nt < 256 ? 256 : nt; }   // of a workgroup
+
+// Over the NT threads of a row: a wavefront, or the whole workgroup.
 template <int NT, bool MAX>
-__device__ __forceinline__ float block_reduce(float x, float* part) {
+__device__ __forceinline__ float row_reduce(float x, float* part) {
     x = MAX ? wave_max(x) : wave_sum(x);
+    if constexpr (NT == 64) return x;
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
     __syncthreads();
     float s = part[0];
@@ -116,10 +121,16 @@ __device__ __forceinline__ void row_loss(const PolicyArgs& a, uint32_t row, floa
 
 // NV: groups of eight a thread keeps; 0: the row is read twice.
 template <class T, int NT, int NV>
-__global__ __launch_bounds__(NT) void policy_row_kernel(PolicyArgs a) {
+__global__ __launch_bounds__(row_threads(NT)) void policy_row_kernel(PolicyArgs a) {
     __shared__ float part[2][NT / 64];
-    const uint32_t row = a.first + blockIdx.x;
-    const int tid = threadIdx.x, V = a.vocab, G = (V + 7) >> 3;
+    constexpr int R = row_threads(NT) / NT;
+    uint32_t row = a.first + blockIdx.x;
+    int tid = threadIdx.x;
+    if constexpr (R > 1) {
+        row = a.first + blockIdx.x * R + __builtin_amdgcn_readfirstlane(threadIdx.x / NT), tid %= NT;
+        if (row >= a.rows) return;
+    }
+    const int V = a.vocab, G = (V + 7) >> 3;
     const T* x = (const T*)a.logits + (int64_t)row * a.ld;
     T* dx = a.dlogits ? (T*)a.dlogits + (int64_t)row * a.ldd : nullptr;
     const float w = gptr(a.weight)[row];
@@ -153,14 +164,14 @@ __global__ __launch_bounds__(NT) void policy_row_kernel(PolicyArgs a) {
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) m = fmaxf(m, keep[i].get(e));
-        m = block_reduce<NT, true>(m * c, part[0]);
+        m = row_reduce<NT, true>(m * c, part[0]);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             keep[i].again();
 #pragma unroll
             for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f(fmaf(keep[i].get(e), c, -m));
         }
-        s = block_reduce<NT, false>(s, part[1]);
+        s = row_reduce<NT, false>(s, part[1]);
     } else {
         constexpr int U = 4;
         for (int g0 = tid; g0 < G; g0 += U * NT) {
@@ -189,10 +200,10 @@ __global__ __launch_bounds__(NT) void policy_row_kernel(PolicyArgs a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f(fmaf(r[u].get(e), c, -m));
         }
-        const float all = block_reduce<NT, true>(m, part[0]);
+        const float all = row_reduce<NT, true>(m, part[0]);
         if (m != -INFINITY) s *= __builtin_amdgcn_exp2f(m - all);
         m = all;
-        s = block_reduce<NT, false>(s, part[1]);
+        s = row_reduce<NT, false>(s, part[1]);
     }
     const float lse2 = m + log2f(s);   // of z, in base 2
     const float lse = lse2 * kLn2;
@@ -265,17 +276,14 @@ __global__ __launch_bounds__(kBackThreads) void policy_backward_kernel(PolicyArg
     }
 }
 
+// Sums of `per` values each, a workgroup per sum.
 constexpr int kLossThreads = 1024;
-__global__ __launch_bounds__(kLossThreads) void policy_sum_kernel(int64_t rows, const float* term, float* loss) {
+template <class I, class O>
+__global__ __launch_bounds__(kLossThreads) void policy_sum_kernel(int64_t n, int64_t per, const I* in, O* out) {
     __shared__ double part[kLossThreads / 64];
+    const int64_t from = blockIdx.x * per, to = from + per < n ? from + per : n;
     double s = 0.0;
-    for (int64_t r0 = threadIdx.x; r0 < rows; r0 += 8 * kLossThreads) {
-        float v[8];   // eight loads in flight
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = r0 + k * kLossThreads < rows ? gptr(term)[r0 + k * kLossThreads] : 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s += v[k];
-    }
+    for (int64_t r = from + threadIdx.x; r < to; r += kLossThreads) s += gptr(in)[r];
 #pragma unroll
     for (int m = 32; m; m >>= 1) s += __shfl_xor(s, m);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
@@ -283,24 +291,50 @@ __global__ __launch_bounds__(kLossThreads) void policy_sum_kernel(int64_t rows, 
     if (threadIdx.x) return;
     s = part[0];
     for (int k = 1; k < kLossThreads / 64; ++k) s += part[k];
-    *gptr(loss) = (float)s;
+    gptr(out)[blockIdx.x] = (O)s;
 }
 
-// Small vocabularies take small workgroups, so that several rows share a CU;
-// past what 1024 threads hold in 80 registers the row is streamed.
+// One workgroup adds 4096 terms in 3 us, 16384 in 5.5 and 65536 in 18, at its
+// own pace and not memory's: past 16384 they are added in parts first, and
+// then the parts (5.7 and 9.4 us; 10^6 terms 10 in place of 270).
+constexpr int64_t kLossPart = 4096;
+int64_t loss_parts(int64_t rows) { return rows <= 4 * kLossPart ? 0 : (rows + kLossPart - 1) / kLossPart; }
+uint64_t align256(uint64_t n) { return (n + 255) / 256 * 256; }
+
+void launch_sum(int64_t rows, const float* term, float* loss, hipStream_t s) {
+    const int64_t parts = loss_parts(rows);
+    if (parts == 0) {
+        policy_sum_kernel<<<1, kLossThreads, 0, s>>>(rows, rows, term, loss);
+        return;
+    }
+    double* part = (double*)((char*)term + align256((uint64_t)rows * 4));
+    policy_sum_kernel<<<dim3((uint32_t)parts), kLossThreads, 0, s>>>(rows, kLossPart, term, part);
+    policy_sum_kernel<<<1, kLossThreads, 0, s>>>(parts, parts, (const double*)part, loss);
+}
+
+// Small vocabularies take a wavefront a row, four rows a workgroup, without
+// barriers: 65536 rows of 1000 16-bit logits 48 us, of 2000 103, against 122
+// and 169 with 256 threads a row, where starting the workgroups is the bound
+// (64 rows of 2000: 4.8 against 4.2). Then small workgroups, so that several
+// rows share a CU; past what 1024 threads hold in 80 registers the row is
+// streamed.
 template <class T, int NT, int NV>
 void launch_rows(PolicyArgs a, int64_t rows, hipStream_t s) {
-    constexpr int64_t most = most_blocks(NT);
-    for (int64_t r = 0; r < rows; r += most) {
+    constexpr int64_t N = row_threads(NT), R = N / NT, most = most_blocks(N);
+    a.rows = (uint32_t)rows;
+    for (int64_t r = 0; r < rows; r += most * R) {
+        const int64_t blocks = (rows - r + R - 1) / R;
         a.first = (uint32_t)r;
-        policy_row_kernel<T, NT, NV><<<dim3((uint32_t)(rows - r < most ? rows - r : most)), NT, 0, s>>>(a);
+        policy_row_kernel<T, NT, NV><<<dim3((uint32_t)(blocks < most ? blocks : most)), N, 0, s>>>(a);
     }
 }
 template <class T>
 void launch_rows(const PolicyArgs& a, int64_t rows, hipStream_t s) {
     const int64_t v = a.vocab;
     constexpr int K = 4 / sizeof(T);   // logits per register
-    if (v <= 8 * 256 * 2) launch_rows<T, 256, 2>(a, rows, s);
+    if (v <= 8 * 64 * 2) launch_rows<T, 64, 2>(a, rows, s);
+    else if (v <= 8 * 64 * 4) launch_rows<T, 64, 4>(a, rows, s);
+    else if (v <= 8 * 256 * 2) launch_rows<T, 256, 2>(a, rows, s);
     else if (v <= 8 * 256 * 4) launch_rows<T, 256, 4>(a, rows, s);
     else if (v <= 8 * 1024 * 2) launch_rows<T, 1024, 2>(a, rows, s);
     else if (v <= 8 * 1024 * 4) launch_rows<T, 1024, 4>(a, rows, s);
@@ -369,7 +403,9 @@ PolicyArgs policy_args(const opt_policy_desc* a, const void* logits, const opt_p
     return p;
 }
 
-uint64_t policy_bytes(const opt_policy_desc* a) { return ((uint64_t)a->rows * 4 + 255) / 256 * 256; }
+uint64_t policy_bytes(const opt_policy_desc* a) {
+    return align256((uint64_t)a->rows * 4) + align256((uint64_t)loss_parts(a->rows) * 8);
+}
 
 opt_status run_rows(const opt_policy_desc* a, PolicyArgs p, float* loss, void* ws, uint64_t ws_bytes, void* stream) {
     if (opt_status st = check_vector(loss, 4, "loss")) return st;
@@ -383,7 +419,7 @@ opt_status run_rows(const opt_policy_desc* a, PolicyArgs p, float* loss, void* w
         else if (a->dtype == OPT_BF16) launch_rows<__bf16>(p, a->rows, s);
         else launch_rows<_Float16>(p, a->rows, s);
     }
-    policy_sum_kernel<<<1, kLossThreads, 0, s>>>(a->rows, p.term, loss);
+    launch_sum(a->rows, p.term, loss, s);
     return train_launched("policy loss");
 }
 

@@ -205,3 +205,30 @@ def test_more_rows_than_one_launch_holds():
     assert torch.equal(g[-5:], g[:5]) and torch.equal(g, often(g[:4096]))
     want = float(few[0]) * (rows // 4096) + float(train.policy_loss_step(x[:5], t[:5], old[:5], adv[:5], w[:5])[0])
     assert abs(float(loss) - want) <= 2 ** -22 * abs(want) + 1e-30 and torch.equal(loss, f.loss)
+
+
+@pytest.mark.parametrize("rows", [16384, 16385, 40001])
+def test_sum_of_many_rows(rows):
+    """The terms' sum is 64-bit wherever it is split: off by one rounding to 32."""
+    torch, train = _torch(), _train()
+    print("policy sum", rows, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(rows, 17, generator=g, device="cuda")
+    t = torch.zeros(rows, device="cuda", dtype=torch.int32)
+    adv = torch.randn(rows, generator=g, device="cuda")
+    one = torch.ones(rows, device="cuda")
+    old = train.policy_loss_forward(x, t, one, adv, one).logp   # ratio exp(0) = 1: the terms are -adv to the bit
+    loss = float(train.policy_loss_forward(x, t, old, adv, one).loss)
+    want = float(-adv.double().sum())
+    assert abs(loss - want) <= 2.0 ** -24 * abs(want) + rows * 2.0 ** -53 * float(adv.double().abs().sum())
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 5, 9])
+@pytest.mark.parametrize("vocab", [1, 8, 505, 1024, 1025, 2047, 2048, 2049])
+def test_small_vocabularies(rows, vocab):
+    """Rows of a wavefront share workgroups: the last ones are not full."""
+    torch, train = _torch(), _train()
+    print("policy small", rows, vocab, flush=True)
+    x, t, old, ref, adv, w = make(rows, vocab, "bf16", seed=vocab + rows)
+    loss, logp, d = train.policy_loss_step(x, t, old, adv, w, ref_logp=ref, kl_coef=0.1, clip_high=0.28)
+    compare({"loss": loss, "logp": logp, "dlogits": d}, x, t, old, ref, adv, w, "bf16", 0.1, 1.0)
