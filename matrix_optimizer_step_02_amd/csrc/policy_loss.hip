@@ -12,11 +12,11 @@
 // threads: 163840 16-bit or 81920 32-bit logits, more than half of a CU's
 // register file), takes the maximum, the sum of exponentials and the gradient
 // from there, so a pass moves one read and one write of the logits: 4096 rows
-// of 131072 16-bit logits take 405 to 435 us, 4.9 to 5.3 TB/s. Longer rows keep a running
-// maximum and sum and read the row a second time, mostly from the last-level
-// cache (2048 rows of 131072 32-bit logits: 511 us; 150000 16-bit logits 349
-// us that way, 270 from registers). The exponentials are taken
-// in base 2, with log2(e) folded into the scale.
+// of 131072 16-bit logits take 405 to 435 us, 4.9 to 5.3 TB/s. Longer rows keep
+// a running maximum and sum and read the row a second time, mostly from the
+// last-level cache (2048 rows of 131072 32-bit logits: 511 us; 150000 16-bit
+// logits 349 us that way, 270 from registers). The exponentials are taken in
+// base 2, with log2(e) folded into the scale.
 //
 // The loss is the sum of the rows' terms, which a second kernel (past 16384
 // rows a third) adds in 64 bits in a fixed order.
@@ -242,12 +242,16 @@ __global__ __launch_bounds__(row_threads(NT)) void policy_row_kernel(PolicyArgs 
         gptr(dx)[t] = from_f32<T>(k * (1.f - __builtin_amdgcn_exp2f(fmaf(xt, c, -lse2))));
 }
 
-// dlogits from the saved log-sum and slope: kBackPer groups of a row per thread.
+// dlogits from the saved log-sum and slope: kBackPer groups of a row per
+// thread, NT threads of a workgroup on one row: a wavefront up to 2048 logits
+// (65536 rows of 1000 16-bit logits 30 us, of 2000 77; with 256 threads a row
+// 65 and 109).
 constexpr int kBackThreads = 256, kBackPer = 4;
-template <class T>
+template <class T, int NT>
 __global__ __launch_bounds__(kBackThreads) void policy_backward_kernel(PolicyArgs a, const float* grad) {
-    const uint32_t row = a.first + blockIdx.x;
-    const int V = a.vocab, G = (V + 7) >> 3, g0 = blockIdx.y * (kBackThreads * kBackPer) + threadIdx.x;
+    const uint32_t row = a.first + blockIdx.x * (kBackThreads / NT) + __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+    if (row >= a.rows) return;
+    const int V = a.vocab, G = (V + 7) >> 3, g0 = blockIdx.y * (NT * kBackPer) + threadIdx.x % NT;
     const T* x = (const T*)a.logits + (int64_t)row * a.ld;
     T* dx = (T*)a.dlogits + (int64_t)row * a.ldd;
     const float slope = gptr(a.slope)[row];
@@ -257,12 +261,12 @@ __global__ __launch_bounds__(kBackThreads) void policy_backward_kernel(PolicyArg
     Raw8<T> r[kBackPer];
 #pragma unroll
     for (int i = 0; i < kBackPer; ++i) {
-        const int g = g0 + i * kBackThreads;
+        const int g = g0 + i * NT;
         if (k != 0.f) r[i].load_n(x + 8 * (int64_t)(g < G ? g : 0), g < G ? V - 8 * g : 0);
     }
 #pragma unroll
     for (int i = 0; i < kBackPer; ++i) {
-        const int g = g0 + i * kBackThreads;
+        const int g = g0 + i * NT;
         if (g >= G) continue;
         float o[8] = {};
         if (k != 0.f) {   // a row without slope is not read: it may hold anything
@@ -344,14 +348,22 @@ void launch_rows(const PolicyArgs& a, int64_t rows, hipStream_t s) {
     else launch_rows<T, 1024, 0>(a, rows, s);
 }
 
-template <class T>
+template <class T, int NT>
 void launch_backward(PolicyArgs a, int64_t rows, int64_t chunks, const float* grad, hipStream_t s) {
+    constexpr int64_t R = kBackThreads / NT;
     const int64_t most = most_blocks(kBackThreads) / chunks;
-    for (int64_t r = 0; r < rows; r += most) {
+    a.rows = (uint32_t)rows;
+    for (int64_t r = 0; r < rows; r += most * R) {
+        const int64_t blocks = (rows - r + R - 1) / R;
         a.first = (uint32_t)r;
-        const dim3 grid((uint32_t)(rows - r < most ? rows - r : most), (uint32_t)chunks);
-        policy_backward_kernel<T><<<grid, kBackThreads, 0, s>>>(a, grad);
+        const dim3 grid((uint32_t)(blocks < most ? blocks : most), (uint32_t)chunks);
+        policy_backward_kernel<T, NT><<<grid, kBackThreads, 0, s>>>(a, grad);
     }
+}
+template <class T>
+void launch_backward(const PolicyArgs& a, int64_t rows, int64_t chunks, const float* grad, hipStream_t s) {
+    if (a.vocab <= 8 * 64 * kBackPer) launch_backward<T, 64>(a, rows, 1, grad, s);
+    else launch_backward<T, kBackThreads>(a, rows, chunks, grad, s);
 }
 
 opt_status check_policy(const opt_policy_desc* a) {

@@ -232,3 +232,7 @@ def test_small_vocabularies(rows, vocab):
     x, t, old, ref, adv, w = make(rows, vocab, "bf16", seed=vocab + rows)
     loss, logp, d = train.policy_loss_step(x, t, old, adv, w, ref_logp=ref, kl_coef=0.1, clip_high=0.28)
     compare({"loss": loss, "logp": logp, "dlogits": d}, x, t, old, ref, adv, w, "bf16", 0.1, 1.0)
+    f = train.policy_loss_forward(x, t, old, adv, w, ref_logp=ref, kl_coef=0.1, clip_high=0.28)
+    d = train.policy_loss_backward(x, t, f)
+    compare({"loss": f.loss, "logp": f.logp, "lse": f.lse, "slope": f.slope, "dlogits": d}, x, t, old, ref, adv, w, "bf16",
+            0.1, 1.0)
