@@ -153,7 +153,8 @@ opt_status opt_layer_norm_backward(int64_t rows, int64_t cols, int32_t dtype, co
  * The weights hold the normalisation (mask / tokens, for a mean over tokens).
  * A row of weight 0 is not read: logp = lse = slope = 0 and its dlogits are
  * zeros, whatever its logits and target hold. Elsewhere a target outside
- * [0, vocab) makes the row's results and the loss NaN.
+ * [0, vocab) makes the row's results and the loss NaN, and a NaN among the
+ * row's other inputs its slope, its dlogits and the loss.
  */
 typedef struct {
     int32_t dtype;             /* of logits and dlogits: OPT_F32, OPT_BF16 or OPT_F16 */

@@ -100,13 +100,16 @@ __device__ __forceinline__ int64_t target_of(const PolicyArgs& a, uint32_t row) 
     return a.target_i64 ? gptr((const int64_t*)a.target)[row] : gptr((const int32_t*)a.target)[row];
 }
 
-// What a row's log probability makes of the loss: its term and slope.
+// What a row's log probability makes of the loss: its term and slope. max and
+// >= would lose a NaN of any of the row's inputs; the unclipped term holds
+// them all but ref's. An advantage of 0 makes that term 0 also where the ratio
+// passes the range of fp32.
 __device__ __forceinline__ void row_loss(const PolicyArgs& a, uint32_t row, float w, float logp, float& term,
                                          float& slope) {
     const float adv = gptr(a.advantage)[row];
     const float r = expf(logp - gptr(a.old_logp)[row]);
     const float clipped = fminf(fmaxf(r, a.lo), a.hi);
-    const float free = -adv * r, bound = -adv * clipped;
+    const float free = adv == 0.f && r == INFINITY ? 0.f : -adv * r, bound = -adv * clipped;
     term = fmaxf(free, bound);
     slope = free >= bound ? free : 0.f;
     if (a.kl != 0.f) {
@@ -114,7 +117,7 @@ __device__ __forceinline__ void row_loss(const PolicyArgs& a, uint32_t row, floa
         term += a.kl * (e - d);
         slope -= a.kl * e;
     }
-    if (logp != logp) term = slope = logp;   // max and >= would lose a NaN
+    if (free != free) term = slope = free;
     term *= w;
     slope *= w;
 }

@@ -236,3 +236,40 @@ def test_small_vocabularies(rows, vocab):
     d = train.policy_loss_backward(x, t, f)
     compare({"loss": f.loss, "logp": f.logp, "lse": f.lse, "slope": f.slope, "dlogits": d}, x, t, old, ref, adv, w, "bf16",
             0.1, 1.0)
+
+
+@pytest.mark.parametrize("vocab", [1000, 5000, 170001])
+@pytest.mark.parametrize("bad", ["old", "advantage", "reference", "weight"])
+def test_nan_of_a_rows_inputs_reaches_its_results(vocab, bad):
+    """One NaN makes its row's slope and gradient and the loss NaN, and leaves the other rows as they were."""
+    torch, train = _torch(), _train()
+    print(f"policy nan {bad} {vocab}", flush=True)
+    x, t, old, ref, adv, w = make(4, vocab, "f32")
+    w[:] = 0.25
+    how = dict(ref_logp=ref, kl_coef=0.1)
+    want = train.policy_loss_step(x, t, old, adv, w, **how)
+    f0 = train.policy_loss_forward(x, t, old, adv, w, **how)
+    g0 = train.policy_loss_backward(x, t, f0)
+    {"old": old, "advantage": adv, "reference": ref, "weight": w}[bad][2] = float("nan")
+    loss, logp, d = train.policy_loss_step(x, t, old, adv, w, **how)
+    f = train.policy_loss_forward(x, t, old, adv, w, **how)
+    g = train.policy_loss_backward(x, t, f)
+    assert loss.isnan() and f.loss.isnan() and f.slope[2].isnan()
+    assert d[2].isnan().all() and g[2].isnan().all()
+    for n in (0, 1, 3):
+        assert torch.equal(d[n], want[2][n]) and torch.equal(g[n], g0[n]) and f.slope[n] == f0.slope[n]
+    assert torch.equal(logp, want[1])
+    if bad == "reference":   # not read without a KL term
+        assert torch.equal(train.policy_loss_step(x, t, old, adv, w, ref_logp=ref)[0],
+                           train.policy_loss_step(x, t, old, adv, w)[0])
+
+
+def test_no_advantage_is_no_term_whatever_the_ratio():
+    """0 times a ratio past the range of fp32 is 0, as it is for every ratio."""
+    torch, train = _torch(), _train()
+    print("policy advantage 0", flush=True)
+    x, t, old, ref, adv, w = make(3, 100, "f32")
+    w[:], adv[1], old[1] = 0.5, 0.0, -200.0
+    f = train.policy_loss_forward(x, t, old, adv, w)
+    assert f.loss.isfinite() and f.slope[1] == 0
+    assert not train.policy_loss_step(x, t, old, adv, w)[2][1].any()
