@@ -162,6 +162,11 @@ typedef struct {
     int64_t rows, vocab;       /* rows < 2^31, vocab < 2^31 */
     int64_t ld;                /* row stride of logits */
     float logit_scale, clip_low, clip_high, kl_coef;
+    /* rows floats (may be NULL): lse is rounded to fp32, off by up to
+     * 2^-24 |lse|, and this is what the rounding left out. The forward call
+     * writes it; the backward call, given the same, forms exp(z_j - lse)
+     * without that error, which an offset common to the logits enlarges. */
+    float* lse_rest;
 } opt_policy_desc;
 
 /* Per-row inputs: target, old_logp, advantage, weight and, unless kl_coef is

@@ -18,6 +18,17 @@
 // logits 349 us that way, 270 from registers). The exponentials are taken in
 // base 2, with log2(e) folded into the scale.
 //
+// Logits enter as differences from the row's maximum M, taken before anything
+// is rounded at M's magnitude: with s = sum_j exp(z_j - M),
+//   logp = (z_t - M) - log s,  p_j = exp(z_j - M) / s,  1 - p_t = -expm1(logp)
+// so that an offset common to the row's logits costs nothing (a rounded
+// M + log s put 7e-5 into logp at an offset of 1000). Logits in registers take
+// one fused operation for it, x c - fl(M c), whose common shift M c - fl(M c)
+// is known to the bit and leaves log s again; (x - M) c is an operation more
+// (4096 x 131072: 500 against 486 us). Longer rows take that, and rows whose
+// shift would grow large (|M c| from 2^20, as where all logits are the type's
+// lowest value) are rewritten as x - M.
+//
 // The loss is the sum of the rows' terms, which a second kernel (past 16384
 // rows a third) adds in 64 bits in a fixed order.
 #include "train.h"
@@ -30,7 +41,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 struct PolicyArgs {
     const void *logits, *target;
     const float *old_logp, *ref_logp, *advantage, *weight;
-    float *logp, *lse, *slope, *term;   // logp, lse, slope: NULL where the call does not return them
+    float *logp, *lse, *rest, *slope, *term;   // NULL where the call does not return them; rest: of lse's rounding
     void* dlogits;                      // NULL: forward only
     int64_t ld, ldd;
     int32_t vocab, target_i64;
@@ -83,21 +94,34 @@ struct Raw8 {
 
 constexpr int row_threads(int nt) { return nt < 256 ? 256 : nt; }   // of a workgroup
 
+// A value that all of a wavefront's threads have: in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
 // Over the NT threads of a row: a wavefront, or the whole workgroup.
 template <int NT, bool MAX>
 __device__ __forceinline__ float row_reduce(float x, float* part) {
     x = MAX ? wave_max(x) : wave_sum(x);
-    if constexpr (NT == 64) return x;
+    if constexpr (NT == 64) return uniform(x);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
     __syncthreads();
     float s = part[0];
 #pragma unroll
     for (int k = 1; k < NT / 64; ++k) s = MAX ? fmaxf(s, part[k]) : s + part[k];
-    return s;
+    return uniform(s);
 }
 
 __device__ __forceinline__ int64_t target_of(const PolicyArgs& a, uint32_t row) {
     return a.target_i64 ? gptr((const int64_t*)a.target)[row] : gptr((const int32_t*)a.target)[row];
+}
+
+// a + b rounded, and the error of that rounding (Knuth).
+__device__ __forceinline__ float two_sum(float a, float b, float& rest) {
+#pragma clang fp contract(off) reassociate(off)
+    const float s = a + b, t = s - a;
+    rest = (a - (s - t)) + (b - t);
+    return s;
 }
 
 // What a row's log probability makes of the loss: its term and slope. max and
@@ -146,6 +170,7 @@ __global__ __launch_bounds__(row_threads(NT)) void policy_row_kernel(PolicyArgs 
             gptr(a.term)[row] = 0.f;
             if (a.logp) gptr(a.logp)[row] = 0.f;
             if (a.lse) gptr(a.lse)[row] = 0.f;
+            if (a.rest) gptr(a.rest)[row] = 0.f;
             if (a.slope) gptr(a.slope)[row] = 0.f;
         }
         return;
@@ -156,7 +181,8 @@ __global__ __launch_bounds__(row_threads(NT)) void policy_row_kernel(PolicyArgs 
     const float xt = valid ? (float)gptr(x)[t] : NAN;   // before any store: dlogits may be logits
 
     Raw8<T> keep[NV > 0 ? NV : 1];
-    float m = -INFINITY, s = 0.f;
+    float m = -INFINITY, s = 0.f;   // the maximum, and the sum of exp2((x - m) c + shift)
+    float mc = 0.f, shift = 0.f;
     if constexpr (NV > 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -167,12 +193,31 @@ __global__ __launch_bounds__(row_threads(NT)) void policy_row_kernel(PolicyArgs 
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) m = fmaxf(m, keep[i].get(e));
-        m = row_reduce<NT, true>(m * c, part[0]);
+        m = row_reduce<NT, true>(m, part[0]);
+        mc = uniform(m * c);
+        shift = fmaf(m, c, -mc);
+        if (!(fabsf(mc) < 0x1p20f)) {   // the same for all threads of the row
+            // The differences in place of the logits, rounded to their type:
+            // exact within a factor of two of m, and past that below -2^19 / c
+            // and without a part in any sum.
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                keep[i].again();
+                Raw8<T> r;
+#pragma unroll
+                for (int j = 0; j < Raw8<T>::W; ++j) r.w[j] = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) r.set(e, from_f32<T>(keep[i].get(e) - m));
+                r.again();
+                keep[i] = r;
+            }
+            mc = shift = 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             keep[i].again();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f(fmaf(keep[i].get(e), c, -m));
+            for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f(fmaf(keep[i].get(e), c, -mc));
         }
         s = row_reduce<NT, false>(s, part[1]);
     } else {
@@ -188,7 +233,7 @@ __global__ __launch_bounds__(row_threads(NT)) void policy_row_kernel(PolicyArgs 
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) top = fmaxf(top, r[u].get(e) * c);
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, r[u].get(e));
             if (top == -INFINITY) {   // nothing yet but -inf, or a NaN, which must reach the sum
 #pragma unroll
                 for (int u = 0; u < U; ++u)
@@ -196,35 +241,43 @@ __global__ __launch_bounds__(row_threads(NT)) void policy_row_kernel(PolicyArgs 
                     for (int e = 0; e < 8; ++e) s += r[u].get(e) != r[u].get(e) ? NAN : 0.f;
                 continue;
             }
-            s *= __builtin_amdgcn_exp2f(m - top);
+            s *= __builtin_amdgcn_exp2f((m - top) * c);
             m = top;
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f(fmaf(r[u].get(e), c, -m));
+                for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f((r[u].get(e) - m) * c);
         }
         const float all = row_reduce<NT, true>(m, part[0]);
-        if (m != -INFINITY) s *= __builtin_amdgcn_exp2f(m - all);
+        if (m != -INFINITY) s *= __builtin_amdgcn_exp2f((m - all) * c);
         m = all;
         s = row_reduce<NT, false>(s, part[1]);
     }
-    const float lse2 = m + log2f(s);   // of z, in base 2
-    const float lse = lse2 * kLn2;
-    const float logp = fmaf(xt, a.scale, -lse);
+    const float ls = (log2f(s) - shift) * kLn2;
+    float logp = fmaf(xt - m, a.scale, -ls);
+    if (logp > 0.f) logp = 0.f;   // the sum's rounding, where the target holds nearly all of it
     float term, slope;
     row_loss(a, row, w, logp, term, slope);
     if (tid == 0) {
         gptr(a.term)[row] = term;
         if (a.logp) gptr(a.logp)[row] = logp;
-        if (a.lse) gptr(a.lse)[row] = lse;
+        if (a.lse) {
+            // scale m + ls as the nearest fp32 value, and what that leaves out
+            const float z = a.scale * m, small = fmaf(a.scale, m, -z) + ls;
+            float rest;
+            const float lse = two_sum(z, small, rest);
+            gptr(a.lse)[row] = lse;
+            if (a.rest) gptr(a.rest)[row] = rest;
+        }
         if (a.slope) gptr(a.slope)[row] = slope;
     }
     if (!dx) return;
-    const float k = a.grad * a.scale * slope;
+    const float k = a.grad * a.scale * slope, ks = uniform(k / s);
     auto write = [&](int g, const Raw8<T>& r) {
         float o[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = -k * __builtin_amdgcn_exp2f(fmaf(r.get(e), c, -lse2));
+        for (int e = 0; e < 8; ++e)
+            o[e] = -ks * __builtin_amdgcn_exp2f(NV > 0 ? fmaf(r.get(e), c, -mc) : (r.get(e) - m) * c);
         store_n(dx + 8 * (int64_t)g, V - 8 * g, o);
     };
     if constexpr (NV > 0) {
@@ -241,11 +294,12 @@ __global__ __launch_bounds__(row_threads(NT)) void policy_row_kernel(PolicyArgs 
         }
     }
     // the target's entry, by the thread that wrote its group
-    if (valid && (int)(t >> 3) % NT == tid)
-        gptr(dx)[t] = from_f32<T>(k * (1.f - __builtin_amdgcn_exp2f(fmaf(xt, c, -lse2))));
+    if (valid && (int)(t >> 3) % NT == tid) gptr(dx)[t] = from_f32<T>(k * -expm1f(logp));
 }
 
-// dlogits from the saved log-sum and slope: kBackPer groups of a row per
+// dlogits from the saved log-sum and slope: z_j - lse is one rounding of the
+// exact difference, of its own magnitude, and takes what lse's rounding left
+// out (rest) from there. kBackPer groups of a row per
 // thread, NT threads of a workgroup on one row: a wavefront up to 2048 logits
 // (65536 rows of 1000 16-bit logits 30 us, of 2000 77; with 256 threads a row
 // 65 and 109).
@@ -259,7 +313,7 @@ __global__ __launch_bounds__(kBackThreads) void policy_backward_kernel(PolicyArg
     T* dx = (T*)a.dlogits + (int64_t)row * a.ldd;
     const float slope = gptr(a.slope)[row];
     const float k = slope == 0.f ? 0.f : (grad ? *gptr(grad) : 1.f) * a.scale * slope;
-    const float c = a.scale * kLog2e, lse2 = gptr(a.lse)[row] * kLog2e;
+    const float lse = gptr(a.lse)[row], rest = a.rest ? gptr(a.rest)[row] : 0.f;
     const int64_t t = target_of(a, row);
     Raw8<T> r[kBackPer];
 #pragma unroll
@@ -271,15 +325,17 @@ __global__ __launch_bounds__(kBackThreads) void policy_backward_kernel(PolicyArg
     for (int i = 0; i < kBackPer; ++i) {
         const int g = g0 + i * NT;
         if (g >= G) continue;
-        float o[8] = {};
+        float o[8] = {}, logp = 0.f;
         if (k != 0.f) {   // a row without slope is not read: it may hold anything
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(r[i].get(e), c, -lse2));
-                o[e] = 8 * (int64_t)g + e == t ? k * (1.f - p) : -k * p;
+                const float z = fmaf(r[i].get(e), a.scale, -lse) - rest;
+                if (8 * (int64_t)g + e == t) logp = z;
+                o[e] = -k * __builtin_amdgcn_exp2f(z * kLog2e);
             }
         }
         store_n(dx + 8 * (int64_t)g, V - 8 * g, o);
+        if (k != 0.f && t >> 3 == g && t < V) gptr(dx)[t] = from_f32<T>(k * -expm1f(logp));
     }
 }
 
@@ -379,6 +435,7 @@ opt_status check_policy(const opt_policy_desc* a) {
     if (!(a->clip_low >= 0.f && a->clip_low <= 1.f) || !(a->clip_high >= 0.f))
         return fail(OPT_EINVAL, "clip_low must be in [0, 1] and clip_high >= 0");
     if (!(a->kl_coef >= 0.f)) return fail(OPT_EINVAL, "kl_coef must be >= 0");
+    if (!train_aligned(a->lse_rest, 4)) return fail(OPT_EINVAL, "lse_rest is not aligned to its element size");
     return OPT_OK;
 }
 
@@ -413,6 +470,7 @@ PolicyArgs policy_args(const opt_policy_desc* a, const void* logits, const opt_p
         p.target = in->target, p.old_logp = in->old_logp, p.ref_logp = in->ref_logp;
         p.advantage = in->advantage, p.weight = in->weight;
     }
+    p.rest = a->lse_rest;
     p.ld = a->ld, p.vocab = (int32_t)a->vocab, p.target_i64 = a->target_i64;
     p.scale = a->logit_scale, p.lo = 1.f - a->clip_low, p.hi = 1.f + a->clip_high, p.kl = a->kl_coef, p.grad = 1.f;
     return p;

@@ -96,7 +96,7 @@ class opt_policy_desc(C.Structure):
     _fields_ = [
         ("dtype", C.c_int32), ("target_i64", C.c_int32), ("rows", C.c_int64), ("vocab", C.c_int64),
         ("ld", C.c_int64), ("logit_scale", C.c_float), ("clip_low", C.c_float), ("clip_high", C.c_float),
-        ("kl_coef", C.c_float),
+        ("kl_coef", C.c_float), ("lse_rest", C.c_void_p),
     ]
 
 

@@ -343,13 +343,24 @@ def layer_norm_backward(dy, h, weight, mean, rstd, *, dh=None, p=0.0, rng=None, 
 # ------------------------------------------------------------ policy loss ----
 
 
-class PolicyForward(NamedTuple):
-    """What policy_loss_forward returns: the loss (a scalar tensor) and per
-    row the target's log probability, the log-sum and d loss / d logp."""
+class _PolicyForward(NamedTuple):
     loss: torch.Tensor
     logp: torch.Tensor
     lse: torch.Tensor
     slope: torch.Tensor
+
+
+class PolicyForward(_PolicyForward):
+    """What policy_loss_forward returns: the loss (a scalar tensor) and per
+    row the target's log probability, the log-sum and d loss / d logp. Beside
+    these four it holds what policy_loss_backward takes from the same call:
+    ``lse_rest``, what lse's rounding left out (None: nothing is known of it)."""
+    lse_rest: Optional[torch.Tensor] = None
+
+    def _replace(self, **kw):
+        new = super()._replace(**kw)
+        new.__dict__.update(self.__dict__)
+        return new
 
 
 def _policy(logits, target, clip_low, clip_high, kl_coef, logit_scale):
@@ -386,10 +397,13 @@ def policy_loss_forward(logits, target, old_logp, advantage, weight, *, ref_logp
     st = _stream(dev)
     n = native.opt_policy_loss_workspace_size(a)
     ws = _bytes(logits, n)
-    loss, logp, lse, slope = (weight.new_empty(s) for s in ((), a.rows, a.rows, a.rows))
+    loss, logp, lse, slope, rest = (weight.new_empty(s) for s in ((), a.rows, a.rows, a.rows, a.rows))
+    a.lse_rest = rest.data_ptr()
     native.opt_policy_loss_forward(a, lp, rows, loss.data_ptr(), logp.data_ptr(), lse.data_ptr(), slope.data_ptr(),
                                    ws.data_ptr() if n else 0, n, st)
-    return PolicyForward(loss, logp, lse, slope)
+    f = PolicyForward(loss, logp, lse, slope)
+    f.lse_rest = rest
+    return f
 
 
 @_streamed
@@ -400,6 +414,9 @@ def policy_loss_backward(logits, target, fwd, *, grad=None, logit_scale=1.0, out
     d = _out(out, "out", logits, dev)
     dp, ldd = _rows(d, "out")
     sp, ep = _vector(fwd.slope, "slope", dev, a.rows), _vector(fwd.lse, "lse", dev, a.rows)
+    rest = getattr(fwd, "lse_rest", None)
+    if rest is not None:
+        a.lse_rest = _vector(rest, "lse_rest", dev, a.rows)
     gp = 0
     if grad is not None:
         _is(grad, "grad", dev, torch.float32, ())

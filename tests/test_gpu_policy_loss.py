@@ -273,3 +273,85 @@ def test_no_advantage_is_no_term_whatever_the_ratio():
     f = train.policy_loss_forward(x, t, old, adv, w)
     assert f.loss.isfinite() and f.slope[1] == 0
     assert not train.policy_loss_step(x, t, old, adv, w)[2][1].any()
+
+
+@pytest.mark.parametrize("offset", [0.0, 100.0, 1000.0, -1000.0])
+@pytest.mark.parametrize("vocab", [1000, 5000, 170001])
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_a_common_offset_of_the_logits_costs_nothing(vocab, offset, dtype):
+    """The softmax depends on differences of logits, so bounds do not grow with
+    an offset. With u = 2^-24 and a sum of n terms in turn and in a tree: the
+    sum is off by n u, an exponential by 4 u + 3 u |z - max| (the rounded
+    difference, the rounded change of base and the instruction), the logarithm
+    and what is done with it by 4 u of what it holds, which is below log V."""
+    torch, train = _torch(), _train()
+    print(f"policy offset {vocab} {offset} {dtype}", flush=True)
+    scale, kl, lo, hi, u = float(np.float32(0.7)), 0.1, 0.2, 0.28, 2.0 ** -24
+    added = {1000: 16 + 6, 5000: 32 + 10, 170001: 168 + 22}[vocab]
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    rows = 12
+    t = torch.randint(0, vocab, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    x = 2 * torch.randn(rows, vocab, generator=g, device="cuda")
+    x[torch.arange(rows), t.long()] += torch.tensor([0.0, 12.0, 25.0, 45.0], device="cuda").repeat(3)
+    x = (x + offset).to({"f32": torch.float32, "f16": torch.float16}[dtype])
+    z = x.double() * scale
+    true = z.gather(1, t.long()[:, None])[:, 0] - z.logsumexp(1)
+    gap = torch.tensor([0.0, 0.1, -0.1, 0.5, -0.5, 2.0], device="cuda").repeat(2)
+    old, ref = (true - gap).float(), (true + 0.3 * torch.randn(rows, generator=g, device="cuda")).float()
+    adv, w = torch.randn(rows, generator=g, device="cuda"), torch.full((rows,), 1.0 / rows, device="cuda")
+    how = dict(ref_logp=ref, kl_coef=kl, logit_scale=scale, clip_low=lo, clip_high=hi)
+    loss, logp, d = train.policy_loss_step(x, t, old, adv, w, **how)
+    f = train.policy_loss_forward(x, t, old, adv, w, **how)
+    b = train.policy_loss_backward(x, t, f, logit_scale=scale)
+    r = T.policy_loss(np64(x), t.cpu().numpy(), np64(old), np64(ref), np64(adv), np64(w), lo, hi, kl, scale)
+    zc = np64(z)
+    below = zc.max(1) - zc[np.arange(rows), t.cpu().numpy()]         # of the target, below the maximum
+    p = np.exp(zc - r["lse"][:, None])
+    mean = (p * (zc.max(1)[:, None] - zc)).sum(1)                    # what the terms' own errors weigh
+    e_logp = u * (added + 4 + 3 * mean + 4 * np.log(vocab) + 4 * below + 4 * np.abs(r["logp"]))
+    assert np.all(np.abs(np64(logp) - r["logp"]) <= e_logp) and (logp <= 0).all()
+    assert torch.equal(f.logp, logp)
+    assert np.all(np.abs(np64(f.lse) - r["lse"]) <= e_logp + u * np.abs(r["lse"]))
+    # exp(logp - old) and exp(ref - logp): e_logp, the difference's rounding and the function's two steps
+    ratio, back = np.exp(r["logp"] - np64(old)), np.exp(np64(ref) - r["logp"])
+    wide = np64(w) * (np.abs(np64(adv)) * ratio + kl * back)
+    e_slope = wide * (e_logp + 12 * u)
+    assert np.all(np.abs(np64(f.slope) - r["slope"]) <= e_slope)
+    assert abs(float(loss) - r["loss"]) <= (e_slope + np64(w) * kl * (e_logp + 4 * u)).sum() + u * abs(r["loss"]) + 8 * u * np.abs(r["term"]).sum()
+    hot = np.zeros_like(p)
+    hot[np.arange(rows), t.cpu().numpy()] = 1
+    e_p = p * (e_logp[:, None] + u * (8 + 4 * np.abs(zc - r["lse"][:, None]))) + hot * 4 * u * (1 - p)
+    tiny = 2.0 ** -25 if dtype == "f16" else 0
+    for got in (d, b):
+        err = np.abs(np64(got) - r["dlogits"])
+        bound = scale * (e_slope[:, None] * np.abs(hot - p) + (np.abs(r["slope"]) + e_slope)[:, None] * e_p)
+        bound += (U[dtype] + 4 * u) * (np.abs(r["dlogits"]) + bound) + tiny + 1e-37
+        assert np.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("vocab", [9, 1000, 5000, 40000, 170001])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_of_the_types_lowest_value(vocab, dtype):
+    """Logits masked by the type's lowest value: beside others they count for nothing, a row of nothing else is
+    uniform; and finite logits far past the range of exact whole numbers keep their differences."""
+    torch, train = _torch(), _train()
+    print(f"policy lowest {vocab} {dtype}", flush=True)
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    low = torch.finfo(dt).min
+    x = torch.full((3, vocab), low, device="cuda", dtype=dt)
+    x[1, 1:3] = 1.0
+    x[2], x[2, 2] = 2.0 ** 40, 2.0 ** 40 + 2.0 ** 33
+    t = torch.tensor([2, 2, 2], device="cuda", dtype=torch.int32)
+    one, none = torch.ones(3, device="cuda"), torch.zeros(3, device="cuda")
+    old = torch.tensor([-np.log(vocab), -np.log(2), 0.0], device="cuda", dtype=torch.float32)
+    f = train.policy_loss_forward(x, t, old, one, one)
+    g = train.policy_loss_backward(x, t, f)
+    loss, logp, d = train.policy_loss_step(x, t, old, one, one)
+    want = torch.zeros(3, vocab, device="cuda", dtype=torch.float64)   # slope -1: p - onehot
+    want[0], want[1, 1:3] = 1 / vocab, 0.5
+    want[0, 2] -= 1
+    want[1, 2] -= 1
+    # as in compare: logp within 2e-5, gradients within 2e-4 of themselves and the rounding
+    assert ((logp.double().cpu() - old.double().cpu()).abs() <= 2e-5).all() and torch.equal(f.logp, logp)
+    for got in (d, g):
+        assert ((got.double() - want).abs() <= (2e-4 + U[dtype]) * want.abs() + 1e-12).all()

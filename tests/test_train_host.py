@@ -235,3 +235,8 @@ def test_tensors_are_checked_before_a_device_is_needed(N):
         train.policy_loss_step(torch.zeros(3, 5), torch.zeros(3, dtype=torch.int64), v, v, v, kl_coef=0.1)
     with pytest.raises(ValueError, match="target"):
         train.policy_loss_step(torch.zeros(3, 5), v, v, v, v)
+
+
+def test_policy_lse_rest_must_be_aligned(N):
+    refused(N, N.OPT_EINVAL, N.opt_policy_loss_workspace_size, policy(N, lse_rest=BASE + 2))
+    N.opt_policy_loss_workspace_size(policy(N, lse_rest=BASE + 4))
