@@ -354,8 +354,10 @@ class PolicyForward(_PolicyForward):
     """What policy_loss_forward returns: the loss (a scalar tensor) and per
     row the target's log probability, the log-sum and d loss / d logp. Beside
     these four it holds what policy_loss_backward takes from the same call:
-    ``lse_rest``, what lse's rounding left out (None: nothing is known of it)."""
+    ``lse_rest``, what lse's rounding left out, and ``logit_scale`` (None:
+    nothing is known of them)."""
     lse_rest: Optional[torch.Tensor] = None
+    logit_scale: Optional[float] = None
 
     def _replace(self, **kw):
         new = super()._replace(**kw)
@@ -402,14 +404,20 @@ def policy_loss_forward(logits, target, old_logp, advantage, weight, *, ref_logp
     native.opt_policy_loss_forward(a, lp, rows, loss.data_ptr(), logp.data_ptr(), lse.data_ptr(), slope.data_ptr(),
                                    ws.data_ptr() if n else 0, n, st)
     f = PolicyForward(loss, logp, lse, slope)
-    f.lse_rest = rest
+    f.lse_rest, f.logit_scale = rest, logit_scale
     return f
 
 
 @_streamed
-def policy_loss_backward(logits, target, fwd, *, grad=None, logit_scale=1.0, out=None):
+def policy_loss_backward(logits, target, fwd, *, grad=None, logit_scale=None, out=None):
     """dlogits from policy_loss_forward's result; grad: the loss's gradient, a
-    scalar tensor on the device (None: 1). out may be logits."""
+    scalar tensor on the device (None: 1). logit_scale is the forward call's
+    and may be left out. out may be logits."""
+    scale = getattr(fwd, "logit_scale", None)
+    if logit_scale is None:
+        logit_scale = 1.0 if scale is None else scale
+    elif scale is not None and logit_scale != scale:
+        raise ValueError(f"logit_scale is {logit_scale}, the forward call's was {scale}")
     a, dev, lp, tp = _policy(logits, target, 0.2, 0.2, 0.0, logit_scale)
     d = _out(out, "out", logits, dev)
     dp, ldd = _rows(d, "out")

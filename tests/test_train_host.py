@@ -240,3 +240,25 @@ def test_tensors_are_checked_before_a_device_is_needed(N):
 def test_policy_lse_rest_must_be_aligned(N):
     refused(N, N.OPT_EINVAL, N.opt_policy_loss_workspace_size, policy(N, lse_rest=BASE + 2))
     N.opt_policy_loss_workspace_size(policy(N, lse_rest=BASE + 4))
+
+
+def test_policy_backward_takes_the_forward_calls_scale(N, monkeypatch):
+    """The gradient is of the loss that was computed: its logit_scale comes with it, and another one is refused."""
+    from matrix_optimizer_step_02_amd import train
+    seen = []
+    monkeypatch.setattr(train, "_stream", lambda dev: 0)
+    monkeypatch.setattr(N, "opt_policy_loss_forward", lambda a, *rest: seen.append(a.logit_scale))
+    monkeypatch.setattr(N, "opt_policy_loss_backward", lambda a, *rest: seen.append(a.logit_scale))
+    x, t, v = torch.zeros(3, 5), torch.zeros(3, dtype=torch.int64), torch.zeros(3)
+    f = train.policy_loss_forward(x, t, v, v, v, logit_scale=0.5)
+    train.policy_loss_backward(x, t, f)
+    train.policy_loss_backward(x, t, f, logit_scale=0.5)
+    train.policy_loss_backward(x, t, f._replace(slope=2 * f.slope))
+    assert seen == [0.5] * 4
+    with pytest.raises(ValueError, match="logit_scale"):
+        train.policy_loss_backward(x, t, f, logit_scale=1.0)
+    del seen[:]
+    four = train.PolicyForward(*f)   # of the four tensors alone
+    train.policy_loss_backward(x, t, four)
+    train.policy_loss_backward(x, t, four, logit_scale=0.5)
+    assert seen == [1.0, 0.5]
