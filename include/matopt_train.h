@@ -61,7 +61,8 @@ typedef struct {
     float scale;
     /* Packed sequences: batch + 1 ascending device offsets into the token
      * axis (then batch strides are unused). Both or neither. Tokens outside
-     * every sequence are neither read nor written. */
+     * every sequence, and past the first q_len or k_len of a longer one, are
+     * not read; outputs and gradients are written there as zeros (L: -inf). */
     const int32_t* q_start;
     const int32_t* k_start;
     int64_t q_tokens, k_tokens;       /* packed: rows of the token axes */

@@ -947,6 +947,37 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kv_kernel(AttnArgs a, 
     store8((T*)(rows_of(t, b, sq.k0, hk) + (int64_t)j * t.token) + col, x);
 }
 
+// Packed token axes: writes the rows that no sequence covers, which lie before
+// the first one, between two, after the last and past q_len or k_len of a
+// longer one, as zeros (lse: -inf); the products that take these tensors read
+// whole token axes. Workgroups of gap x (the one before sequence x), most of
+// which are empty: 4 us for 14 gaps, 8192 tokens and nothing to do.
+constexpr int kGapThreads = 256;
+__global__ __launch_bounds__(kGapThreads) void attn_uncovered_kernel(AttnArgs a, int backward) {
+    const bool keys = blockIdx.z;
+    const int32_t* start = keys ? a.k_start : a.q_start;
+    const int64_t tokens = keys ? a.k_tokens : a.q_tokens;
+    const int most = keys ? a.k_len : a.q_len, groups = a.head_dim / 8, each = (keys ? a.kv_heads : a.heads) * groups;
+    const Tensor t = keys ? a.dk : backward ? a.dq : a.o;
+    const u32x4 zero = {};
+    for (int64_t gap = blockIdx.x; gap <= a.batch; gap += gridDim.x) {
+        int n;
+        int64_t from = 0, to = tokens;
+        if (gap > 0) {
+            from = packed(start, tokens, most, (int)gap - 1, n);
+            from += n;
+        }
+        if (gap < a.batch) to = packed(start, tokens, most, (int)gap, n);
+        for (int64_t i = (int64_t)blockIdx.y * kGapThreads + threadIdx.x; i < (to - from) * each; i += (int64_t)gridDim.y * kGapThreads) {
+            const int64_t row = from + i / each;
+            const int h = (int)(i % each) / groups, c = (int)(i % each) % groups;
+            *gptr((u32x4*)(rows_of(t, 0, row, h) + 16 * c)) = zero;
+            if (keys) *gptr((u32x4*)(rows_of(a.dv, 0, row, h) + 16 * c)) = zero;
+            if (!backward && c == 0) gptr(a.lse)[(int64_t)h * a.q_tokens + row] = -INFINITY;
+        }
+    }
+}
+
 // ------------------------------------------------------------------ host ----
 
 opt_status check_attention(const opt_attention_desc* a) {
@@ -1121,6 +1152,13 @@ void launch(Kind kind, int32_t dtype, const AttnArgs& x, hipStream_t s) {
     dtype == OPT_BF16 ? launch<__bf16>(kind, x, s) : launch<_Float16>(kind, x, s);
 }
 
+void launch_uncovered(bool backward, const AttnArgs& x, hipStream_t s) {
+    if (!x.q_start) return;
+    const int64_t gaps = (int64_t)x.batch + 1, slices = 1024 / gaps;
+    const dim3 g((uint32_t)(gaps < 65536 ? gaps : 65536), (uint32_t)(slices < 1 ? 1 : slices > 64 ? 64 : slices), backward ? 2 : 1);
+    attn_uncovered_kernel<<<g, kGapThreads, 0, s>>>(x, backward);
+}
+
 // The workspace: D (backward), then the splits' partial results. dQ's are
 // joined before dK's and dV's are written, in the same place.
 struct Space {
@@ -1183,19 +1221,22 @@ opt_status opt_attention_forward(const opt_attention_desc* a, const opt_attentio
                                  uint64_t workspace_bytes, void* stream) {
     if (opt_status st = check_attention(a)) return st;
     AttnArgs x = attn_args(a);
+    // nothing to read, and nothing to write (packed tokens are written without sequences too)
     const bool no_q = x.q_tokens == 0 || a->q_len == 0 || a->batch == 0, no_k = x.k_tokens == 0 || a->k_len == 0;
+    const bool no_out = x.q_tokens == 0;
     if (opt_status st = tensor(a, q, "q", no_q, x.q)) return st;
     if (opt_status st = tensor(a, k, "k", no_k || no_q, x.k)) return st;
     if (opt_status st = tensor(a, v, "v", no_k || no_q, x.v)) return st;
-    if (opt_status st = output(a, out, "out", no_q, a->heads, a->q_len, x.o)) return st;
-    if (!no_q && (!lse || !train_aligned(lse, 4))) return fail(OPT_EINVAL, "lse is NULL or not aligned to 4 bytes");
+    if (opt_status st = output(a, out, "out", no_out, a->heads, a->q_len, x.o)) return st;
+    if (!no_out && (!lse || !train_aligned(lse, 4))) return fail(OPT_EINVAL, "lse is NULL or not aligned to 4 bytes");
     const Space space = space_of(x, false);
     if (opt_status st = check_workspace(workspace, workspace_bytes, space.bytes)) return st;
-    if (no_q) return OPT_OK;
+    if (no_out) return OPT_OK;
     if (opt_status st = train_pending()) return st;
     x.lse = lse;
     use_space(x, space, workspace);
     launch(FORWARD, a->dtype, x, (hipStream_t)stream);
+    launch_uncovered(false, x, (hipStream_t)stream);
     return train_launched("attention");
 }
 
@@ -1209,23 +1250,25 @@ opt_status opt_attention_backward(const opt_attention_desc* a, const opt_attenti
     AttnArgs x = attn_args(a);
     const bool no_q = x.q_tokens == 0 || a->q_len == 0 || a->batch == 0;
     const bool no_k = x.k_tokens == 0 || a->k_len == 0 || a->batch == 0;
+    const bool no_dq = x.q_tokens == 0, no_dk = x.k_tokens == 0;   // nothing to write
     if (opt_status st = tensor(a, dout, "dout", no_q, x.dout)) return st;
     if (opt_status st = tensor(a, q, "q", no_q, x.q)) return st;
     if (opt_status st = tensor(a, k, "k", no_k, x.k)) return st;
     if (opt_status st = tensor(a, v, "v", no_k, x.v)) return st;
     if (opt_status st = tensor(a, out, "out", no_q, x.o)) return st;
     if (!no_q && (!lse || !train_aligned(lse, 4))) return fail(OPT_EINVAL, "lse is NULL or not aligned to 4 bytes");
-    if (opt_status st = output(a, dq, "dq", no_q, a->heads, a->q_len, x.dq)) return st;
-    if (opt_status st = output(a, dk, "dk", no_k, a->kv_heads, a->k_len, x.dk)) return st;
-    if (opt_status st = output(a, dv, "dv", no_k, a->kv_heads, a->k_len, x.dv)) return st;
+    if (opt_status st = output(a, dq, "dq", no_dq, a->heads, a->q_len, x.dq)) return st;
+    if (opt_status st = output(a, dk, "dk", no_dk, a->kv_heads, a->k_len, x.dk)) return st;
+    if (opt_status st = output(a, dv, "dv", no_dk, a->kv_heads, a->k_len, x.dv)) return st;
     const Space space = space_of(x, true);
     if (opt_status st = check_workspace(workspace, workspace_bytes, space.bytes)) return st;
-    if (no_q && no_k) return OPT_OK;
+    if (no_dq && no_dk) return OPT_OK;
     if (opt_status st = train_pending()) return st;
     x.lse = (float*)lse;
     use_space(x, space, workspace);
     if (!no_q) launch(DQ, a->dtype, x, (hipStream_t)stream);
     if (!no_k) launch(DKV, a->dtype, x, (hipStream_t)stream);
+    launch_uncovered(true, x, (hipStream_t)stream);
     return train_launched("attention backward");
 }
 

@@ -168,7 +168,8 @@ def attention_forward(q, k, v, *, causal=False, window=0, scale=None, q_start=No
     axis. Packed sequences: q, k, v without the batch axis, q_start and k_start
     int32 offsets of batch + 1, max_q and max_k the longest lengths. Padded
     batches: q_lens, k_lens int32 lengths. lse is fp32, (heads, all query
-    tokens). scale defaults to dim^-1/2."""
+    tokens). scale defaults to dim^-1/2. Tokens outside every sequence, past a
+    length or past max_q or max_k are not read; out is 0 and lse -inf there."""
     a, dev, per_row = _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens)
     st = _stream(dev)
     o = _out(out, "out", q, dev)
@@ -185,7 +186,7 @@ def attention_backward(dout, q, k, v, out, lse, *, causal=False, window=0, scale
                        max_q=None, max_k=None, q_lens=None, k_lens=None, dq=None, dk=None, dv=None):
     """(dq, dk, dv) from the output's gradient and what attention_forward took
     and returned. dq, dk, dv may be given, for instance as views of one
-    projection's gradient."""
+    projection's gradient. They are 0 for tokens outside every sequence."""
     a, dev, per_row = _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens)
     for t, name in ((dout, "dout"), (out, "out")):
         if not (t.dtype == q.dtype and t.device == dev and t.shape == q.shape):

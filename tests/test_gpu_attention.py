@@ -465,3 +465,45 @@ def test_equal_bits_with_wavefronts_that_skip_tiles():
         one = {x: c[x][a:a + m] for x in ("out", "dq", "dk", "dv")} | {"lse": c["lse"][:, a:a + m]}
         check_sequence(q[a:a + m], k[a:a + m], v[a:a + m], dout[a:a + m], one, 128 ** -0.5, T.visible(m, m, True), U["bf16"])
         a += m
+
+
+@pytest.mark.parametrize("window", [0, 5])
+@pytest.mark.parametrize("case", ["gaps", "cut", "no sequences", "no lengths"])
+def test_packed_tokens_outside_every_sequence_are_zeros(case, window):
+    """Before the first sequence, after the last one and past max_q or max_k: outputs and gradients 0, lse -inf, in
+    memory that held NaN before."""
+    torch, train = _torch(), _train()
+    print(f"attention packed, uncovered {case} {window}", flush=True)
+    ti = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    nq, nk, h, hk, d = 700, 900, 4, 2, 64
+    qs, ks, mq, mk_ = {"gaps": ([3, 3, 200, 650], [100, 130, 400, 890], 450, 490),
+                       "cut": ([0, 300, 300, 700], [0, 20, 500, 900], 130, 70),
+                       "no sequences": ([0], [0], 10, 10), "no lengths": ([0, 700], [0, 900], 0, 0)}[case]
+    g = torch.Generator(device="cuda").manual_seed(16)
+    mk = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    q, k, v, dout = mk(nq, h, d), mk(nk, hk, d), mk(nk, hk, d), mk(nq, h, d)
+    cover = lambda s, most, n: [(a, min(max(b, a), a + most)) for a, b in zip(s[:-1], s[1:])]  # noqa: E731
+    cq, ck = cover(qs, mq, nq), cover(ks, mk_, nk)
+    for t, c in ((q, cq), (dout, cq), (k, ck), (v, ck)):   # never read either
+        keep = torch.zeros(len(t), dtype=torch.bool, device="cuda")
+        for a, b in c:
+            keep[a:b] = True
+        t[~keep] = float("nan")
+    how = dict(causal=True, window=window, q_start=ti(qs), k_start=ti(ks), max_q=mq, max_k=mk_)
+    bad = lambda like: torch.full_like(like, float("nan"))  # noqa: E731
+    for given in (False, True):
+        held = [bad(q) for _ in range(6)] + [bad(k) for _ in range(4)] + [torch.full((h, nq), float("nan"), device="cuda")]
+        del held
+        out, lse = train.attention_forward(q, k, v, out=bad(q) if given else None, **how)
+        more = dict(dq=bad(q), dk=bad(k), dv=bad(k)) if given else {}
+        dq, dk, dv = train.attention_backward(dout, q, k, v, out, lse, **how, **more)
+        got = {n: np64(t) for n, t in (("out", out), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv))}
+        for (a, m), (c, n) in zip(cq, ck):
+            one = {x: got[x][a:m] for x in ("out", "dq")} | {x: got[x][c:n] for x in ("dk", "dv")}
+            check_sequence(np64(q[a:m]), np64(k[c:n]), np64(v[c:n]), np64(dout[a:m]), one | {"lse": got["lse"][:, a:m]},
+                           d ** -0.5, T.visible(m - a, n - c, True, window), U["bf16"])
+            got["out"][a:m], got["dq"][a:m], got["lse"][:, a:m] = 0, 0, -np.inf
+            got["dk"][c:n], got["dv"][c:n] = 0, 0
+        for x in ("out", "dq", "dk", "dv"):
+            assert (got[x] == 0).all(), x
+        assert np.isneginf(got["lse"]).all()
