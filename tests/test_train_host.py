@@ -262,3 +262,13 @@ def test_policy_backward_takes_the_forward_calls_scale(N, monkeypatch):
     train.policy_loss_backward(x, t, four)
     train.policy_loss_backward(x, t, four, logit_scale=0.5)
     assert seen == [1.0, 0.5]
+
+
+def test_packed_outputs_whose_tokens_overlap_are_refused(N):
+    """Sequences of one token share no row with each other either."""
+    a = desc(N, batch=3, q_len=1, k_len=1, q_start=BASE, k_start=BASE, q_tokens=3, k_tokens=3)
+    ok, bad, ws = tensor(N), tensor(N, t=0), N.opt_attention_workspace_size(a, 1)
+    refused(N, N.OPT_EINVAL, N.opt_attention_forward, a, ok, ok, ok, bad, BASE, 0, 0, 0)
+    for at in range(3):
+        grads = [bad if n == at else ok for n in range(3)]
+        refused(N, N.OPT_EINVAL, N.opt_attention_backward, a, *[ok] * 5, BASE, *grads, BASE, ws - 1, 0)
