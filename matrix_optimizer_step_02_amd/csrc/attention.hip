@@ -751,6 +751,17 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
         store_t<T, DB>(dq, a.scale, rows_of(a.dq, b, sq.q0, hq) + (int64_t)i * a.dq.token, a.head_dim);
 }
 
+// The dK/dV kernel holds P times 2^kLift<T>. float16 has steps of 2^-24 below
+// 2^-14, which a P of 1 / n is at n keys seen alike: 1.3 % off, all to one
+// side, at 10^6, and 0 from 2^25. Lifted by 2^14 it is a normal number down to
+// 2^-28 (sequences have at most 2^29 tokens), and P = 1, with room for the
+// rounding of large scores, stays below float16's largest, 2^16. dP - D is
+// lowered by as much in the operation that forms it, and dV where it is stored.
+template <class T>
+constexpr int kLift = __is_same(T, _Float16) ? 14 : 0;
+template <class T>
+constexpr float kLower = 1.f / (1 << kLift<T>);
+
 // dK and dV of 32 W keys, summed over the queries that see them and over the
 // heads of the group; the steps are (head, query tile). A lane owns one key.
 // The keys' accumulators (128 registers at head_dim 128) and operands (64)
@@ -825,8 +836,8 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
             float L = INFINITY, D = 0.f;
             if (i < sq.nq) {
                 L = gptr(a.lse)[at] * kLog2e;
-                if (L == -INFINITY) L = INFINITY;
-                D = gptr(a.delta)[at];
+                L = L == -INFINITY ? INFINITY : L - kLift<T>;
+                D = gptr(a.delta)[at] * kLower<T>;
             }
             stat[set][r & 1][0][lane] = L;
             stat[set][r & 1][1][lane] = D;
@@ -867,7 +878,7 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     s[4 * g + e] = __builtin_amdgcn_exp2f(fmaf(s[4 * g + e], c, -L[e]));
-                    dp[4 * g + e] = s[4 * g + e] * (dp[4 * g + e] - D[e]);
+                    dp[4 * g + e] = s[4 * g + e] * fmaf(dp[4 * g + e], kLower<T>, -D[e]);
                 }
             }
 #pragma unroll
@@ -920,7 +931,7 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
     if (SETS == 1 || set == 0)
         store_t<T, DB>(dk, a.scale, rows_of(a.dk, b, sq.k0, hk) + (int64_t)j * a.dk.token, a.head_dim);
     if (SETS == 1 || set == 1)
-        store_t<T, DB>(dv, 1.f, rows_of(a.dv, b, sq.k0, hk) + (int64_t)j * a.dv.token, a.head_dim);
+        store_t<T, DB>(dv, kLower<T>, rows_of(a.dv, b, sq.k0, hk) + (int64_t)j * a.dv.token, a.head_dim);
 }
 
 // Adds the splits of dK and dV: eight columns a thread, 16 threads a row.
@@ -940,7 +951,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kv_kernel(AttnArgs a, 
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += v[e];
     }
-    const float mul = v_part ? 1.f : a.scale;
+    const float mul = v_part ? kLower<T> : a.scale;
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] *= mul;
     const Tensor& t = v_part ? a.dv : a.dk;

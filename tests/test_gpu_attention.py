@@ -507,3 +507,26 @@ def test_packed_tokens_outside_every_sequence_are_zeros(case, window):
         for x in ("out", "dq", "dk", "dv"):
             assert (got[x] == 0).all(), x
         assert np.isneginf(got["lse"]).all()
+
+
+def test_half_precision_value_gradients_over_many_keys():
+    """Each of n keys that are seen alike has the probability 1 / n: far below float16's normal numbers, and no less
+    exact. dv_j = dout / n is off by the two roundings, u each, and the fp32 arithmetic's 2^-12."""
+    torch, train = _torch(), _train()
+    n = 10 ** 6
+    print("attention f16, keys", n, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(17)
+    q = torch.zeros(1, 1, 1, 64, device="cuda").half()
+    k, v = (torch.randn(1, n, 1, 64, generator=g, device="cuda").half() for _ in range(2))
+    dout = (1000 * (1 + torch.rand(1, 1, 1, 64, generator=g, device="cuda"))).half()
+    out, lse = train.attention_forward(q, k, v)
+    dq, dk, dv = train.attention_backward(dout, q, k, v, out, lse)
+    want = dout.double() / n   # above 2^-14 everywhere
+    assert ((dv.double() - want).abs() <= (2 * U["f16"] + SLACK) * want).all()
+
+
+@pytest.mark.parametrize("nq,nk,causal", [(3000, 100, False), (2000, 130, True), (100, 4000, True)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_half_precision_over_splits(nq, nk, causal, d):
+    """Queries (or keys) split over workgroups, whose fp32 parts a second kernel joins."""
+    dense(1, nq, nk, 2, 1, d, dtype="f16", causal=causal, seed=nq + d)
