@@ -272,3 +272,13 @@ def test_packed_outputs_whose_tokens_overlap_are_refused(N):
     for at in range(3):
         grads = [bad if n == at else ok for n in range(3)]
         refused(N, N.OPT_EINVAL, N.opt_attention_backward, a, *[ok] * 5, BASE, *grads, BASE, ws - 1, 0)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Kernels are launched on the current device: its default stream has the same handle as every other device's."""
+    from matrix_optimizer_step_02_amd import train
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 64 + index)
+    assert train._stream(torch.device("cuda", 0)) == 64
+    with pytest.raises(ValueError, match="current device"):
+        train._stream(torch.device("cuda", 1))
