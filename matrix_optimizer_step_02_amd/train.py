@@ -41,16 +41,32 @@ class Rng(NamedTuple):
         return native.opt_rng(self.seed & m, self.offset & m, d.data_ptr() if d is not None else 0)
 
 
+def _tensors(values):
+    for x in values:
+        if isinstance(x, torch.Tensor):
+            yield x
+        elif isinstance(x, tuple):   # Rng, PolicyForward
+            yield from _tensors(x)
+            yield from _tensors((getattr(x, "lse_rest", None),))
+
+
 def _streamed(fn):
     """Gives fn a ``stream`` argument. Everything of the call happens there:
     the kernels, the copies it may need, and the allocation of what it returns
-    (so that no memory is taken that the current stream may still be using)."""
+    (so that no memory is taken that the current stream may still be using).
+    The tensors it was given are recorded on that stream: their memory is not
+    handed out again before the stream is past the call. It does not wait for
+    what writes them, nor the current stream for its results."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         if stream is None:
             return fn(*args, **kw)
         with torch.cuda.stream(stream):
-            return fn(*args, **kw)
+            result = fn(*args, **kw)
+        for t in _tensors((*args, *kw.values())):
+            if t.is_cuda:
+                t.record_stream(stream)
+        return result
     return call
 
 

@@ -249,3 +249,25 @@ def test_more_rows_than_one_launch_holds():
     assert torch.equal(h, train.dropout(x, 0.25, train.Rng(5, 9)))
     y2, _, mean2, rstd2 = train.layer_norm_forward(h[-part:].contiguous(), w)
     assert torch.equal(y[-part:], y2) and torch.equal(mean[-part:], mean2) and torch.equal(rstd[-part:], rstd2)
+
+
+def test_memory_of_a_call_on_another_stream_is_not_handed_out_early():
+    """An input dropped after a call on another stream keeps its memory until that stream is past the call."""
+    torch, train = _torch(), _train()
+    print("dropout, dropped input", flush=True)
+    x = torch.randn(3001, 5003, device="cuda")
+    rng = train.Rng(3, 4)
+    want = train.dropout(x, 0.3, rng)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        busy = torch.randn(4096, 4096, device="cuda")
+        for _ in range(20):
+            busy = busy @ busy / 64
+    at = x.data_ptr()
+    got = train.dropout(x, 0.3, rng, stream=s)
+    del x
+    other = [torch.full((3001, 5003), float("nan"), device="cuda") for _ in range(3)]
+    assert all(t.data_ptr() != at for t in other)
+    s.synchronize()
+    assert torch.equal(got, want)

@@ -282,3 +282,28 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     assert train._stream(torch.device("cuda", 0)) == 64
     with pytest.raises(ValueError, match="current device"):
         train._stream(torch.device("cuda", 1))
+
+
+def test_a_calls_tensors_are_recorded_on_its_stream(monkeypatch):
+    """The allocator keeps their memory until that stream is done with it."""
+    import contextlib
+
+    from matrix_optimizer_step_02_amd import train
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    seen = []
+
+    class Fake(torch.Tensor):
+        is_cuda = True
+
+        def record_stream(self, s):
+            seen.append((int(self.numel()), s))
+
+    mk = lambda n: torch.zeros(n).as_subclass(Fake)  # noqa: E731
+    fwd = train.PolicyForward(mk(3), mk(4), mk(5), mk(6))
+    fwd.lse_rest = mk(7)
+    call = train._streamed(lambda *a, **kw: None)
+    call(mk(1), 0.5, fwd, train.Rng(1, 2, mk(8)), out=mk(2), eps=1e-5, none=None, stream="s")
+    assert sorted(seen) == [(n, "s") for n in range(1, 9)]
+    del seen[:]
+    call(mk(1), out=mk(2))   # on the current stream
+    assert not seen
