@@ -5,8 +5,9 @@ Functions check their tensors, allocate what they return and call the C entry
 points of include/matopt_train.h on the current stream, or on the one given as
 ``stream``. There is no autograd graph: a backward function is called with what its
 forward function returned, and its results are ordinary tensors (a weight's
-gradient goes into the G of a RotatedAdamGroup). All shapes and argument errors
-raise before anything is launched.
+gradient goes into the G of a RotatedAdamGroup). Tensors that require a
+gradient are therefore refused, except under torch.no_grad(). All shapes and
+argument errors raise before anything is launched.
 """
 
 from __future__ import annotations
@@ -59,6 +60,12 @@ def _streamed(fn):
     what writes them, nor the current stream for its results."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
+        if torch.is_grad_enabled():
+            for values in args, kw.values():
+                for t in values:
+                    if isinstance(t, torch.Tensor) and t.requires_grad:
+                        raise ValueError(f"{fn.__name__} keeps no graph for a tensor that requires a gradient: call it "
+                                         "under torch.no_grad(), and the backward function for the gradient")
         if stream is None:
             return fn(*args, **kw)
         with torch.cuda.stream(stream):

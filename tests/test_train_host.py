@@ -307,3 +307,23 @@ def test_a_calls_tensors_are_recorded_on_its_stream(monkeypatch):
     del seen[:]
     call(mk(1), out=mk(2))   # on the current stream
     assert not seen
+
+
+def test_tensors_that_require_a_gradient_are_refused_unless_gradients_are_off(N, monkeypatch):
+    """There is no graph that would carry the gradient on: results that look whole would lose it."""
+    from matrix_optimizer_step_02_amd import train
+    monkeypatch.setattr(train, "_stream", lambda dev: 0)
+    for name in ("opt_attention_forward", "opt_layer_norm_forward", "opt_dropout", "opt_policy_loss_forward"):
+        monkeypatch.setattr(N, name, lambda *a: None)
+    x, w, v = torch.zeros(3, 8), torch.zeros(8), torch.zeros(3)
+    t, g = torch.zeros(3, dtype=torch.int64), lambda z: z.clone().requires_grad_()   # noqa: E731
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    calls = [lambda f: train.layer_norm_forward(f(x), w), lambda f: train.layer_norm_forward(x, f(w)),
+             lambda f: train.layer_norm_forward(x, w, residual=f(x)), lambda f: train.dropout(f(x), 0.5, train.Rng(1)),
+             lambda f: train.attention_forward(q, f(q), q), lambda f: train.policy_loss_forward(f(x), t, v, v, v)]
+    for call in calls:
+        call(lambda z: z)
+        with pytest.raises(ValueError, match="gradient"):
+            call(g)
+        with torch.no_grad():
+            call(g)
