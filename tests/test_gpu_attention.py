@@ -530,3 +530,51 @@ def test_half_precision_value_gradients_over_many_keys():
 def test_half_precision_over_splits(nq, nk, causal, d):
     """Queries (or keys) split over workgroups, whose fp32 parts a second kernel joins."""
     dense(1, nq, nk, 2, 1, d, dtype="f16", causal=causal, seed=nq + d)
+
+
+def some(batch, heads, kv, d, dtype, causal, n=300, pick=3):
+    """Like dense, but only a few of the sequences are compared."""
+    torch = _torch()
+    print(f"attention {batch}x{n} heads {heads}/{kv} d {d} {dtype} causal {causal}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(d + batch)
+    mk = lambda h: torch.randn(batch, n, h, d, generator=g, device="cuda").to(_dt(dtype))  # noqa: E731
+    q, k, v, dout = mk(heads), mk(kv), mk(kv), mk(heads)
+    got = run(q, k, v, dout, causal=causal)
+    lse = got["lse"].view(heads, batch, n)
+    for b in sorted({0, batch // 2, batch - 1})[:pick]:
+        one = {x: np64(got[x][b]) for x in ("out", "dq", "dk", "dv")} | {"lse": np64(lse[:, b])}
+        check_sequence(np64(q[b]), np64(k[b]), np64(v[b]), np64(dout[b]), one, d ** -0.5, T.visible(n, n, causal), U[dtype])
+    assert all(t.isfinite().all() for t in got.values())
+
+
+# Blocks of 128 rows times heads: up to 256 take two sets of wavefronts, below 1024 one set of four, from there eight
+@pytest.mark.parametrize("batch,heads,kv", [(7, 16, 16), (14, 16, 8), (22, 16, 16), (43, 16, 8)])
+@pytest.mark.parametrize("d", [72, 96, 128])
+@pytest.mark.parametrize("dtype,causal", [("bf16", True), ("bf16", False), ("f16", True), ("f16", False)])
+def test_wide_heads_in_every_workgroup_shape(batch, heads, kv, d, dtype, causal):
+    """Forward, dQ and dK/dV of 300 tokens (a ragged tail in each shape's last block): 336 and 672 blocks, 1056 and 2064."""
+    some(batch, heads, kv, d, dtype, causal)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,count", [(96, 60), (128, 60), (128, 300)])
+def test_wide_heads_of_many_packed_sequences(d, count, dtype):
+    """Enough packed blocks for eight wavefronts a workgroup, found in the list and (past 256 sequences) without it."""
+    torch = _torch()
+    print(f"attention packed wide {d} {count} {dtype}", flush=True)
+    rng = np.random.default_rng(count + d)
+    lens = [int(x) for x in rng.integers(0, 300 if count == 60 else 60, count)]
+    lens[1], lens[count // 2], lens[-1] = 0, 517, 1
+    g = torch.Generator(device="cuda").manual_seed(count)
+    mk = lambda h: torch.randn(sum(lens), h, d, generator=g, device="cuda").to(_dt(dtype))  # noqa: E731
+    q, k, v, dout = mk(16), mk(16), mk(16), mk(16)
+    at = np.concatenate([[0], np.cumsum(lens)])
+    st = torch.tensor(at, dtype=torch.int32, device="cuda")
+    got = run(q, k, v, dout, causal=True, q_start=st, k_start=st, max_q=517, max_k=517)
+    assert all(t.isfinite().all() for t in got.values())
+    for b in (0, 1, 2, count // 2, count - 1):
+        a, e = int(at[b]), int(at[b + 1])
+        if e > a:
+            one = {x: np64(got[x][a:e]) for x in ("out", "dq", "dk", "dv")} | {"lse": np64(got["lse"][:, a:e])}
+            check_sequence(np64(q[a:e]), np64(k[a:e]), np64(v[a:e]), np64(dout[a:e]), one, d ** -0.5,
+                           T.visible(e - a, e - a, True), U[dtype])
