@@ -262,10 +262,15 @@ def _size(t):
     return (t.numel() // cols if cols else 0), cols
 
 
-def _p_rng(p, rng):
+def _p_rng(p, rng, dev):
     if p > 0 and rng is None:
         raise ValueError("dropout needs an rng")
-    return rng.c() if rng is not None and p > 0 else None
+    if rng is None or not p > 0:
+        return None
+    c = rng.c()
+    if rng.device_offset is not None and rng.device_offset.device != dev:
+        raise ValueError(f"device_offset is on {rng.device_offset.device}, expected {dev}")
+    return c
 
 
 @_streamed
@@ -273,7 +278,7 @@ def dropout(x, p, rng, *, residual=None, out=None):
     """residual + dropout(x) (no residual: dropout(x)); out may be x or
     residual. The mask depends on rng and on an element's position in x
     (leading axes as rows, the last axis as columns)."""
-    dev, dt, bits = x.device, _code(x, "x"), _p_rng(p, rng)
+    dev, dt, bits = x.device, _code(x, "x"), _p_rng(p, rng, x.device)
     rows, cols = _size(x)
     y = _out(out, "out", x, dev)
     xp, ldx = _rows(x, "x")
@@ -301,7 +306,7 @@ def layer_norm_forward(x, weight, bias=None, *, eps=1e-5, residual=None, p=0.0, 
     """(y, h, mean, rstd): h = residual + dropout(x) in the residual's type,
     y its norm over the last axis in x's type. Without residual and dropout h
     is x. weight and bias are fp32."""
-    dev, dt, bits = x.device, _code(x, "x"), _p_rng(p, rng)
+    dev, dt, bits = x.device, _code(x, "x"), _p_rng(p, rng, x.device)
     rows, cols = _size(x)
     y = _out(out, "out", x, dev)
     xp, ldx = _rows(x, "x")
@@ -330,7 +335,7 @@ def layer_norm_backward(dy, h, weight, mean, rstd, *, dh=None, p=0.0, rng=None, 
     layer_norm_forward returned; dh is the gradient that reaches h past the
     norm. dres, h's gradient, goes to the residual; without dropout and in the
     same type it is dx itself. residual_grad=False: dres is None."""
-    dev, dt, bits = dy.device, _code(dy, "dy"), _p_rng(p, rng)
+    dev, dt, bits = dy.device, _code(dy, "dy"), _p_rng(p, rng, dy.device)
     rows, cols = _size(dy)
     hdt, shape = _code(h, "h"), dy.shape
     if not (h.device == dev and h.shape == shape):

@@ -327,3 +327,18 @@ def test_tensors_that_require_a_gradient_are_refused_unless_gradients_are_off(N,
             call(g)
         with torch.no_grad():
             call(g)
+
+
+def test_a_step_counter_of_another_device_is_refused(N):
+    """Kernels read it on the tensors' device."""
+    from types import SimpleNamespace
+
+    from matrix_optimizer_step_02_amd import train
+    far = SimpleNamespace(dtype=torch.int64, numel=lambda: 1, device=torch.device("cuda", 1), data_ptr=lambda: BASE)
+    with pytest.raises(ValueError, match="device_offset"):
+        train.dropout(torch.zeros(4, 8), 0.5, train.Rng(0, 0, far))
+    with pytest.raises(ValueError, match="device_offset"):
+        train.layer_norm_forward(torch.zeros(4, 8), torch.zeros(8), p=0.5, rng=train.Rng(0, 0, far))
+    with pytest.raises(ValueError, match="device_offset"):
+        train.layer_norm_backward(torch.zeros(4, 8), torch.zeros(4, 8), torch.zeros(8), torch.zeros(4), torch.zeros(4),
+                                  p=0.5, rng=train.Rng(0, 0, far))
