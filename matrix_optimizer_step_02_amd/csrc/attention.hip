@@ -968,7 +968,8 @@ __global__ __launch_bounds__(kGapThreads) void attn_uncovered_kernel(AttnArgs a,
     const bool keys = blockIdx.z;
     const int32_t* start = keys ? a.k_start : a.q_start;
     const int64_t tokens = keys ? a.k_tokens : a.q_tokens;
-    const int most = keys ? a.k_len : a.q_len, groups = a.head_dim / 8, each = (keys ? a.kv_heads : a.heads) * groups;
+    const int most = keys ? a.k_len : a.q_len, groups = a.head_dim / 8;
+    const int64_t each = (int64_t)(keys ? a.kv_heads : a.heads) * groups;
     const Tensor t = keys ? a.dk : backward ? a.dq : a.o;
     const u32x4 zero = {};
     for (int64_t gap = blockIdx.x; gap <= a.batch; gap += gridDim.x) {
@@ -981,7 +982,7 @@ __global__ __launch_bounds__(kGapThreads) void attn_uncovered_kernel(AttnArgs a,
         if (gap < a.batch) to = packed(start, tokens, most, (int)gap, n);
         for (int64_t i = (int64_t)blockIdx.y * kGapThreads + threadIdx.x; i < (to - from) * each; i += (int64_t)gridDim.y * kGapThreads) {
             const int64_t row = from + i / each;
-            const int h = (int)(i % each) / groups, c = (int)(i % each) % groups;
+            const int h = (int)(i % each / groups), c = (int)(i % each % groups);
             *gptr((u32x4*)(rows_of(t, 0, row, h) + 16 * c)) = zero;
             if (keys) *gptr((u32x4*)(rows_of(a.dv, 0, row, h) + 16 * c)) = zero;
             if (!backward && c == 0) gptr(a.lse)[(int64_t)h * a.q_tokens + row] = -INFINITY;
