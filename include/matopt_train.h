@@ -49,8 +49,13 @@ enum { OPT_F16 = 2 };
  * which needs causal, also j > i + n_k - n_q - window. A query that sees no
  * key has O = 0, L = -inf, dQ = 0. Keys and queries past a sequence's length
  * are not read, whatever they hold; a non-finite key or value inside the
- * length may reach a query whose causal bound or window hides it (0 times
- * infinity).
+ * length may reach a query whose causal bound or window hides it, and a
+ * non-finite query or dO a key it does not see (0 times infinity).
+ *
+ * P and dS enter matrix instructions in dtype. OPT_F16 holds dS in steps of
+ * 2^-24 below 2^-14 and up to 65504, as it does dQ, dK and dV: scale the loss
+ * so that they lie between. (P is kept clear of both.) Scores S are fp32, which
+ * tells them apart up to 2^24.
  */
 typedef struct {
     int32_t dtype;            /* OPT_BF16 or OPT_F16: every tensor but lse */
@@ -160,7 +165,7 @@ opt_status opt_layer_norm_backward(int64_t rows, int64_t cols, int32_t dtype, co
 typedef struct {
     int32_t dtype;             /* of logits and dlogits: OPT_F32, OPT_BF16 or OPT_F16 */
     int32_t target_i64;        /* targets are int64_t (else int32_t) */
-    int64_t rows, vocab;       /* rows < 2^31, vocab < 2^31 */
+    int64_t rows, vocab;       /* rows < 2^31, vocab < 2^31 - 2^16; backward: vocab <= 2^29 - 2^13 */
     int64_t ld;                /* row stride of logits */
     float logit_scale, clip_low, clip_high, kl_coef;
     /* rows floats (may be NULL): lse is rounded to fp32, off by up to

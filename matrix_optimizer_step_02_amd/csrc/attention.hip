@@ -28,6 +28,21 @@
 // sits in slot q ^ swz(r); with swz taking the low two row bits as the high
 // slot bits, both the reads of 16 rows at one group (A operands) and of four
 // rows at four groups (transposed) touch every bank once.
+//
+// Precision. The matrix instructions take 16-bit operands, so P and dS are
+// rounded once each where they enter one (half a step of the tensors' type);
+// S, dP, L, D and every sum are fp32, and D is of the rounded O, which is what
+// the caller holds. Holding P or dS as two 16-bit parts would double the
+// products that take it.
+//
+// What bounds it. The matrix units are busy 47 to 58 % of the time at the
+// clock measured (8192 x 8192, 16 heads of 128). The copies of the next tile
+// are issued before the products of this one, but the compiler, which cannot
+// tell the two tiles' LDS apart, waits for them before the first transposed
+// read: in the dQ kernel after 16 of 48 products, with two sets of wavefronts
+// also in the forward kernel, after 16 of 32 (not with one set). In the dK/dV
+// kernel the wait stands before the first product: the loads of L and D, which
+// follow the copies, complete in order behind them.
 #include "train.h"
 
 namespace matopt {
@@ -256,7 +271,8 @@ __device__ __forceinline__ float other_half(float x) {
     return __uint_as_float((threadIdx.x & 63) < 32 ? r[1] : r[0]);
 }
 
-// Registers 8 k .. 8 k + 7 of an accumulator, rounded to 16 bits.
+// Registers 8 k .. 8 k + 7 of an accumulator, rounded to 16 bits: P or dS as
+// an operand.
 template <class T>
 __device__ __forceinline__ typename Frag<T>::type pack8(const f32x16& x, int k) {
     typename Frag<T>::type f;
@@ -766,7 +782,9 @@ constexpr float kLower = 1.f / (1 << kLift<T>);
 // heads of the group; the steps are (head, query tile). A lane owns one key.
 // The keys' accumulators (128 registers at head_dim 128) and operands (64)
 // leave little of the 256 registers that two wavefronts a SIMD have, so the
-// addresses are computed where they are used. At head_dim <= 64 a workgroup of
+// addresses are computed where they are used; past head_dim 96 some are
+// spilled all the same (12 bytes a lane with two sets, 20 with one) and read
+// back in each step. At head_dim <= 64 a workgroup of
 // four is held to 168 registers, three wavefronts a SIMD: 68 us against 78 (6 x
 // 1000 tokens, 16 heads of 64).
 template <class T, int DB, int W, int SETS>
