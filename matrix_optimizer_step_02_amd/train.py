@@ -58,14 +58,19 @@ def _streamed(fn):
     The tensors it was given are recorded on that stream: their memory is not
     handed out again before the stream is past the call. It does not wait for
     what writes them, nor the current stream for its results."""
+    needs_no_grad = (f"{fn.__name__} keeps no graph for a tensor that requires a gradient: call it under "
+                     "torch.no_grad(), and the backward function for the gradient")
+    grad_enabled, tensor = torch.is_grad_enabled, torch.Tensor
+
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        if torch.is_grad_enabled():
-            for values in args, kw.values():
-                for t in values:
-                    if isinstance(t, torch.Tensor) and t.requires_grad:
-                        raise ValueError(f"{fn.__name__} keeps no graph for a tensor that requires a gradient: call it "
-                                         "under torch.no_grad(), and the backward function for the gradient")
+        if grad_enabled():
+            for t in args:
+                if isinstance(t, tensor) and t.requires_grad:
+                    raise ValueError(needs_no_grad)
+            for t in kw.values():
+                if isinstance(t, tensor) and t.requires_grad:
+                    raise ValueError(needs_no_grad)
         if stream is None:
             return fn(*args, **kw)
         with torch.cuda.stream(stream):
