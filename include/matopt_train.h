@@ -6,6 +6,10 @@
  *                    recomputes the probabilities from the saved log-sums
  *   layer norm       with the residual sum and dropout in the same pass, and
  *                    the backward pass with the weight's and bias's gradients
+ *   rotary           position rotation of queries and keys, and its gradient
+ *   qk norm          norms of queries and keys per head with the rotation in
+ *                    the same pass, and the backward pass with the weights'
+ *                    gradients
  *   dropout          from a counter-based generator; no mask is stored
  *   policy loss      clipped policy-gradient loss with a KL term on logits,
  *                    forward, backward, or both in one pass over the logits
@@ -98,6 +102,64 @@ opt_status opt_attention_backward(const opt_attention_desc* a, const opt_attenti
                                   const opt_attention_tensor* dq, const opt_attention_tensor* dk,
                                   const opt_attention_tensor* dv, void* workspace, uint64_t workspace_bytes,
                                   void* stream);
+
+/* --------------------------------------------------------------- rotary ----
+ *
+ * Pair i of a head at position p turns by the angle p f_i:
+ *   (a, b) -> scale (a cos - b sin, b cos + a sin)
+ * Layout HALF pairs element i with i + rot / 2, PAIRS 2 i with 2 i + 1; the
+ * elements from rot on stay as they are (unscaled). The gradient is the same call
+ * with inverse set: it turns by -p f_i.
+ *
+ * Frequencies are given as turns[i] = round(2^64 f_i / (2 pi)) mod 2^64, so that
+ * p turns[i] mod 2^64 is the angle in 2^-64 turns, exact but for that rounding
+ * (|p| 2^-65 turns). Angles, sines and the rotation are fp32 (the fraction of a
+ * turn is cut at 2^-32); y is rounded once.
+ */
+enum { OPT_ROTARY_HALF = 0, OPT_ROTARY_PAIRS = 1 };
+typedef struct {
+    const uint64_t* turns;     /* rot / 2, device */
+    int32_t rot, layout;       /* rot even, 2 <= rot <= head_dim */
+    float scale;               /* > 0: of cosine and sine */
+    int32_t positions_i64;     /* positions are int64_t (else int32_t); any value */
+    const void* positions;     /* device, (batch, tokens) by strides >= 0; NULL: first + index along the tokens */
+    int64_t position_batch_stride, position_token_stride, first;
+} opt_rotary;
+
+/* Queries (batch, tokens, heads, head_dim) and keys (kv_heads; 0: no keys, and
+ * what belongs to them is ignored). Tensors have strides in elements, a contiguous
+ * last axis and one element's alignment; opt_attention_tensor describes them. */
+typedef struct {
+    int32_t dtype;             /* OPT_F32, OPT_BF16 or OPT_F16, of all but weights and statistics */
+    int32_t heads, kv_heads, head_dim;   /* heads, kv_heads <= 65536, head_dim <= 512 */
+    int64_t batch, tokens;     /* batch * tokens < 2^31 */
+} opt_heads_desc;
+
+/* yq may be q and yk may be k (same strides). */
+opt_status opt_rotary_apply(const opt_heads_desc* d, const opt_rotary* r, int32_t inverse, const opt_attention_tensor* q,
+                            const opt_attention_tensor* k, const opt_attention_tensor* yq,
+                            const opt_attention_tensor* yk, void* stream);
+
+/* -------------------------------------------------------------- qk norm ----
+ *
+ *   y = R(x rstd w),  rstd = 1 / sqrt(mean(x^2) + eps) over a head's elements
+ * backward, with R the rotation of opt_rotary_apply (r NULL: none):
+ *   g = R^T dy,  z = g w,  xh = x rstd,  dx = rstd (z - xh mean(z xh)),  dw = sum g xh
+ * Weights (head_dim) and their gradients are fp32, one for all heads of q and one
+ * for those of k; rstd is fp32, (batch, tokens, heads) contiguous. yq may be q, dq
+ * may be dyq or q (same strides), and so for k.
+ */
+opt_status opt_qk_norm_forward(const opt_heads_desc* d, const opt_rotary* r, const opt_attention_tensor* q,
+                               const opt_attention_tensor* k, const float* q_weight, const float* k_weight, float eps,
+                               const opt_attention_tensor* yq, const opt_attention_tensor* yk, float* q_rstd,
+                               float* k_rstd, void* stream);
+opt_status opt_qk_norm_workspace_size(const opt_heads_desc* d, uint64_t* bytes);   /* backward; 256-byte aligned */
+opt_status opt_qk_norm_backward(const opt_heads_desc* d, const opt_rotary* r, const opt_attention_tensor* dyq,
+                                const opt_attention_tensor* dyk, const opt_attention_tensor* q,
+                                const opt_attention_tensor* k, const float* q_weight, const float* k_weight,
+                                const float* q_rstd, const float* k_rstd, const opt_attention_tensor* dq,
+                                const opt_attention_tensor* dk, float* dq_weight, float* dk_weight, void* workspace,
+                                uint64_t workspace_bytes, void* stream);
 
 /* -------------------------------------------------------------- dropout ----
  *

@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(HERE, "_lib", "libmatopt.so")
 OPT_OK, OPT_EINVAL, OPT_ENOWS, OPT_EHIP, OPT_EUNSUPPORTED, OPT_ESTATE = 0, -1, -2, -3, -4, -5
 OPT_F32, OPT_BF16 = 0, 1
 OPT_F16 = 2   # the training-pass operators only
+OPT_ROTARY_HALF, OPT_ROTARY_PAIRS = 0, 1
 OPT_FLAG_ROTATED_MOMENTUM = 1
 OPT_FLAG_BF16_ROTATION = 2
 OPT_FLAG_MUON = 4
@@ -41,6 +42,7 @@ EXPORTED_TRAIN = (
     "opt_attention_workspace_size", "opt_attention_forward", "opt_attention_backward", "opt_dropout",
     "opt_layer_norm_forward", "opt_layer_norm_workspace_size", "opt_layer_norm_backward",
     "opt_policy_loss_workspace_size", "opt_policy_loss_forward", "opt_policy_loss_backward", "opt_policy_loss_step",
+    "opt_rotary_apply", "opt_qk_norm_forward", "opt_qk_norm_workspace_size", "opt_qk_norm_backward",
 )
 
 
@@ -90,6 +92,19 @@ class opt_attention_tensor(C.Structure):
 
 class opt_rng(C.Structure):
     _fields_ = [("seed", C.c_uint64), ("offset", C.c_uint64), ("device_offset", C.c_void_p)]
+
+
+class opt_rotary(C.Structure):
+    _fields_ = [
+        ("turns", C.c_void_p), ("rot", C.c_int32), ("layout", C.c_int32), ("scale", C.c_float),
+        ("positions_i64", C.c_int32), ("positions", C.c_void_p), ("position_batch_stride", C.c_int64),
+        ("position_token_stride", C.c_int64), ("first", C.c_int64),
+    ]
+
+
+class opt_heads_desc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("heads", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("batch", C.c_int64), ("tokens", C.c_int64)]
 
 
 class opt_policy_desc(C.Structure):
@@ -164,6 +179,13 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         "opt_policy_loss_forward": ([P, vp, PR, vp, vp, vp, vp, vp, u64, vp], i32),
         "opt_policy_loss_backward": ([P, vp, vp, vp, vp, vp, vp, i64, vp], i32),
         "opt_policy_loss_step": ([P, vp, PR, f32, vp, vp, vp, i64, vp, u64, vp], i32),
+    }
+    Q, RO = C.POINTER(opt_heads_desc), C.POINTER(opt_rotary)
+    sig |= {
+        "opt_rotary_apply": ([Q, RO, i32, T, T, T, T, vp], i32),
+        "opt_qk_norm_forward": ([Q, RO, T, T, vp, vp, f32, T, T, vp, vp, vp], i32),
+        "opt_qk_norm_workspace_size": ([Q, C.POINTER(u64)], i32),
+        "opt_qk_norm_backward": ([Q, RO, T, T, T, T, vp, vp, vp, vp, T, T, vp, vp, vp, u64, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -405,3 +427,24 @@ def opt_policy_loss_step(a, logits: int, rows, grad: float, loss: int, logp: int
                          workspace: int, workspace_bytes: int, stream_ptr: int):
     _check(load().opt_policy_loss_step(a, logits, rows, grad, loss, logp, dlogits, ldd, workspace, workspace_bytes,
                                        stream_ptr))
+
+
+def opt_rotary_apply(d, r, inverse: int, q, k, yq, yk, stream_ptr: int):
+    _check(load().opt_rotary_apply(d, r, inverse, q, k, yq, yk, stream_ptr))
+
+
+def opt_qk_norm_forward(d, r, q, k, q_weight: int, k_weight: int, eps: float, yq, yk, q_rstd: int, k_rstd: int,
+                        stream_ptr: int):
+    _check(load().opt_qk_norm_forward(d, r, q, k, q_weight, k_weight, eps, yq, yk, q_rstd, k_rstd, stream_ptr))
+
+
+def opt_qk_norm_workspace_size(d) -> int:
+    out = C.c_uint64(0)
+    _check(load().opt_qk_norm_workspace_size(d, out))
+    return out.value
+
+
+def opt_qk_norm_backward(d, r, dyq, dyk, q, k, q_weight: int, k_weight: int, q_rstd: int, k_rstd: int, dq, dk,
+                         dq_weight: int, dk_weight: int, workspace: int, workspace_bytes: int, stream_ptr: int):
+    _check(load().opt_qk_norm_backward(d, r, dyq, dyk, q, k, q_weight, k_weight, q_rstd, k_rstd, dq, dk, dq_weight,
+                                       dk_weight, workspace, workspace_bytes, stream_ptr))

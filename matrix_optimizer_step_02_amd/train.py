@@ -1,5 +1,6 @@
-"""The training pass's operators on torch tensors: attention, layer norm,
-dropout and the clipped policy loss, each with its backward pass.
+"""The training pass's operators on torch tensors: attention, position rotation,
+norms of queries and keys, layer norm, dropout and the clipped policy loss, each
+with its backward pass.
 
 Functions check their tensors, allocate what they return and call the C entry
 points of include/matopt_train.h on the current stream, or on the one given as
@@ -13,14 +14,18 @@ argument errors raise before anything is launched.
 from __future__ import annotations
 
 import functools
+import math
+from fractions import Fraction
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import native
 
-__all__ = ["Rng", "attention_forward", "attention_backward", "dropout", "dropout_backward", "layer_norm_forward",
-           "layer_norm_backward", "PolicyForward", "policy_loss_forward", "policy_loss_backward", "policy_loss_step"]
+__all__ = ["Rng", "attention_forward", "attention_backward", "rotary_frequencies", "Rotary", "rotary_forward",
+           "rotary_backward", "qk_norm_forward", "qk_norm_backward", "dropout", "dropout_backward",
+           "layer_norm_forward", "layer_norm_backward", "PolicyForward", "policy_loss_forward",
+           "policy_loss_backward", "policy_loss_step"]
 
 _HALF = {torch.bfloat16: native.OPT_BF16, torch.float16: native.OPT_F16}
 _DTYPE = {torch.float32: native.OPT_F32, torch.bfloat16: native.OPT_BF16, torch.float16: native.OPT_F16}
@@ -234,6 +239,223 @@ def attention_backward(dout, q, k, v, out, lse, *, causal=False, window=0, scale
                                   _bhtd(out, "out"), lse.data_ptr(), _bhtd(gq, "dq"), _bhtd(gk, "dk"),
                                   _bhtd(gv, "dv"), ws.data_ptr() if n else 0, n, st)
     return gq, gk, gv
+
+
+# --------------------------------------------------- rotary and qk norm ----
+
+
+def rotary_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_length=0, low=1.0, high=32.0):
+    """(frequencies, scale) for Rotary: f_i = base^(-2 i / rot), i < rot / 2, in
+    64 bits. Scaled for contexts ``factor`` times as long:
+
+    * "linear": f_i / factor.
+    * "base": the base is raised to base factor^(rot / (rot - 2)), which divides
+      the lowest frequency by factor and leaves the highest.
+    * "ramp": f_i / factor for pairs that turn fewer than ``low`` times over
+      ``original_length`` positions, f_i for those that turn more than ``high``
+      times, linear in the number of turns between, and scale = 1 + 0.1 ln factor
+      (Peng, Quesnel, Fan, Shippole: "YaRN", 2023)."""
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and >= 2")
+    if not (base > 0 and math.isfinite(base)):
+        raise ValueError("base must be positive and finite")
+    if scaling is not None and not (factor >= 1 and math.isfinite(factor)):
+        raise ValueError("factor must be >= 1 and finite")
+    if scaling == "base":
+        if rot == 2:
+            raise ValueError("scaling of the base needs rot > 2")
+        base = base * factor ** (rot / (rot - 2))
+    f = [base ** (-2 * i / rot) for i in range(rot // 2)]
+    if scaling in (None, "base"):
+        return f, 1.0
+    if scaling == "linear":
+        return [x / factor for x in f], 1.0
+    if scaling != "ramp":
+        raise ValueError(f"scaling is {scaling!r}, expected None, 'linear', 'base' or 'ramp'")
+    if not (original_length > 0 and high > low):
+        raise ValueError("scaling by a ramp needs original_length > 0 and high > low")
+    keep = [min(max((x * original_length / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for x in f]
+    return [x * k + x / factor * (1 - k) for x, k in zip(f, keep)], 1.0 + 0.1 * math.log(factor)
+
+
+_TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+class _Rotary(NamedTuple):
+    turns: torch.Tensor
+    rot: int
+    layout: int
+    scale: float
+
+
+class Rotary(_Rotary):
+    """What turns queries and keys: a program makes it once. ``frequencies``:
+    radians a position, one per pair (2 len(frequencies) elements of a head are
+    turned). layout "half" pairs element i with i + rot / 2, "pairs" 2 i with
+    2 i + 1. ``scale``: factor of cosine and sine."""
+
+    def __new__(cls, frequencies, *, layout="half", scale=1.0, device="cuda"):
+        if layout not in ("half", "pairs"):
+            raise ValueError(f"layout is {layout!r}, expected 'half' or 'pairs'")
+        f = [float(x) for x in frequencies]
+        if not f or not all(math.isfinite(x) for x in f):
+            raise ValueError("frequencies must be finite, one at least")
+        if not (scale > 0 and math.isfinite(scale)):
+            raise ValueError("scale must be positive and finite")
+        # 2^64 f / (2 pi), rounded and reduced to one turn, as the two's complement that int64 holds
+        turns = [round(Fraction(x) / _TWO_PI * (1 << 64)) % (1 << 64) for x in f]
+        table = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+        code = native.OPT_ROTARY_HALF if layout == "half" else native.OPT_ROTARY_PAIRS
+        return super().__new__(cls, table, 2 * len(f), code, float(scale))
+
+    def c(self, positions, first, dev, lead):
+        """The descriptor for tokens of shape ``lead``, (batch, tokens) or (tokens,)."""
+        if self.turns.device != dev:
+            raise ValueError(f"rope is on {self.turns.device}, expected {dev}")
+        if positions is None:
+            return native.opt_rotary(self.turns.data_ptr(), self.rot, self.layout, self.scale, 0, 0, 0, 0, first)
+        if first:
+            raise ValueError("first goes without positions")
+        if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
+            raise ValueError("positions must be an int32 or int64 tensor")
+        shape = positions.shape
+        if positions.device != dev or (shape != lead and shape != lead[-1:]):
+            _is(positions, "positions", dev, positions.dtype, lead)
+        s = positions.stride()
+        return native.opt_rotary(self.turns.data_ptr(), self.rot, self.layout, self.scale,
+                                 positions.dtype == torch.int64, positions.data_ptr(), s[0] if len(s) == 2 else 0,
+                                 s[-1])
+
+
+def _heads(q, k, names):
+    """(descriptor, device, leading shape) of queries and keys (k may be None)."""
+    code, dim = _code(q, names[0]), q.dim()
+    if dim not in (3, 4):
+        raise ValueError(f"{names[0]} must have axes (batch, tokens, heads, dim) or (tokens, heads, dim)")
+    qs, ks = q.shape, None if k is None else k.shape
+    if k is not None and not (k.dtype == q.dtype and k.device == q.device and len(ks) == dim
+                              and ks[:-2] == qs[:-2] and ks[-1] == qs[-1]):
+        _is(k, names[1], q.device, q.dtype)
+        raise ValueError(f"{names[1]} has shape {tuple(ks)}, expected {tuple(qs)} but for the heads")
+    d = native.opt_heads_desc(code, qs[-2], 0 if k is None else ks[-2], qs[-1], qs[0] if dim == 4 else 1, qs[-3])
+    return d, q.device, qs[:-2]
+
+
+def _like(t, name, like, dev):
+    if not (t.dtype == like.dtype and t.device == dev and t.shape == like.shape):
+        _is(t, name, dev, like.dtype, like.shape)
+    return t
+
+
+def _rotary(names, q, k, rope, positions, first, out_q, out_k, inverse):
+    d, dev, lead = _heads(q, k, names)
+    if not isinstance(rope, Rotary):
+        raise TypeError("rope must be a Rotary")
+    r = rope.c(positions, first, dev, lead)
+    st = _stream(dev)
+    yq = q.new_empty(q.shape) if out_q is None else _like(out_q, names[2], q, dev)
+    tq, ty = _bhtd(q, names[0]), _bhtd(yq, names[2])
+    if k is None:
+        native.opt_rotary_apply(d, r, inverse, tq, None, ty, None, st)
+        return yq, None
+    yk = k.new_empty(k.shape) if out_k is None else _like(out_k, names[3], k, dev)
+    native.opt_rotary_apply(d, r, inverse, tq, _bhtd(k, names[1]), ty, _bhtd(yk, names[3]), st)
+    return yq, yk
+
+
+@_streamed
+def rotary_forward(q, k, rope, positions=None, *, first=0, out_q=None, out_k=None):
+    """(yq, yk): queries (batch, tokens, heads, dim) and keys (batch, tokens,
+    kv_heads, dim), or both without the batch axis, turned by ``rope`` at their
+    positions: an int32 or int64 tensor (batch, tokens) or (tokens,), or first + the
+    index along the tokens. k may be None. out_q may be q and out_k may be k."""
+    return _rotary(("q", "k", "out_q", "out_k"), q, k, rope, positions, first, out_q, out_k, 0)
+
+
+@_streamed
+def rotary_backward(dyq, dyk, rope, positions=None, *, first=0, dq=None, dk=None):
+    """(dq, dk) from the gradients of rotary_forward's results. dq and dk may be
+    given, for instance as views of one projection's gradient, or be dyq and dyk."""
+    return _rotary(("dyq", "dyk", "dq", "dk"), dyq, dyk, rope, positions, first, dq, dk, 1)
+
+
+def _rope(rope, positions, first, dev, lead):
+    if rope is None:
+        if positions is not None or first:
+            raise ValueError("positions go with a rope")
+        return None
+    if not isinstance(rope, Rotary):
+        raise TypeError("rope must be a Rotary or None")
+    return rope.c(positions, first, dev, lead)
+
+
+@_streamed
+def qk_norm_forward(q, k, q_weight, k_weight, *, eps=1e-6, rope=None, positions=None, first=0, out_q=None, out_k=None):
+    """(yq, yk, q_rstd, k_rstd): each head's row divided by its root mean square
+    and multiplied by a weight (dim, fp32; one for queries, one for keys), then
+    turned as rotary_forward turns it (rope None: not turned). k may be None, and
+    with it what belongs to keys. out_q may be q and out_k may be k (but the
+    backward pass needs q and k)."""
+    d, dev, lead = _heads(q, k, ("q", "k"))
+    r = _rope(rope, positions, first, dev, lead)
+    wq = _vector(q_weight, "q_weight", dev, d.head_dim)
+    st = _stream(dev)
+    yq = q.new_empty(q.shape) if out_q is None else _like(out_q, "out_q", q, dev)
+    q_rstd = q_weight.new_empty(q.shape[:-1])
+    if k is None:
+        native.opt_qk_norm_forward(d, r, _bhtd(q, "q"), None, wq, 0, eps, _bhtd(yq, "out_q"), None,
+                                   q_rstd.data_ptr(), 0, st)
+        return yq, None, q_rstd, None
+    wk = _vector(k_weight, "k_weight", dev, d.head_dim)
+    yk = k.new_empty(k.shape) if out_k is None else _like(out_k, "out_k", k, dev)
+    k_rstd = k_weight.new_empty(k.shape[:-1])
+    native.opt_qk_norm_forward(d, r, _bhtd(q, "q"), _bhtd(k, "k"), wq, wk, eps, _bhtd(yq, "out_q"), _bhtd(yk, "out_k"),
+                               q_rstd.data_ptr(), k_rstd.data_ptr(), st)
+    return yq, yk, q_rstd, k_rstd
+
+
+def _statistic(t, name, dev, shape):
+    if not (t.dtype == torch.float32 and t.device == dev and t.shape == shape):
+        _is(t, name, dev, torch.float32, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+@_streamed
+def qk_norm_backward(dyq, dyk, q, k, q_weight, k_weight, q_rstd, k_rstd, *, rope=None, positions=None, first=0, dq=None,
+                     dk=None):
+    """(dq, dk, dq_weight, dk_weight) from the gradients of qk_norm_forward's
+    results, what it took and the rstd it returned. dq and dk may be given, for
+    instance as views of one projection's gradient, or be dyq and dyk."""
+    d, dev, lead = _heads(q, k, ("q", "k"))
+    r = _rope(rope, positions, first, dev, lead)
+    for t, name, like in ((dyq, "dyq", q), (dyk, "dyk", k)):
+        if like is not None:
+            _like(t, name, like, dev)
+    if dyq.stride(-1) != 1:   # an expanded gradient has stride 0
+        dyq = dyq.contiguous()
+    if k is not None and dyk.stride(-1) != 1:
+        dyk = dyk.contiguous()
+    wq = _vector(q_weight, "q_weight", dev, d.head_dim)
+    sq = _statistic(q_rstd, "q_rstd", dev, q.shape[:-1])
+    st = _stream(dev)
+    gq = q.new_empty(q.shape) if dq is None else _like(dq, "dq", q, dev)
+    gwq = q_weight.new_empty(d.head_dim)
+    n = native.opt_qk_norm_workspace_size(d)
+    ws = _bytes(q, n)
+    wp = ws.data_ptr() if n else 0
+    if k is None:
+        native.opt_qk_norm_backward(d, r, _bhtd(dyq, "dyq"), None, _bhtd(q, "q"), None, wq, 0, sq, 0, _bhtd(gq, "dq"),
+                                    None, gwq.data_ptr(), 0, wp, n, st)
+        return gq, None, gwq, None
+    wk = _vector(k_weight, "k_weight", dev, d.head_dim)
+    sk = _statistic(k_rstd, "k_rstd", dev, k.shape[:-1])
+    gk = k.new_empty(k.shape) if dk is None else _like(dk, "dk", k, dev)
+    gwk = k_weight.new_empty(d.head_dim)
+    native.opt_qk_norm_backward(d, r, _bhtd(dyq, "dyq"), _bhtd(dyk, "dyk"), _bhtd(q, "q"), _bhtd(k, "k"), wq, wk, sq, sk,
+                                _bhtd(gq, "dq"), _bhtd(gk, "dk"), gwq.data_ptr(), gwk.data_ptr(), wp, n, st)
+    return gq, gk, gwq, gwk
 
 
 # ---------------------------------------------------------------- dropout ----

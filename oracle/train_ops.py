@@ -118,3 +118,33 @@ def policy_loss(x, target, old, ref, adv, w, lo, hi, kl, scale=1.0, grad=1.0):
         dx[i, target[i]] += 1
         dx[i] *= grad * scale * slope[i]
     return {"loss": term.sum(), "logp": logp, "lse": lse, "slope": slope, "dlogits": dx, "term": term}
+
+
+# --------------------------------------------------- rotary and qk norm ----
+
+
+def rotary(x, positions, frequencies, layout="half", scale=1.0, inverse=False):
+    """x (tokens, heads, dim), positions (tokens,) integers. Angles from exact integer positions: the product with a
+    frequency is reduced by whole turns in extended precision."""
+    turns = np.asarray(positions, dtype=np.longdouble)[:, None] * (
+        np.asarray(frequencies, dtype=np.longdouble) / (2 * np.longdouble("3.14159265358979323846264338327950288")))
+    angle = ((turns - np.round(turns)) * 2).astype(np.float64)[:, None] * np.pi
+    c, s = scale * np.cos(angle), scale * np.sin(angle) * (-1 if inverse else 1)
+    rot, y = 2 * len(frequencies), x.copy()
+    a, b = (slice(0, rot // 2), slice(rot // 2, rot)) if layout == "half" else (slice(0, rot, 2), slice(1, rot, 2))
+    y[..., a], y[..., b] = x[..., a] * c - x[..., b] * s, x[..., b] * c + x[..., a] * s
+    return y
+
+
+def rms_norm(x, w, eps):
+    """Rows along the last axis: y, rstd, xh."""
+    rstd = 1 / np.sqrt((x ** 2).mean(-1) + eps)
+    xh = x * rstd[..., None]
+    return {"y": xh * w, "rstd": rstd, "xh": xh}
+
+
+def rms_norm_backward(g, x, w, eps):
+    f = rms_norm(x, w, eps)
+    z, xh = g * w, f["xh"]
+    dx = f["rstd"][..., None] * (z - xh * (z * xh).mean(-1, keepdims=True))
+    return {"dx": dx, "dw": (g * xh).reshape(-1, x.shape[-1]).sum(0), "z": z} | f

@@ -1,0 +1,356 @@
+"""GPU tests of position rotation and of norms of queries and keys with it,
+against the fp64 oracle.
+
+Bounds, with e = 2^-24 and u = eps / 2 of the storage type. A sine or cosine is
+off by at most 2 e (its polynomial) + e / 2 (scale) + e / 32 (a fraction of a turn
+cut at 2^-32), 3 e in all, relative to scale; a product, a sum and fp32's rounding
+add 2 e. float16 holds what is below 2^-14 in steps of 2^-24 (2^-25 off).
+  rotation: u |y| + 5 e scale (|a| + |b|) + 2^-25
+  norm:     a sum of up to 512 squares, 16 a lane and a tree of 5 levels, is off by
+            24 e of itself, rstd by 2^-19 with its division and root
+  y:  u |y| + scale (5 e + 2^-18) (|z_a| + |z_b|),  z = xh w
+  g:  e_g = 5 e scale (|dy_a| + |dy_b|)
+  dx: u |dx| + rstd (|w| e_g + 2^-17 (|z| + |xh| mean|z xh|) + |xh| mean(|w| e_g |xh|))
+  dw: sum(e_g |xh|) + (2^-18 + (rows + 16) e) sum |g xh|   (in the worst order of addition)
+"""
+
+import numpy as np
+import pytest
+
+from oracle import train_ops as T
+
+pytestmark = pytest.mark.gpu
+
+U = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}
+E, TINY = 2.0 ** -24, 2.0 ** -25
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _train():
+    from matrix_optimizer_step_02_amd import train
+    return train
+
+
+def _dt(name):
+    torch = _torch()
+    return {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[name]
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def inside(got, ref, bound, what):
+    assert got.shape == ref.shape, what
+    assert np.isfinite(got).all(), what
+    r = float(np.max(np.abs(got - ref) / (bound + TINY))) if ref.size else 0.0
+    assert r <= 1, f"{what}: {r}"
+
+
+def randn(*shape, seed=0, dtype="bf16", mul=1.0):
+    torch = _torch()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (mul * torch.randn(*shape, generator=g, device="cuda")).to(_dt(dtype))
+
+
+def freqs(rot, factor=1.0):
+    return [10000.0 ** (-2 * i / rot) / factor for i in range(rot // 2)]
+
+
+def partner_sum(x, rot, layout):
+    """|a| + |b| at both elements of a pair; 0 past rot."""
+    y, m = np.zeros_like(x), np.abs(x)
+    if rot:
+        a, b = (slice(0, rot // 2), slice(rot // 2, rot)) if layout == "half" else (slice(0, rot, 2), slice(1, rot, 2))
+        y[..., a] = y[..., b] = m[..., a] + m[..., b]
+    return y
+
+
+def positions_of(pos, b, tokens):
+    """(tokens,) numpy positions of sequence b."""
+    p = pos.cpu().numpy()
+    return p if p.ndim == 1 else p[b]
+
+
+def check_rotated(x, y, pos, f, layout, scale, dtype, inverse=False, what="y"):
+    """x, y: (batch, tokens, heads, dim) tensors."""
+    rot = 2 * len(f)
+    for b in range(x.shape[0]):
+        xs = np64(x[b])
+        ref = T.rotary(xs, pos(b), f, layout, scale, inverse)
+        inside(np64(y[b]), ref, U[dtype] * np.abs(ref) + 5 * E * scale * partner_sum(xs, rot, layout), what)
+
+
+@pytest.mark.parametrize("dim,rot", [(2, 2), (7, 4), (16, 16), (32, 32), (64, 16), (72, 36), (80, 44), (96, 96), (100, 50),
+                                     (128, 128), (128, 126), (192, 64), (256, 256), (512, 512), (511, 510)])
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_rotation(dim, rot, layout, dtype):
+    torch, train = _torch(), _train()
+    print(f"rotary dim {dim} rot {rot} {layout} {dtype}", flush=True)
+    q, k = randn(2, 19, 5, dim, dtype=dtype, seed=dim), randn(2, 19, 2, dim, dtype=dtype, seed=dim + 1)
+    f = freqs(rot, 2.0)
+    rope = train.Rotary(f, layout=layout, scale=1.25)
+    pos = torch.randint(-(2 ** 31), 2 ** 31 - 1, (2, 19), device="cuda", dtype=torch.int32)
+    yq, yk = train.rotary_forward(q, k, rope, pos)
+    dq, dk = train.rotary_backward(q, k, rope, pos)
+    torch.cuda.synchronize()
+    at = lambda b: positions_of(pos, b, 19)  # noqa: E731
+    for x, y, d in ((q, yq, dq), (k, yk, dk)):
+        check_rotated(x, y, at, f, layout, 1.25, dtype)
+        check_rotated(x, d, at, f, layout, 1.25, dtype, inverse=True, what="gradient")
+
+
+@pytest.mark.parametrize("tokens,heads,kv", [(1, 1, 0), (1, 16, 8), (2, 3, 1), (63, 24, 24), (257, 1, 1), (1000, 16, 4), (4097, 4, 2)])
+def test_rotation_sizes(tokens, heads, kv):
+    torch, train = _torch(), _train()
+    print(f"rotary sizes {tokens} {heads} {kv}", flush=True)
+    q = randn(tokens, heads, 64, seed=tokens)
+    k = randn(tokens, kv, 64, seed=tokens + 1) if kv else None
+    rope = train.Rotary(freqs(64))
+    yq, yk = train.rotary_forward(q, k, rope, first=12345)
+    torch.cuda.synchronize()
+    at = lambda b: 12345 + np.arange(tokens)  # noqa: E731
+    check_rotated(q[None], yq[None], at, freqs(64), "half", 1.0, "bf16")
+    if kv:
+        check_rotated(k[None], yk[None], at, freqs(64), "half", 1.0, "bf16")
+    else:
+        assert yk is None
+
+
+def test_far_positions():
+    """An angle is as exact at 2^62 as at 1: the table holds 64 bits of a turn, the oracle's extended precision as many."""
+    torch, train = _torch(), _train()
+    print("rotary far positions", flush=True)
+    far = [0, 1, -1, 2 ** 31 - 1, -2 ** 31, 2 ** 24 + 1, 10 ** 9 + 7, 2 ** 31 + 5]
+    pos = torch.tensor(far, device="cuda", dtype=torch.int64)
+    x = randn(len(far), 2, 64, dtype="f32")
+    rope = train.Rotary(freqs(64), layout="pairs")
+    y, _ = train.rotary_forward(x, None, rope, pos)
+    check_rotated(x[None], y[None], lambda b: np.array(far), freqs(64), "pairs", 1.0, "f32")
+    # positions that differ by a whole number of turns of a frequency of pi / 2 turn alike, up to the ends of 64 bits
+    rope = train.Rotary([np.pi / 2], layout="pairs")
+    pos = torch.tensor([3, 2 ** 40 + 3, -2 ** 40 + 3], device="cuda")
+    y, _ = train.rotary_forward(x[:1, :1, :2].expand(3, 1, 2), None, rope, pos)
+    assert float((y - y[:1]).abs().max()) < 1e-3   # pi / 2 in 64 bits is 2^-54 off, times 2^40
+    train.rotary_forward(x[:2], None, rope, torch.tensor([2 ** 63 - 1, -2 ** 63], device="cuda"))
+    train.rotary_backward(x[:2], None, rope, torch.tensor([2 ** 63 - 1, -2 ** 63], device="cuda"))
+    torch.cuda.synchronize()
+
+
+def test_strides_positions_and_places():
+    """Views of one projection, unaligned ones, broadcast positions, results in place and into given views."""
+    torch, train = _torch(), _train()
+    print("rotary strides", flush=True)
+    for dim, dtype in ((72, "bf16"), (64, "f16"), (40, "f32")):
+        wide = randn(3, 33, 12 * dim + 3, dtype=dtype, seed=dim)
+        whole = wide[..., 1:1 + 12 * dim].unflatten(-1, (12, dim))
+        q, k, v = whole.split([7, 3, 2], dim=2)
+        f = freqs(dim - 8)
+        rope = train.Rotary(f, scale=0.5)
+        pos = torch.randint(0, 100000, (33,), device="cuda")
+        at = lambda b: pos.cpu().numpy()  # noqa: E731
+        yq, yk = train.rotary_forward(q, k, rope, pos)
+        check_rotated(q, yq, at, f, "half", 0.5, dtype)
+        check_rotated(k, yk, at, f, "half", 0.5, dtype)
+        yq2, yk2 = train.rotary_forward(q, k, rope, pos[None].expand(3, 33))
+        assert torch.equal(yq, yq2) and torch.equal(yk, yk2)
+        before, vs = wide.clone(), v.clone()
+        a, b = train.rotary_forward(q, k, rope, pos, out_q=q, out_k=k)
+        assert a is q and b is k
+        assert torch.equal(q, yq) and torch.equal(k, yk) and torch.equal(v, vs)
+        assert torch.equal(wide[..., :1], before[..., :1]) and torch.equal(wide[..., -2:], before[..., -2:])
+        t = q.transpose(0, 1)   # (tokens, batch, ...): strides out of order
+        y, _ = train.rotary_forward(t, None, rope, first=5)
+        check_rotated(t, y, lambda b: 5 + np.arange(3), f, "half", 0.5, dtype)
+        one = q[:, :, :1].expand(3, 33, 4, dim)   # one head, four times
+        y, _ = train.rotary_forward(one, None, rope, pos)
+        assert torch.equal(y[:, :, 0], y[:, :, 3])
+        torch.cuda.synchronize()
+
+
+def test_past_2_31_elements():
+    torch, train = _torch(), _train()
+    print("rotary past 2^31 elements", flush=True)
+    tokens, heads, dim = 2200, 8192, 128
+    x = torch.empty(tokens, heads, dim, device="cuda", dtype=torch.bfloat16)
+    x.normal_()
+    y, _ = train.rotary_forward(x, None, train.Rotary(freqs(dim)), first=7)
+    torch.cuda.synchronize()
+    for t in (0, 1024, 2199):
+        check_rotated(x[None, t:t + 1, -3:], y[None, t:t + 1, -3:], lambda b: [7 + t], freqs(dim), "half", 1.0, "bf16")
+
+
+# ---------------------------------------------------------------- qk norm ----
+
+
+def check_norm(q, w, d, pos, f, layout, scale, eps, dtype, y, rstd, dx, dw, what):
+    """One tensor (batch, tokens, heads, dim) with its weight and the gradient of its result."""
+    rot, dim = 2 * len(f), q.shape[-1]
+    u, ww = U[dtype], np64(w)
+    ref_dw, bound_dw, total = np.zeros(dim), np.zeros(dim), np.zeros(dim)
+    for b in range(q.shape[0]):
+        x, g0 = np64(q[b]), np64(d[b])
+        turn = (lambda z, inv=False: T.rotary(z, pos(b), f, layout, scale, inv)) if rot else (lambda z, inv=False: z)  # noqa: B023
+        n = T.rms_norm(x, ww, eps)
+        ref = turn(n["y"])
+        inside(np64(rstd[b]), n["rstd"], 2.0 ** -19 * n["rstd"], what + " rstd")
+        mag = scale * partner_sum(n["y"], rot, layout)
+        mag[..., rot:] = np.abs(n["y"][..., rot:])
+        inside(np64(y[b]), ref, u * np.abs(ref) + (5 * E + 2.0 ** -18) * mag, what + " y")
+        r = T.rms_norm_backward(turn(g0, True), x, ww, eps)
+        g = turn(g0, True)
+        eg = 5 * E * scale * partner_sum(g0, rot, layout)
+        xh, z = np.abs(r["xh"]), np.abs(r["z"])
+        bound = u * np.abs(r["dx"]) + r["rstd"][..., None] * (
+            np.abs(ww) * eg + 2.0 ** -17 * (z + xh * (z * xh).mean(-1, keepdims=True))
+            + xh * (np.abs(ww) * eg * xh).mean(-1, keepdims=True))
+        inside(np64(dx[b]), r["dx"], bound, what + " dx")
+        ref_dw += r["dw"]
+        bound_dw += (eg * xh).reshape(-1, dim).sum(0)
+        total += (np.abs(g) * xh).reshape(-1, dim).sum(0)
+    rows = q.shape[0] * q.shape[1] * q.shape[2]
+    inside(np64(dw), ref_dw, bound_dw + (2.0 ** -18 + (rows + 16) * E) * total, what + " dw")
+
+
+def norm_case(batch, tokens, heads, kv, dim, rot, layout="half", dtype="bf16", scale=1.0, eps=1e-6, mul=1.0, seed=0):
+    torch, train = _torch(), _train()
+    print(f"qk norm {batch}x{tokens} heads {heads}/{kv} dim {dim} rot {rot} {layout} {dtype}", flush=True)
+    qkv = randn(batch, tokens, heads + 2 * kv, dim, dtype=dtype, seed=seed, mul=mul)
+    q, k, _ = qkv.split([heads, kv, kv], dim=2)
+    wq, wk = 1 + 0.2 * randn(dim, dtype="f32", seed=seed + 1), 1 + 0.2 * randn(dim, dtype="f32", seed=seed + 2)
+    f = freqs(rot) if rot else []
+    rope = train.Rotary(f, layout=layout, scale=scale) if rot else None
+    pos = torch.randint(0, 1 << 20, (batch, tokens), device="cuda", dtype=torch.int32) if rot else None
+    at = lambda b: positions_of(pos, b, tokens)  # noqa: E731
+    yq, yk, sq, sk = train.qk_norm_forward(q, k, wq, wk, eps=eps, rope=rope, positions=pos)
+    gq, gk = randn(*yq.shape, dtype=dtype, seed=seed + 3), randn(*yk.shape, dtype=dtype, seed=seed + 4)
+    dqkv = torch.zeros_like(qkv)
+    a, b, _ = dqkv.split([heads, kv, kv], dim=2)
+    dq, dk, dwq, dwk = train.qk_norm_backward(gq, gk, q, k, wq, wk, sq, sk, rope=rope, positions=pos, dq=a, dk=b)
+    torch.cuda.synchronize()
+    assert dq is a and dk is b
+    check_norm(q, wq, gq, at, f, layout, scale, eps, dtype, yq, sq, dq, dwq, "q")
+    check_norm(k, wk, gk, at, f, layout, scale, eps, dtype, yk, sk, dk, dwk, "k")
+
+
+@pytest.mark.parametrize("dim,rot", [(2, 0), (8, 8), (32, 12), (72, 36), (80, 80), (96, 64), (101, 100), (128, 128), (128, 0),
+                                     (256, 128), (512, 512)])
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_norm(dim, rot, layout, dtype):
+    norm_case(2, 11, 6, 2, dim, rot, layout, dtype, scale=1.5 if rot else 1.0, seed=dim)
+
+
+@pytest.mark.parametrize("batch,tokens,heads,kv", [(1, 1, 1, 1), (16, 1, 16, 8), (1, 300, 5, 5), (3, 129, 12, 3), (1, 2049, 16, 8)])
+def test_norm_sizes(batch, tokens, heads, kv):
+    norm_case(batch, tokens, heads, kv, 128, 128, seed=tokens)
+
+
+@pytest.mark.parametrize("mul,eps", [(1e-4, 1e-6), (0.0, 1e-6), (100.0, 0.0)])
+def test_norm_scales(mul, eps):
+    """Rows of the size of eps, of zeros, and large ones."""
+    norm_case(1, 9, 4, 2, 64, 64, dtype="f32", mul=mul, eps=eps)
+
+
+def test_norm_gradient_is_the_difference_quotient():
+    """The gradient of a random functional against central differences in 64 bits of the kernel's own formula, by the
+    oracle's pins; here the kernels' forward pass itself, in fp32: steps of 2^-7 leave 2^-24 / 2^-7 of rounding a value."""
+    torch, train = _torch(), _train()
+    q, w = randn(1, 3, 2, 32, dtype="f32", seed=5), 1 + 0.2 * randn(32, dtype="f32", seed=6)
+    g = randn(1, 3, 2, 32, dtype="f32", seed=7)
+    rope = train.Rotary(freqs(32), layout="pairs")
+    _, _, sq, _ = train.qk_norm_forward(q, None, w, None, rope=rope)
+    dq, _, dw, _ = train.qk_norm_backward(g, None, q, None, w, None, sq, None, rope=rope)
+    loss = lambda q, w: float((train.qk_norm_forward(q, None, w, None, rope=rope)[0].double() * g.double()).sum())  # noqa: E731
+    h = 2.0 ** -7
+    for at in [(0, 0, 0, 0), (0, 1, 1, 17), (0, 2, 0, 31)]:
+        e = torch.zeros_like(q)
+        e[at] = h
+        # third derivatives of a row of unit rms are below 8 |g|: h^2 8 / 6, and 64 values' rounding over 2 h
+        assert abs((loss(q + e, w) - loss(q - e, w)) / (2 * h) - float(dq[at])) < 8 * 4 / 6 * h * h + 64 * 2.0 ** -22 / h
+    for at in (0, 13):
+        e = torch.zeros_like(w)
+        e[at] = h   # linear in the weight
+        assert abs((loss(q, w + e) - loss(q, w - e)) / (2 * h) - float(dw[at])) < 64 * 2.0 ** -22 / h
+
+
+def test_rows_do_not_mix():
+    """A head that holds NaN or infinities reaches its own results only; with zeros for a gradient nothing of dw."""
+    torch, train = _torch(), _train()
+    q = randn(2, 40, 6, 64, seed=3)
+    w = torch.ones(64, device="cuda")
+    rope = train.Rotary(freqs(64))
+    want = train.qk_norm_forward(q, None, w, None, rope=rope)
+    bad = q.clone()
+    bad[1, 7, 2, 5] = float("nan")
+    bad[0, 3, 4] = float("inf")
+    got = train.qk_norm_forward(bad, None, w, None, rope=rope)
+    rows = torch.ones(2, 40, 6, dtype=torch.bool, device="cuda")
+    rows[1, 7, 2] = rows[0, 3, 4] = False
+    assert torch.equal(got[0][rows], want[0][rows]) and torch.equal(got[2][rows], want[2][rows])
+    assert got[0][1, 7, 2].isnan().any()
+
+
+def test_no_tokens():
+    torch, train = _torch(), _train()
+    w = torch.ones(32, device="cuda")
+    for shape in ((0, 5, 2, 32), (3, 0, 2, 32)):
+        q = torch.empty(shape, device="cuda", dtype=torch.bfloat16)
+        yq, yk, sq, sk = train.qk_norm_forward(q, q, w, w, rope=train.Rotary(freqs(32)))
+        assert yq.shape == shape and sq.shape == shape[:-1]
+        dq, dk, dwq, dwk = train.qk_norm_backward(q, q, q, q, w, w, sq, sk)
+        assert not dwq.any() and not dwk.any() and dq.shape == shape
+        yq, _ = train.rotary_forward(q, q, train.Rotary(freqs(32)))
+        assert yq.shape == shape
+    torch.cuda.synchronize()
+
+
+def test_equal_inputs_give_equal_bits_and_graphs_replay():
+    torch, train = _torch(), _train()
+    print("qk norm in a graph", flush=True)
+    q, k = randn(1, 700, 8, 128, seed=1), randn(1, 700, 2, 128, seed=2)
+    wq, wk = torch.ones(128, device="cuda"), torch.ones(128, device="cuda")
+    pos = torch.arange(700, device="cuda")
+    rope = train.Rotary(freqs(128))
+    gq, gk = randn(1, 700, 8, 128, seed=3), randn(1, 700, 2, 128, seed=4)
+
+    def call():
+        yq, yk, sq, sk = train.qk_norm_forward(q, k, wq, wk, rope=rope, positions=pos)
+        rq, rk = train.rotary_forward(q, k, rope, pos)
+        return (yq, yk, rq, rk, *train.qk_norm_backward(gq, gk, q, k, wq, wk, sq, sk, rope=rope, positions=pos))
+
+    first = call()
+    assert all(torch.equal(a, b) for a, b in zip(first, call()))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for n in range(3):
+        pos.add_(1000 * n)
+        q.copy_(randn(1, 700, 8, 128, seed=10 + n))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), n
+
+
+def test_another_stream():
+    torch, train = _torch(), _train()
+    q = randn(1, 300, 8, 64, seed=1)
+    rope = train.Rotary(freqs(64))
+    want, _ = train.rotary_forward(q, None, rope)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got, _ = train.rotary_forward(q, None, rope, stream=s)
+    s.synchronize()
+    assert torch.equal(want, got)

@@ -1,0 +1,166 @@
+"""Host-side tests of position rotation and the norms of queries and keys: bad
+arguments are refused before the device is touched (no GPU needed)."""
+
+import ctypes as C
+import os
+
+import pytest
+import torch
+
+BASE = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def N():
+    from matrix_optimizer_step_02_amd import native
+    if not os.path.exists(native.LIB_PATH):
+        pytest.skip("libmatopt.so not built (run __graft_entry__.build())")
+    native.load()
+    return native
+
+
+def refused(N, status, fn, *args):
+    with pytest.raises(N.MatoptError) as e:
+        fn(*args)
+    assert e.value.status == getattr(N, "OPT_" + status), str(e.value)
+    assert len(str(e.value)) > 20
+
+
+def desc(N, **kw):
+    return N.opt_heads_desc(**(dict(dtype=N.OPT_BF16, heads=4, kv_heads=2, head_dim=64, batch=2, tokens=8) | kw))
+
+
+def rope(N, **kw):
+    base = dict(turns=BASE, rot=64, layout=0, scale=1.0, positions_i64=0, positions=BASE, position_batch_stride=8,
+                position_token_stride=1, first=0)
+    return N.opt_rotary(**(base | kw))
+
+
+def tensor(N, data=BASE, b=8 * 256, t=256, h=64):
+    return N.opt_attention_tensor(data, b, t, h)
+
+
+BAD_DESC = [(dict(dtype=3), "EUNSUPPORTED"), (dict(heads=0), "EINVAL"), (dict(kv_heads=-1), "EINVAL"),
+            (dict(heads=65537), "EUNSUPPORTED"), (dict(head_dim=0), "EINVAL"), (dict(head_dim=513), "EUNSUPPORTED"),
+            (dict(batch=-1), "EINVAL"), (dict(tokens=-1), "EINVAL"), (dict(tokens=1 << 31), "EUNSUPPORTED"),
+            (dict(batch=1 << 40, tokens=1 << 40), "EUNSUPPORTED"), (dict(batch=1 << 16, tokens=1 << 15), "EUNSUPPORTED")]
+BAD_ROPE = [(dict(turns=0), "EINVAL"), (dict(turns=BASE + 4), "EINVAL"), (dict(rot=0), "EINVAL"), (dict(rot=63), "EINVAL"),
+            (dict(rot=66), "EINVAL"), (dict(layout=2), "EINVAL"), (dict(scale=0.0), "EINVAL"),
+            (dict(scale=float("inf")), "EINVAL"), (dict(scale=float("nan")), "EINVAL"), (dict(positions=BASE + 2), "EINVAL"),
+            (dict(positions=BASE + 4, positions_i64=1), "EINVAL"), (dict(position_batch_stride=-1), "EINVAL"),
+            (dict(position_token_stride=-1), "EINVAL")]
+BAD_TENSOR = [dict(data=0), dict(data=BASE + 1), dict(b=-1), dict(t=-1), dict(h=-1)]
+OVERLAP = [dict(b=0), dict(t=0), dict(h=0), dict(h=63), dict(t=255), dict(t=64, h=64), dict(b=256 * 8 - 1)]
+
+
+def calls(N, d, r, ts, w=BASE, eps=1e-6, stat=BASE, ws=BASE, ws_bytes=1 << 40):
+    """The three calls on tensors ts: q, k, yq, yk, dyq, dyk, dq, dk."""
+    q, k, yq, yk, dyq, dyk, dq, dk = ts
+    return [(N.opt_rotary_apply, d, r, 0, q, k, yq, yk, 0),
+            (N.opt_qk_norm_forward, d, r, q, k, w, w, eps, yq, yk, stat, stat, 0),
+            (N.opt_qk_norm_backward, d, r, dyq, dyk, q, k, w, w, stat, stat, dq, dk, BASE, BASE, ws, ws_bytes, 0)]
+
+
+@pytest.mark.parametrize("kw,status", BAD_DESC)
+def test_descriptions_refused(N, kw, status):
+    for c in calls(N, desc(N, **kw), rope(N), [tensor(N)] * 8):
+        refused(N, status, *c)
+    refused(N, status, N.opt_qk_norm_workspace_size, desc(N, **kw))
+
+
+@pytest.mark.parametrize("kw,status", BAD_ROPE)
+def test_rotations_refused(N, kw, status):
+    for c in calls(N, desc(N), rope(N, **kw), [tensor(N)] * 8):
+        refused(N, status, *c)
+
+
+@pytest.mark.parametrize("at,call", [(0, 0), (1, 0), (2, 0), (3, 0), (0, 1), (1, 1), (2, 1), (3, 1), (0, 2), (1, 2), (4, 2),
+                                     (5, 2), (6, 2), (7, 2)])
+def test_tensors_refused(N, at, call):
+    for bad in BAD_TENSOR + (OVERLAP if at in (2, 3, 6, 7) else []):
+        ts = [tensor(N, **bad) if i == at else tensor(N) for i in range(8)]
+        if at in (3, 7) and bad in (dict(t=255), dict(b=256 * 8 - 1)):   # two key heads leave room
+            continue
+        refused(N, "EINVAL", *calls(N, desc(N), rope(N), ts)[call])
+    ts = [None if i == at else tensor(N) for i in range(8)]
+    refused(N, "EINVAL", *calls(N, desc(N), rope(N), ts)[call])
+
+
+def test_norm_arguments_refused(N):
+    ok = [tensor(N)] * 8
+    for kw in (dict(w=0), dict(w=BASE + 2), dict(stat=0), dict(stat=BASE + 2)):
+        for c in calls(N, desc(N), rope(N), ok, **kw)[1:]:
+            refused(N, "EINVAL", *c)
+    for eps in (-1.0, float("nan"), float("inf")):
+        refused(N, "EINVAL", *calls(N, desc(N), rope(N), ok, eps=eps)[1])
+    need = N.opt_qk_norm_workspace_size(desc(N))
+    assert need > 0 and need % 256 == 0
+    refused(N, "ENOWS", *calls(N, desc(N), rope(N), ok, ws_bytes=need - 1)[2])
+    refused(N, "EINVAL", *calls(N, desc(N), rope(N), ok, ws=0)[2])
+    refused(N, "EINVAL", *calls(N, desc(N), rope(N), ok, ws=BASE + 128)[2])
+    refused(N, "EINVAL", N.opt_rotary_apply, desc(N), None, 0, *ok[:4], 0)
+    args = list(calls(N, desc(N), rope(N), ok)[2])
+    for at in (13, 14):
+        bad = list(args)
+        bad[at] = 0
+        refused(N, "EINVAL", *bad)
+
+
+def test_null_descriptions_refused(N):
+    lib, u = N.load(), C.c_uint64(0)
+    assert lib.opt_qk_norm_workspace_size(None, C.byref(u)) == N.OPT_EINVAL
+    assert lib.opt_qk_norm_workspace_size(desc(N), None) == N.OPT_EINVAL
+    assert lib.opt_rotary_apply(None, rope(N), 0, None, None, None, None, None) == N.OPT_EINVAL
+    assert lib.opt_qk_norm_forward(None, None, None, None, None, None, 0.0, None, None, None, None, None) == N.OPT_EINVAL
+
+
+def test_nothing_to_do_is_no_error(N):
+    for kw in (dict(batch=0), dict(tokens=0)):
+        for c in calls(N, desc(N, **kw), rope(N), [None] * 8)[:2]:
+            c[0](*c[1:])
+        assert N.opt_qk_norm_workspace_size(desc(N, **kw)) == 0
+
+
+def test_tensors_are_checked_before_a_device_is_needed(N):
+    from matrix_optimizer_step_02_amd import train
+    q, k = torch.zeros(2, 8, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 8, 2, 64, dtype=torch.bfloat16)
+    r, w = train.Rotary([1.0, 0.5], device="cpu"), torch.ones(64)
+    pos = torch.zeros(2, 8, dtype=torch.int32)
+    for match, call in [
+            ("HIP device", lambda: train.rotary_forward(q, k, r, pos)),
+            ("HIP device", lambda: train.qk_norm_forward(q, k, w, w)),
+            ("dtype", lambda: train.rotary_forward(q, k.float(), r)),
+            ("dtype", lambda: train.rotary_forward(q.double(), None, r)),
+            ("axes", lambda: train.rotary_forward(q[0, 0], None, r)),
+            ("shape", lambda: train.rotary_forward(q, k[:1], r)),
+            ("shape", lambda: train.rotary_forward(q, k[..., :32], r)),
+            ("positions", lambda: train.rotary_forward(q, k, r, pos.float())),
+            ("positions", lambda: train.rotary_forward(q, k, r, pos[:, :7])),
+            ("positions", lambda: train.rotary_forward(q, k, r, pos[:1])),
+            ("first", lambda: train.rotary_forward(q, k, r, pos, first=3)),
+            ("rope", lambda: train.qk_norm_forward(q, k, w, w, positions=pos)),
+            ("rope", lambda: train.qk_norm_forward(q, k, w, w, first=1)),
+            ("q_weight", lambda: train.qk_norm_forward(q, k, w[:5], w)),
+            ("q_weight", lambda: train.qk_norm_forward(q, k, w.bfloat16(), w)),
+            ("dyk", lambda: train.qk_norm_backward(q, q, q, k, w, w, torch.zeros(2, 8, 4), torch.zeros(2, 8, 2))),
+            ("q_rstd", lambda: train.qk_norm_backward(q, k, q, k, w, w, torch.zeros(2, 8, 3), torch.zeros(2, 8, 2))),
+            ("gradient", lambda: train.qk_norm_forward(q, k, w.clone().requires_grad_(), w))]:
+        with pytest.raises(ValueError, match=match):
+            call()
+    for call in (lambda: train.rotary_forward(q, k, None), lambda: train.qk_norm_forward(q, k, w, w, rope=[1.0])):
+        with pytest.raises(TypeError, match="rope"):
+            call()
+
+
+def test_a_rope_of_another_device_is_refused(N):
+    from matrix_optimizer_step_02_amd import train
+    r = train.Rotary([1.0], device="meta")
+    with pytest.raises(ValueError, match="rope"):
+        train.rotary_forward(torch.zeros(4, 2, 8), None, r)
+
+
+def test_a_ropes_table_is_recorded_with_the_tensors(N):
+    """It is a tuple of what the kernels read, which _streamed records on the call's stream."""
+    from matrix_optimizer_step_02_amd import train
+    r = train.Rotary([1.0, 2.0], device="cpu")
+    assert any(t is r.turns for t in train._tensors((r,)))

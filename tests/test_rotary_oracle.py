@@ -1,0 +1,104 @@
+"""Pins of the fp64 oracle of position rotation and the norm per head: closed
+forms, symmetries and central differences."""
+
+import numpy as np
+import pytest
+
+from oracle import train_ops as T
+
+
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+def test_rotation_by_quarter_turns_swaps_the_pair(layout):
+    x = np.arange(1.0, 7.0).reshape(1, 1, 6)
+    y = T.rotary(x, [1], [np.pi / 2], layout)
+    i, j = (0, 1)
+    want = x.copy()
+    want[..., i], want[..., j] = -x[..., j], x[..., i]
+    assert np.allclose(y, want, atol=1e-15)
+    y = T.rotary(x, [3], [np.pi, np.pi / 2, 0.0], layout)
+    pairs = [(0, 3), (1, 4), (2, 5)] if layout == "half" else [(0, 1), (2, 3), (4, 5)]
+    assert np.allclose(y[0, 0, pairs[0]], -x[0, 0, pairs[0]])
+    assert np.allclose(y[0, 0, pairs[1]], [x[0, 0, pairs[1][1]], -x[0, 0, pairs[1][0]]])
+    assert np.allclose(y[0, 0, pairs[2]], x[0, 0, pairs[2]])
+
+
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+def test_scores_depend_on_the_distance_alone(layout):
+    r = np.random.default_rng(0)
+    q, k, f = r.standard_normal((1, 1, 8)), r.standard_normal((1, 1, 8)), [1.0, 0.3, 0.01]
+    score = lambda p, s: float((T.rotary(q, [p], f, layout) * T.rotary(k, [s], f, layout)).sum())  # noqa: E731
+    assert abs(score(7, 3) - score(10004, 10000)) < 1e-11
+    assert abs(score(7, 3) - score(1, -3)) < 1e-12
+
+
+def test_the_inverse_turns_back_and_is_the_gradient():
+    r = np.random.default_rng(1)
+    x, g, f, pos = r.standard_normal((3, 2, 10)), r.standard_normal((3, 2, 10)), [1.0, 0.2], [5, 0, 2 ** 40]
+    assert np.allclose(T.rotary(T.rotary(x, pos, f, scale=2.0), pos, f, scale=0.5, inverse=True), x)
+    back = T.rotary(g, pos, f, "pairs", 1.3, inverse=True)
+    for at in [(0, 0, 0), (1, 1, 3), (2, 0, 1), (2, 1, 9)]:
+        e = np.zeros_like(x)
+        e[at] = 1e-6
+        d = ((T.rotary(x + e, pos, f, "pairs", 1.3) - T.rotary(x - e, pos, f, "pairs", 1.3)) * g).sum() / 2e-6
+        assert abs(d - back[at]) < 1e-8
+
+
+def test_norm_gradients_by_differences():
+    r = np.random.default_rng(2)
+    x, w, g, eps = r.standard_normal((4, 3, 7)), r.standard_normal(7), r.standard_normal((4, 3, 7)), 1e-3
+    x[0, 0] = 0
+    b = T.rms_norm_backward(g, x, w, eps)
+    loss = lambda x, w: float((T.rms_norm(x, w, eps)["y"] * g).sum())  # noqa: E731
+    for at in [(0, 0, 0), (1, 2, 3), (3, 1, 6)]:
+        e = np.zeros_like(x)
+        e[at] = 1e-6
+        assert abs((loss(x + e, w) - loss(x - e, w)) / 2e-6 - b["dx"][at]) < 1e-6 * (1 + abs(b["dx"][at]))
+    for at in range(7):
+        e = np.zeros_like(w)
+        e[at] = 1e-6
+        assert abs((loss(x, w + e) - loss(x, w - e)) / 2e-6 - b["dw"][at]) < 1e-7 * (1 + abs(b["dw"][at]))
+
+
+def test_a_planted_mistake_shows():
+    """Turning the gradient forwards, not back, is far off."""
+    r = np.random.default_rng(3)
+    g, f = r.standard_normal((2, 1, 4)), [1.0, 0.5]
+    assert np.abs(T.rotary(g, [1, 2], f) - T.rotary(g, [1, 2], f, inverse=True)).max() > 0.1
+
+
+# ------------------------------------------------- frequencies and their table ----
+
+
+def test_frequencies():
+    import math
+    from matrix_optimizer_step_02_amd import train
+    f, s = train.rotary_frequencies(8, 10000.0)
+    assert s == 1.0 and np.allclose(f, [1, 0.1, 0.01, 0.001])
+    f, s = train.rotary_frequencies(8, scaling="linear", factor=4.0)
+    assert s == 1.0 and np.allclose(f, [0.25, 0.025, 0.0025, 0.00025])
+    f, s = train.rotary_frequencies(8, scaling="base", factor=4.0)
+    assert s == 1.0 and f[0] == 1.0 and np.isclose(f[-1], 0.001 / 4)
+    L = 2 * math.pi * 100   # the pairs turn 100, 10, 1 and 0.1 times
+    f, s = train.rotary_frequencies(8, scaling="ramp", factor=4.0, original_length=L, low=1.0, high=19.0)
+    assert np.isclose(s, 1 + 0.1 * math.log(4))
+    assert np.allclose(f, [1.0, 0.1 * 0.5 + 0.025 * 0.5, 0.0025, 0.00025])
+    for bad in (dict(rot=7), dict(rot=0), dict(rot=8, base=-1.0), dict(rot=8, scaling="linear", factor=0.5),
+                dict(rot=8, scaling="ramp", factor=2.0), dict(rot=8, scaling="other"), dict(rot=2, scaling="base", factor=2.0)):
+        with pytest.raises(ValueError):
+            train.rotary_frequencies(**bad)
+
+
+def test_turns_of_the_table():
+    import torch
+    from matrix_optimizer_step_02_amd import train
+    r = train.Rotary([np.pi / 2, np.pi, 1.0, -1.0, 7.0], layout="pairs", scale=1.5, device="cpu")
+    assert (r.rot, r.layout, r.scale) == (10, 1, 1.5) and r.turns.dtype == torch.int64
+    t = [int(x) % 2 ** 64 for x in r.turns]
+    assert abs(t[0] - 2 ** 62) < 2 ** 12 and abs(t[1] - 2 ** 63) < 2 ** 12   # pi in 64 bits is 2^-53 off
+    assert t[2] + t[3] == 2 ** 64
+    assert t[2] == 2935890503282001226   # 2^64 / (2 pi), from pi to 50 digits
+    assert abs(t[4] - (7 * t[2]) % 2 ** 64) <= 4
+    for bad in (dict(frequencies=[]), dict(frequencies=[float("nan")]), dict(frequencies=[1.0], layout="x"),
+                dict(frequencies=[1.0], scale=0.0)):
+        with pytest.raises(ValueError):
+            train.Rotary(device="cpu", **bad)
