@@ -3,7 +3,9 @@
 The compute path is libmatopt.so (HIP kernels behind a C ABI, include/matopt.h).
 This package only marshals torch tensors (device memory and streams) into the
 C ABI: ``native`` mirrors the C entry points one to one, ``RotatedAdamGroup``
-holds the descriptors and the workspace of one group of matrices.
+holds the descriptors and the workspace of one group of matrices, and
+``AdamWGroup`` (module ``adamw``) those of tensors that AdamW steps. ``train`` has
+the training pass's operators.
 """
 
 from __future__ import annotations
@@ -14,7 +16,15 @@ from typing import List, Optional, Sequence
 from . import native
 from .native import MatoptError, OPT_BF16, OPT_F32, PHASES  # noqa: F401
 
-__all__ = ["RotatedAdamGroup", "Hyper", "MatoptError", "native", "tensor_ptr", "stream_ptr"]
+__all__ = ["RotatedAdamGroup", "Hyper", "AdamWGroup", "AdamWHyper", "GradNorm", "adamw_state", "MatoptError", "native",
+           "tensor_ptr", "stream_ptr"]
+
+
+def __getattr__(name):   # these import torch
+    if name in ("AdamWGroup", "AdamWHyper", "GradNorm", "adamw_state"):
+        from . import adamw
+        return getattr(adamw, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 @dataclass

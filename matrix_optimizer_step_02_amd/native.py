@@ -1,4 +1,5 @@
-"""ctypes binding of libmatopt.so (include/matopt.h), argument marshalling only.
+"""ctypes binding of libmatopt.so (include/matopt.h, matopt_train.h,
+matopt_adamw.h), argument marshalling only.
 
 Every function here has the name of the C entry point it calls and forwards
 plain pointers and sizes; all computation runs in the HIP library. If the
@@ -43,6 +44,13 @@ EXPORTED_TRAIN = (
     "opt_layer_norm_forward", "opt_layer_norm_workspace_size", "opt_layer_norm_backward",
     "opt_policy_loss_workspace_size", "opt_policy_loss_forward", "opt_policy_loss_backward", "opt_policy_loss_step",
     "opt_rotary_apply", "opt_qk_norm_forward", "opt_qk_norm_workspace_size", "opt_qk_norm_backward",
+)
+
+# include/matopt_adamw.h: the AdamW step over many tensors
+OPT_ADAMW_BLOCK = 256
+EXPORTED_ADAMW = (
+    "opt_adamw_workspace_size", "opt_adamw_create", "opt_adamw_grad_norm", "opt_adamw_step", "opt_adamw_get_step",
+    "opt_adamw_set_step", "opt_adamw_set_lr", "opt_adamw_destroy",
 )
 
 
@@ -120,6 +128,18 @@ class opt_policy_rows(C.Structure):
                 ("advantage", C.c_void_p), ("weight", C.c_void_p)]
 
 
+class opt_adamw_desc(C.Structure):
+    _fields_ = [
+        ("n", C.c_int64), ("W", C.c_void_p), ("G", C.c_void_p), ("G_dtype", C.c_int32), ("state_bits", C.c_int32),
+        ("m", C.c_void_p), ("v", C.c_void_p), ("m_scale", C.c_void_p), ("v_scale", C.c_void_p), ("W16", C.c_void_p),
+        ("W16_dtype", C.c_int32), ("lr_scale", C.c_float), ("weight_decay", C.c_float),
+    ]
+
+
+class opt_adamw_hparams(C.Structure):
+    _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_double)]
+
+
 _lib: Optional[C.CDLL] = None
 
 
@@ -186,6 +206,17 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         "opt_qk_norm_forward": ([Q, RO, T, T, vp, vp, f32, T, T, vp, vp, vp], i32),
         "opt_qk_norm_workspace_size": ([Q, C.POINTER(u64)], i32),
         "opt_qk_norm_backward": ([Q, RO, T, T, T, T, vp, vp, vp, vp, T, T, vp, vp, vp, u64, vp], i32),
+    }
+    AD, AH = C.POINTER(opt_adamw_desc), C.POINTER(opt_adamw_hparams)
+    sig |= {
+        "opt_adamw_workspace_size": ([AD, i32, C.POINTER(u64)], i32),
+        "opt_adamw_create": ([AD, i32, AH, vp, u64, vp, C.POINTER(vp)], i32),
+        "opt_adamw_grad_norm": ([vp, f32, vp, vp, vp], i32),
+        "opt_adamw_step": ([vp, vp, R, vp, vp], i32),
+        "opt_adamw_get_step": ([vp, C.POINTER(i64)], i32),
+        "opt_adamw_set_step": ([vp, i64], i32),
+        "opt_adamw_set_lr": ([vp, C.c_double], i32),
+        "opt_adamw_destroy": ([vp], None),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -448,3 +479,51 @@ def opt_qk_norm_backward(d, r, dyq, dyk, q, k, q_weight: int, k_weight: int, q_r
                          dq_weight: int, dk_weight: int, workspace: int, workspace_bytes: int, stream_ptr: int):
     _check(load().opt_qk_norm_backward(d, r, dyq, dyk, q, k, q_weight, k_weight, q_rstd, k_rstd, dq, dk, dq_weight,
                                        dk_weight, workspace, workspace_bytes, stream_ptr))
+
+
+# ------------------------------------------------------------- AdamW step ----
+
+
+def _adamw(descs):
+    return (opt_adamw_desc * len(descs))(*descs), len(descs)
+
+
+def opt_adamw_workspace_size(descs) -> int:
+    arr, n = _adamw(descs)
+    out = C.c_uint64(0)
+    _check(load().opt_adamw_workspace_size(arr, n, out))
+    return out.value
+
+
+def opt_adamw_create(descs, hp: opt_adamw_hparams, workspace: int, workspace_bytes: int, stream_ptr: int) -> int:
+    arr, n = _adamw(descs)
+    out = C.c_void_p(0)
+    _check(load().opt_adamw_create(arr, n, hp, workspace, workspace_bytes, stream_ptr, out))
+    return out.value
+
+
+def opt_adamw_grad_norm(g: int, max_norm: float, norm: int, scale: int, stream_ptr: int):
+    _check(load().opt_adamw_grad_norm(g, max_norm, norm, scale, stream_ptr))
+
+
+def opt_adamw_step(g: int, grad_scale: int, rng: Optional[opt_rng], device_step: int, stream_ptr: int):
+    _check(load().opt_adamw_step(g, grad_scale, rng, device_step, stream_ptr))
+
+
+def opt_adamw_get_step(g: int) -> int:
+    t = C.c_int64(0)
+    _check(load().opt_adamw_get_step(g, t))
+    return t.value
+
+
+def opt_adamw_set_step(g: int, t: int):
+    _check(load().opt_adamw_set_step(g, t))
+
+
+def opt_adamw_set_lr(g: int, lr: float):
+    _check(load().opt_adamw_set_lr(g, lr))
+
+
+def opt_adamw_destroy(g: int):
+    if g:
+        load().opt_adamw_destroy(g)

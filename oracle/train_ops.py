@@ -148,3 +148,47 @@ def rms_norm_backward(g, x, w, eps):
     z, xh = g * w, f["xh"]
     dx = f["rstd"][..., None] * (z - xh * (z * xh).mean(-1, keepdims=True))
     return {"dx": dx, "dw": (g * xh).reshape(-1, x.shape[-1]).sum(0), "z": z} | f
+
+
+# ------------------------------------------------------------------ AdamW ----
+
+
+def adamw_moments(m, v, g, b1, b2):
+    """In float32, each product and sum rounded: what the states of 8 bits are made from."""
+    f = np.float32
+    m, v, g = (np.asarray(x, dtype=f) for x in (m, v, g))
+    with np.errstate(over="ignore", invalid="ignore", under="ignore"):
+        return m * f(b1) + g * f(1 - b1), v * f(b2) + (g * g) * f(1 - b2)
+
+
+def adamw_weights(w, m, v, t, lr, b1, b2, eps, decay):
+    """In float64, from the moments after step t."""
+    u = m / (1 - b1 ** t) / (np.sqrt(v / (1 - b2 ** t)) + eps)
+    return w - lr * (u + decay * w)
+
+
+def random16(n, tensor, seed, offset, first=0):
+    """The 16 random bits of n elements of a tensor from element ``first``, a multiple of 8, on."""
+    groups = (n + 7) // 8
+    c = np.zeros((groups, 4), dtype=np.uint64)
+    c[:, 0], c[:, 1], c[:, 2], c[:, 3] = first // 8 + np.arange(groups), tensor, offset & 0xFFFFFFFF, (offset >> 32) & 0xFFFFFFFF
+    w = philox4x32(c, (seed & 0xFFFFFFFF, (seed >> 32) & 0xFFFFFFFF))
+    return np.stack([w & 0xFFFF, w >> 16], axis=-1).reshape(-1)[:n].astype(np.int64)
+
+
+def encode8(x, r, digits, bias, top, block=256):
+    """(values, scales): x (float32) in blocks with a power of two each, rounded up in magnitude where the discarded
+    fraction plus r / 65536 reaches 1. Values are what the codes stand for, scale included; NaN where x is not finite."""
+    n, f = x.size, np.float64
+    mag = np.abs(np.pad(x.astype(f), (0, -n % block)).reshape(-1, block))
+    big = np.where(np.isfinite(mag), mag, 0).max(axis=1)
+    _, e = np.frexp(big)   # big = f 2^e, f in [1/2, 1)
+    e = np.clip(np.where(big > 0, e - 1 - top, -200), -120, 120)
+    scale = np.ldexp(1.0, e)
+    with np.errstate(invalid="ignore"):
+        y = (mag / scale[:, None]).reshape(-1)[:n]
+        _, ye = np.frexp(np.where(np.isfinite(y), y, 1.0))
+        step = np.ldexp(1.0, np.maximum(ye - 1, 1 - bias) - digits)
+        q = np.floor(y / step + r / 65536) * step
+    q = np.where(np.isfinite(x), np.copysign(q, x), np.nan)
+    return q * np.repeat(scale, block)[:n], scale

@@ -1,0 +1,358 @@
+"""GPU tests of the AdamW step over many tensors against the fp64 oracle.
+
+The moments are defined to the bit (each product and sum rounded to fp32), and so
+are the codes and scales of 8-bit states. A weight is a chain of at most 12 roundings
+of 2^-24 (constants, products, sums, root, division) of the update, and one of its own:
+12 2^-24 lr (|u| + decay |w|) + 2^-24 |w|.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import train_ops as T
+
+pytestmark = pytest.mark.gpu
+
+HP = dict(lr=3e-3, beta1=0.9, beta2=0.99, eps=1e-8)
+E = 2.0 ** -24
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _mo():
+    import matrix_optimizer_step_02_amd as mo
+    return mo
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def dt(name):
+    torch = _torch()
+    return {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16, None: None}[name]
+
+
+def param(n, bits=32, grad="f32", copy=None, seed=0, shift=0, **more):
+    """One tensor as a view that starts ``shift`` elements into its buffers."""
+    torch, mo = _torch(), _mo()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    cut = lambda x: x[shift:shift + n]  # noqa: E731
+    p = {"W": cut(torch.randn(n + shift + 3, generator=g, device="cuda")),
+         "G": cut((0.1 * torch.randn(n + shift + 3, generator=g, device="cuda")).to(dt(grad)))}
+    full = mo.adamw_state(torch.empty(n + shift + 3, device="cuda"), bits)
+    p |= {"m": cut(full["m"]), "v": cut(full["v"])}
+    if bits == 8:
+        p |= {k: full[k][:-(-n // 256)] for k in ("m_scale", "v_scale")}
+    if copy:
+        p["W16"] = cut(torch.zeros(n + shift + 3, device="cuda", dtype=dt(copy)))
+    return p | more
+
+
+def snap(p):
+    """(w, m, v) in 64 bits, states of 8 bits as the values they stand for."""
+    w, m, v = np64(p["W"]), np64(p["m"].float()), np64(p["v"].float())
+    if "m_scale" in p:
+        n = w.size
+        m, v = (x * np.repeat(np64(p[k]), 256)[:n] for x, k in ((m, "m_scale"), (v, "v_scale")))
+    return w, m, v
+
+
+def check(p, index, before, t, rng=None, scale=1.0, hp=HP, first=0, lr=None):
+    """p after step t, from ``before``; ``first``: p's first element within its tensor (a multiple of 256)."""
+    w0, m0, v0 = before
+    g = np.float32(scale) * np64(p["G"]).astype(np.float32)
+    m, v = T.adamw_moments(m0, v0, g, hp["beta1"], hp["beta2"])
+    lr = (hp["lr"] if lr is None else lr) * p.get("lr_scale", 1.0)
+    decay = p.get("weight_decay") or 0.0
+    with np.errstate(invalid="ignore"):
+        want = T.adamw_weights(w0, m.astype(float), v.astype(float), t, lr, hp["beta1"], hp["beta2"], hp["eps"], decay)
+        u = (w0 - want) / lr if lr else np.zeros_like(w0)
+    got, gm, gv = snap(p)
+    bound = 12 * E * lr * (np.abs(u) + 2 * decay * np.abs(w0)) + E * np.abs(want) + 1e-30
+    fin = np.isfinite(want)
+    assert np.array_equal(fin, np.isfinite(got))
+    assert (np.abs(got - want)[fin] <= bound[fin]).all(), float((np.abs(got - want) / bound)[fin].max())
+    if "m_scale" in p:
+        r = T.random16(m.size, index, *rng, first=first)
+        m, ms = T.encode8(m, (r & 255) << 8 | r >> 8, 3, 7, 7)
+        v, vs = T.encode8(v, r, 2, 15, 14)
+        assert np.array_equal(np64(p["m_scale"]), ms) and np.array_equal(np64(p["v_scale"]), vs)
+    assert np.array_equal(gm, m, equal_nan=True) and np.array_equal(gv, v, equal_nan=True)
+    if p.get("W16") is not None:
+        assert _torch().equal(p["W16"].isnan(), p["W"].isnan())
+        assert _torch().equal(p["W16"].nan_to_num(), p["W"].to(p["W16"].dtype).nan_to_num())
+
+
+def steps(params, count=3, hp=HP, scale=None, refill=True):
+    torch, mo = _torch(), _mo()
+    from matrix_optimizer_step_02_amd import train
+    group = mo.AdamWGroup(params, mo.AdamWHyper(**hp))
+    for t in range(1, count + 1):
+        before = [snap(p) for p in params]
+        group.step(grad_scale=None if scale is None else torch.tensor(scale, device="cuda"),
+                   rng=train.Rng(99 << 33, (5 << 40) + t))
+        torch.cuda.synchronize()
+        assert group.t == t
+        for i, (p, b) in enumerate(zip(params, before)):
+            check(p, i, b, t, (99 << 33, (5 << 40) + t), 1.0 if scale is None else scale, hp)
+            if refill:
+                p["G"].copy_(0.1 * torch.randn(p["G"].numel(), device="cuda").view_as(p["G"]))
+    group.close()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("n", [1, 2, 7, 8, 9, 255, 256, 257, 2047, 2048, 4095, 4096, 4097, 12345])
+def test_sizes(n, bits):
+    print(f"adamw {n} elements, {bits} bits", flush=True)
+    steps([param(n, bits, seed=n)])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("grad", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("copy", [None, "bf16", "f16"])
+def test_types(bits, grad, copy):
+    print(f"adamw {bits} bits, gradient {grad}, copy {copy}", flush=True)
+    steps([param(5000, bits, grad, copy, seed=1, weight_decay=0.1)], scale=0.37)
+
+
+def test_many_tensors_of_all_kinds_in_one_group():
+    """Odd starts within their buffers, both kinds of state, their own rates and decays, tensors without elements."""
+    print("adamw mixed group", flush=True)
+    r = np.random.default_rng(3)
+    kinds = [(b, g, c) for b in (32, 8) for g in ("f32", "bf16", "f16") for c in (None, "bf16", "f16")]
+    ps = [param(int(r.integers(1, 9000)), *kinds[i % 18], seed=i, shift=i % 7, lr_scale=0.5 + i % 3, weight_decay=0.01 * (i % 4))
+          for i in range(60)]
+    ps.insert(7, param(0, 32))
+    ps.insert(9, param(0, 8))
+    steps(ps)
+
+
+def test_neighbours_are_left_alone():
+    torch, mo = _torch(), _mo()
+    from matrix_optimizer_step_02_amd import train
+    for bits in (32, 8):
+        n = 777
+        whole = {"W": torch.ones(n + 600, device="cuda"), "G": torch.ones(n + 600, device="cuda")}
+        whole |= mo.adamw_state(whole["W"], bits) | {"W16": torch.zeros(n + 600, device="cuda", dtype=torch.bfloat16)}
+        for k in ("m_scale", "v_scale"):
+            if k in whole:
+                whole[k].fill_(7.0)
+        inner = {k: (t[1:-(-n // 256) + 1] if "scale" in k else t[9:9 + n]) for k, t in whole.items()}
+        group = mo.AdamWGroup([inner], mo.AdamWHyper())
+        was = {k: t.clone() for k, t in whole.items()}
+        group.step(rng=train.Rng(1))
+        torch.cuda.synchronize()
+        for k, t in whole.items():
+            a, b = (1, -(-n // 256) + 1) if "scale" in k else (9, 9 + n)
+            assert torch.equal(t[:a].view(torch.uint8), was[k][:a].view(torch.uint8)), k
+            assert torch.equal(t[b:].view(torch.uint8), was[k][b:].view(torch.uint8)), k
+            assert k == "G" or not torch.equal(t[a:b].view(torch.uint8), was[k][a:b].view(torch.uint8)), k
+
+
+@pytest.mark.parametrize("hp", [dict(lr=0.0), dict(beta1=0.0), dict(beta2=0.0), dict(beta1=0.0, beta2=0.0), dict(eps=1.0),
+                                dict(beta1=0.99, beta2=0.9999)])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_hyperparameters(hp, bits):
+    steps([param(3000, bits, seed=2, weight_decay=0.05)], hp=HP | hp)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_magnitudes(bits):
+    """Gradients from denormal to huge beside each other: blocks of one size, mixed blocks, zeros, and what overflows."""
+    torch = _torch()
+    p = param(256 * 12, bits, seed=4)
+    g = p["G"].view(12, 256)
+    for i, mul in enumerate([0.0, 1e-38, 1e-30, 1e-20, 1e-10, 1.0, 1e10, 1e17]):
+        g[i] *= mul
+    g[8] *= torch.logspace(-20, 4, 256, device="cuda")
+    g[9, ::2] = 0.0
+    g[10] = g[10].abs()
+    g[11] *= 1e20   # squares overflow
+    steps([p], refill=False)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_values_that_are_not_finite_stay_where_they_are(bits):
+    torch = _torch()
+    p = param(3000, bits, copy="bf16", seed=5)
+    p["G"][5], p["G"][700], p["G"][2999] = float("nan"), float("inf"), -float("inf")
+    steps([p], count=2, refill=False)
+    bad = p["W"].isnan().nonzero().flatten().tolist()
+    assert bad == [5, 700, 2999]
+    assert torch.isfinite(p["W"][[4, 6, 699, 701, 2998]]).all()
+
+
+def test_eight_bits_follow_32_over_many_steps():
+    """The rounding's mean is zero, so v reaches its average and does not stall: with a constant gradient of size 1, v is
+    1 - b2^t = 0.63 after 1000 steps at 0.999. A step that moves v by d on a grid of q <= v / 4 adds a variance of at most
+    d q <= 0.001 v / 4; over 1000 steps with v below 0.63, 0.37 on the mean, that is 0.09, a deviation of 0.3 an element
+    and 0.3 / 64 = 0.75 % of 0.63 on the mean of 4096: 5 deviations are 4 %."""
+    torch, mo = _torch(), _mo()
+    from matrix_optimizer_step_02_amd import train
+    p = param(4096, 8)
+    p["G"].fill_(1.0)
+    group = mo.AdamWGroup([p], mo.AdamWHyper(lr=0.0))
+    for t in range(1000):
+        group.step(rng=train.Rng(3, t))
+    _, m, v = snap(p)
+    assert abs(v.mean() / (1 - 0.999 ** 1000) - 1) < 0.04, v.mean()
+    assert abs(m.mean() - 1) < 0.04, m.mean()
+
+
+# ------------------------------------------------------------ gradient norm ----
+
+
+@pytest.mark.parametrize("count,n", [(1, 1), (3, 1000), (50, 5001), (2, 3000000)])
+@pytest.mark.parametrize("grad", ["f32", "bf16", "f16"])
+def test_norm_and_clip(count, n, grad):
+    """Squares are exact in 64 bits and their sums off by far less than fp32's rounding."""
+    torch, mo = _torch(), _mo()
+    ps = [param(n + i, (32, 8)[i % 2], grad, seed=i) for i in range(count)]
+    group = mo.AdamWGroup(ps)
+    want = float(np.sqrt(sum(float((p["G"].double() ** 2).sum()) for p in ps)))
+    for limit in (want / 3, want * 3, float("inf")):
+        norm, scale = group.grad_norm(limit)
+        assert norm.shape == scale.shape == () and norm.dtype == scale.dtype == torch.float32
+        assert abs(float(norm) - want) <= 2.0 ** -23 * want
+        assert abs(float(scale) - min(1.0, np.float32(limit) / (want + 1e-6))) <= 2.0 ** -23
+
+
+def test_norm_of_extremes():
+    """Squares that overflow fp32 do not in 64 bits; nothing at all has norm 0."""
+    torch, mo = _torch(), _mo()
+    p = param(100)
+    p["G"].fill_(1e30)
+    group = mo.AdamWGroup([p])
+    norm, scale = group.grad_norm(1.0)
+    assert abs(float(norm) / 1e31 - 1) < 1e-6 and abs(float(scale) / 1e-31 - 1) < 1e-6
+    p["G"].zero_()
+    norm, scale = group.grad_norm(1.0)
+    assert float(norm) == 0 and float(scale) == 1
+    group = mo.AdamWGroup([param(0), param(0, 8)])
+    norm, scale = group.grad_norm(1.0)
+    assert float(norm) == 0 and float(scale) == 1
+    from matrix_optimizer_step_02_amd import train
+    group.step(rng=train.Rng(0))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_step_is_skipped_where_the_norm_is_not_finite(bad):
+    torch, mo = _torch(), _mo()
+    from matrix_optimizer_step_02_amd import train
+    ps = [param(1000, 32, copy="bf16"), param(1000, 8, copy="f16")]
+    ps[1]["G"][17] = bad
+    group = mo.AdamWGroup(ps)
+    was = [{k: t.clone() for k, t in p.items() if isinstance(t, torch.Tensor)} for p in ps]
+    norm, scale = group.grad_norm(1.0)
+    group.step(grad_scale=scale, rng=train.Rng(1))
+    torch.cuda.synchronize()
+    assert scale.isnan() and not torch.isfinite(norm)
+    for p, w in zip(ps, was):
+        for k, t in w.items():
+            assert torch.equal(p[k].view(torch.uint8), t.view(torch.uint8)), k
+
+
+# ---------------------------------------------------- streams, graphs, resume ----
+
+
+def test_graph_replays_with_a_step_counter_on_the_device():
+    torch, mo = _torch(), _mo()
+    from matrix_optimizer_step_02_amd import train
+    print("adamw in a graph", flush=True)
+    mk = lambda: [param(5000, 32, "bf16", "bf16", seed=1, weight_decay=0.1), param(3001, 8, "f32", "f16", seed=2)]  # noqa: E731
+    a, b = mk(), mk()
+    one, two = mo.AdamWGroup(a, mo.AdamWHyper(**HP)), mo.AdamWGroup(b, mo.AdamWHyper(**HP))
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+
+    def call():
+        step.add_(1)
+        n = one.grad_norm(0.5)
+        one.step(grad_scale=n.scale, rng=train.Rng(7, 0, step), device_step=step)
+        return n
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for t in range(1, 5):
+        if t > 1:
+            graph.replay()
+        torch.cuda.synchronize()
+        n = two.grad_norm(0.5)
+        two.step(grad_scale=n.scale, rng=train.Rng(7, t))
+        torch.cuda.synchronize()
+        assert int(step) == t
+        for p, q in zip(a, b):
+            for k in ("m", "v"):
+                assert torch.equal(p[k].view(torch.uint8), q[k].view(torch.uint8)), (t, k)
+            # 1 / (1 - b^t) by another library's exponential: its last bit may differ
+            assert float((p["W"] - q["W"]).abs().max()) <= 2 ** -22 * 4
+        for p, q in zip(a, b):
+            g = torch.randn(p["G"].numel(), device="cuda").to(p["G"].dtype)
+            p["G"].copy_(g)
+            q["G"].copy_(g)
+
+
+def test_a_step_on_another_stream_and_a_resumed_run():
+    torch, mo = _torch(), _mo()
+    from matrix_optimizer_step_02_amd import train
+    a, b = ([param(4097, bits, seed=bits) for bits in (32, 8)] for _ in range(2))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    group = mo.AdamWGroup(a, stream=s)
+    for t in range(6):
+        group.step(rng=train.Rng(1, t), stream=s)
+    norm = group.grad_norm(1.0, stream=s)
+    s.synchronize()
+    other = mo.AdamWGroup(b)
+    for t in range(6):
+        if t == 3:   # a checkpoint: new tensors, a new group that is told the step
+            b = [{k: x.clone() for k, x in p.items()} for p in b]
+            other = mo.AdamWGroup(b)
+            other.t = 3
+        other.step(rng=train.Rng(1, t))
+    assert torch.equal(norm.norm, other.grad_norm(1.0).norm)
+    torch.cuda.synchronize()
+    for p, q in zip(a, b):
+        for k in p:
+            assert torch.equal(p[k].view(torch.uint8), q[k].view(torch.uint8)), k
+
+
+def test_learning_rate_is_set_between_steps():
+    torch, mo = _torch(), _mo()
+    p = param(100)
+    group = mo.AdamWGroup([p], mo.AdamWHyper(**HP))
+    group.step()
+    group.set_lr(1.0)
+    before = snap(p)
+    group.step()
+    torch.cuda.synchronize()
+    check(p, 0, before, 2, lr=1.0)
+
+
+def test_past_2_31_elements():
+    torch, mo = _torch(), _mo()
+    from matrix_optimizer_step_02_amd import train
+    print("adamw past 2^31 elements", flush=True)
+    n = (1 << 31) + 256 * 5 + 13
+    p = {"W": torch.ones(n, device="cuda"), "G": torch.empty(n, device="cuda", dtype=torch.bfloat16).normal_()}
+    p |= mo.adamw_state(p["W"], 8)
+    group = mo.AdamWGroup([p], mo.AdamWHyper(**HP))
+    group.step(rng=train.Rng(4, 5))
+    torch.cuda.synchronize()
+    for first, last in ((0, 512), ((1 << 31) - 256, n)):
+        part = {k: (t[first // 256:-(-last // 256)] if "scale" in k else t[first:last]) for k, t in p.items()}
+        k = last - first
+        check(part, 0, (np.ones(k), np.zeros(k), np.zeros(k)), 1, (4, 5), first=first)
+    want = torch.linalg.vector_norm(p["G"], dtype=torch.float64)
+    assert abs(float(group.grad_norm().norm) / float(want) - 1) < 1e-6
