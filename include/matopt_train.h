@@ -50,7 +50,8 @@ enum { OPT_F16 = 2 };
  *
  * Query i of n_q sees key j of n_k where j < n_k, with causal also
  * j <= i + n_k - n_q (the last query sees the last key), and with window > 0,
- * which needs causal, also j > i + n_k - n_q - window. A query that sees no
+ * which needs causal, also j > i + n_k - n_q - window or, with sinks > 0, j <
+ * sinks: a sequence's first keys stay in sight of all later queries. A query that sees no
  * key has O = 0, L = -inf, dQ = 0. Keys and queries past a sequence's length
  * are not read, whatever they hold; a non-finite key or value inside the
  * length may reach a query whose causal bound or window hides it, and a
@@ -80,6 +81,7 @@ typedef struct {
      * Not together with q_start. */
     const int32_t* q_lens;
     const int32_t* k_lens;
+    int32_t sinks;            /* 0 for none; needs a window */
 } opt_attention_desc;
 
 /* A tensor (batch, tokens, heads, head_dim), the last axis contiguous;

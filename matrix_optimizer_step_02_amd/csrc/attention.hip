@@ -80,6 +80,7 @@ struct AttnArgs {
     int32_t batch, heads, kv_heads, head_dim, q_len, k_len, causal, window, splits, kv_splits;
     uint32_t first;   // of the workgroups, this launch's first
     int32_t listed;   // packed: row blocks are found by their place in a list (find_listed)
+    int32_t sinks;    // first keys that the window does not hide (SINK kernels)
     float scale;
 };
 
@@ -325,6 +326,14 @@ struct Sight {
     __device__ __forceinline__ int lo(int i) const { return window ? max(i + off - window + 1, 0) : 0; }
 };
 
+// With sinks a row block's keys are two runs of tiles: those of the first
+// `sinks` keys that the window's own do not reach, and the window's. Turn n of the
+// list is tile n below `near`, n + skip from there on.
+struct Tiles {
+    int near, skip;
+    __device__ __forceinline__ int operator()(int n) const { return n < near ? n : n + skip; }
+};
+
 // Workgroups come in three shapes: four wavefronts (128 rows), eight (256
 // rows) that share the same tiles, or two sets of four (128 rows) with LDS
 // tiles of their own, which take the tiles in turn and join their sums through
@@ -409,12 +418,22 @@ __device__ __forceinline__ bool block_of(const AttnArgs& a, int blocks, int rows
     return true;
 }
 
-// Key tiles [first, end) of this workgroup's queries and split.
-__device__ __forceinline__ void tile_range(const AttnArgs& a, const Sight& see, int i0, int rows, int nq, int split, int& first, int& end) {
+// Key tiles [first, end) of this workgroup's queries and split; with sinks,
+// places in the list that `tiles` maps to tiles.
+template <bool SINK>
+__device__ __forceinline__ void tile_range(const AttnArgs& a, const Sight& see, int i0, int rows, int nq, int split, int& first, int& end,
+                                           Tiles& tiles) {
     first = end = 0;
     if (i0 >= nq) return;
+    const int hi = see.hi(min(i0 + rows, nq) - 1);
     first = see.lo(i0) / kTile;
-    end = (see.hi(min(i0 + rows, nq) - 1) + kTile - 1) / kTile;
+    end = (hi + kTile - 1) / kTile;
+    if constexpr (SINK) {
+        tiles.near = min((min(a.sinks, hi) + kTile - 1) / kTile, first);
+        tiles.skip = first - tiles.near;
+        first = 0;
+        end -= tiles.skip;
+    }
     if (a.splits > 1) {
         const int each = (max(end - first, 0) + a.splits - 1) / a.splits;
         first += split * each;
@@ -487,7 +506,7 @@ __device__ __forceinline__ void take(const char* smem, int wave, float mine, flo
 
 // --------------------------------------------------------------- forward ----
 
-template <class T, int DB, int W, int SETS>
+template <class T, int DB, int W, int SETS, bool SINK>
 __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
     using FT = Frag<T>;
@@ -518,7 +537,8 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs
     float m = kLowest, l = 0.f;
     const float c = a.scale * kLog2e;
     int first_t, end_t;
-    tile_range(a, see, i0, 32 * W, sq.nq, wg.split, first_t, end_t);
+    Tiles tiles = {0, 0};
+    tile_range<SINK>(a, see, i0, 32 * W, sq.nq, wg.split, first_t, end_t, tiles);
     // keys that any query of this wavefront sees, and the lane's
     const int wlast = min(w0 + 32, sq.nq) - 1;
     const int whi = w0 < sq.nq ? see.hi(wlast) : 0, wlo = see.lo(w0);
@@ -529,8 +549,9 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs
     // turn r of a set is tile first_t + SETS r + set, in buffers r & 1
     auto kt = [&](int r) { return smem + (4 * set + (r & 1)) * G::BYTES; };
     auto fill = [&](int r) {
-        const int t = first_t + SETS * r + set;
+        int t = first_t + SETS * r + set;
         if (t >= end_t) return;
+        if constexpr (SINK) t = tiles(t);
         ck.tile(kt(r), kb, t * kTile, sq.nk, a.head_dim);
         cv.tile(kt(r) + 2 * G::BYTES, vb, t * kTile, sq.nk, a.head_dim);
     };
@@ -539,8 +560,10 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs
     for (int r = 0; r < turns; ++r) {
         tile_barrier();
         fill(r + 1);
-        const int t = first_t + SETS * r + set;
-        if (t >= end_t || t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
+        int t = first_t + SETS * r + set;
+        if (t >= end_t) continue;
+        if constexpr (SINK) t = tiles(t);
+        if (t * kTile >= whi || ((t + 1) * kTile <= wlo && (!SINK || t * kTile >= a.sinks))) continue;
         const Lane<T, DB> at = ln.in(kt(r));
         constexpr int K = 0, V = 2 * G::BYTES;
         f32x16 s[2] = {};
@@ -548,13 +571,13 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs
         for (int ks = 0; ks < 2 * DB; ++ks)
 #pragma unroll
             for (int n = 0; n < 2; ++n) s[n] = FT::mma(at.rows(K, n, ks), qf[ks], s[n]);
-        if (t >= full_hi || t < full_lo || w0 + 32 > sq.nq) {
+        if (t >= full_hi || (t < full_lo && (!SINK || (t + 1) * kTile > a.sinks)) || w0 + 32 > sq.nq) {
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int j = t * kTile + 32 * n + 8 * (e >> 2) + 4 * h + (e & 3);
-                    if (j >= hi || j < lo) s[n][e] = -INFINITY;
+                    if (j >= hi || (j < lo && (!SINK || j >= a.sinks))) s[n][e] = -INFINITY;
                 }
         }
         float mx = s[0][0];
@@ -650,7 +673,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
 // -------------------------------------------------------------- backward ----
 
 // dQ, and D for the other kernel. A lane owns one query, as in the forward pass.
-template <class T, int DB, int W, int SETS>
+template <class T, int DB, int W, int SETS, bool SINK>
 __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
     using FT = Frag<T>;
@@ -704,7 +727,8 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
     f32x16 dq[DB] = {};
     const float c = a.scale * kLog2e;
     int first_t, end_t;
-    tile_range(a, see, i0, 32 * W, sq.nq, wg.split, first_t, end_t);
+    Tiles tiles = {0, 0};
+    tile_range<SINK>(a, see, i0, 32 * W, sq.nq, wg.split, first_t, end_t, tiles);
     const int wlast = min(w0 + 32, sq.nq) - 1;
     const int whi = w0 < sq.nq ? see.hi(wlast) : 0, wlo = see.lo(w0);
     const int hi = i < sq.nq ? see.hi(i) : 0, lo = see.lo(i);
@@ -712,8 +736,9 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
 
     auto kt = [&](int r) { return smem + (4 * set + (r & 1)) * G::BYTES; };
     auto fill = [&](int r) {
-        const int t = first_t + SETS * r + set;
+        int t = first_t + SETS * r + set;
         if (t >= end_t) return;
+        if constexpr (SINK) t = tiles(t);
         ck.tile(kt(r), kb, t * kTile, sq.nk, a.head_dim);
         cv.tile(kt(r) + 2 * G::BYTES, vb, t * kTile, sq.nk, a.head_dim);
     };
@@ -722,11 +747,13 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
     for (int r = 0; r < turns; ++r) {
         tile_barrier();
         fill(r + 1);
-        const int t = first_t + SETS * r + set;
-        if (t >= end_t || t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
+        int t = first_t + SETS * r + set;
+        if (t >= end_t) continue;
+        if constexpr (SINK) t = tiles(t);
+        if (t * kTile >= whi || ((t + 1) * kTile <= wlo && (!SINK || t * kTile >= a.sinks))) continue;
         const Lane<T, DB> at = ln.in(kt(r));
         constexpr int K = 0, V = 2 * G::BYTES;
-        const bool edge = t >= full_hi || t < full_lo;
+        const bool edge = t >= full_hi || (t < full_lo && (!SINK || (t + 1) * kTile > a.sinks));
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             f32x16 s = {}, dp = {};
@@ -739,7 +766,7 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int j = t * kTile + 32 * n + 8 * (e >> 2) + 4 * h + (e & 3);
-                    if (j >= hi || j < lo) s[e] = -INFINITY;
+                    if (j >= hi || (j < lo && (!SINK || j >= a.sinks))) s[e] = -INFINITY;
                 }
             }
 #pragma unroll
@@ -787,7 +814,7 @@ constexpr float kLower = 1.f / (1 << kLift<T>);
 // back in each step. At head_dim <= 64 a workgroup of
 // four is held to 168 registers, three wavefronts a SIMD: 68 us against 78 (6 x
 // 1000 tokens, 16 heads of 64).
-template <class T, int DB, int W, int SETS>
+template <class T, int DB, int W, int SETS, bool SINK>
 __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) void attn_dkv_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
     using FT = Frag<T>;
@@ -823,17 +850,17 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
     f32x16 dk[DB] = {}, dv[DB] = {};
     const float c = a.scale * kLog2e;
 
-    // queries [lo, hi) that see key j: j <= i + off, and j > i + off - window
+    // queries [lo, hi) that see key j: j <= i + off, and j > i + off - window or j < sinks
     auto qlo = [&](int key) { return a.causal ? clampi(key - off, 0, sq.nq) : 0; };
-    auto qhi = [&](int key) { return a.window ? clampi(key - off + a.window, 0, sq.nq) : sq.nq; };
+    auto qhi = [&](int key) { return a.window && !(SINK && key < a.sinks) ? clampi(key - off + a.window, 0, sq.nq) : sq.nq; };
     const int jl = min(j0 + 32 * W, sq.nk) - 1, wl = min(w0 + 32, sq.nk) - 1;
     const bool any = j0 < sq.nk;
     const int first_t = any ? qlo(j0) / kTile : 0;
-    const int end_t = any ? (qhi(jl) + kTile - 1) / kTile : 0;
+    const int end_t = any ? ((SINK ? max(qhi(j0), qhi(jl)) : qhi(jl)) + kTile - 1) / kTile : 0;
     const int tiles = max(end_t - first_t, 0);
-    const int wlo = qlo(w0), whi = w0 < sq.nk ? qhi(wl) : 0;
+    const int wlo = qlo(w0), whi = w0 < sq.nk ? (SINK ? max(qhi(w0), qhi(wl)) : qhi(wl)) : 0;
     const int lo = qlo(j), hi = j < sq.nk ? qhi(j) : 0;
-    const int full_lo = (qlo(max(wl, w0)) + kTile - 1) / kTile, full_hi = qhi(w0) / kTile;
+    const int full_lo = (qlo(max(wl, w0)) + kTile - 1) / kTile, full_hi = (SINK ? min(qhi(min(max(w0, a.sinks), max(wl, w0))), qhi(w0)) : qhi(w0)) / kTile;
 
     // buffers of turn r
     auto qt = [&](int r) { return smem + (4 * set + (r & 1)) * G::BYTES; };
@@ -1022,6 +1049,8 @@ opt_status check_attention(const opt_attention_desc* a) {
     if (a->q_len > (1 << 29) || a->k_len > (1 << 29)) return fail(OPT_EUNSUPPORTED, "sequence too long");
     if (a->window < 0) return fail(OPT_EINVAL, "window must be >= 0");
     if (a->window > 0 && !a->causal) return fail(OPT_EUNSUPPORTED, "a window needs causal");
+    if (a->sinks < 0) return fail(OPT_EINVAL, "sinks must be >= 0");
+    if (a->sinks > 0 && a->window == 0) return fail(OPT_EINVAL, "sinks need a window");
     if (!(a->scale > 0.f) || !(a->scale < INFINITY)) return fail(OPT_EINVAL, "scale must be positive and finite");
     if ((a->q_start != nullptr) != (a->k_start != nullptr)) return fail(OPT_EINVAL, "q_start and k_start come together");
     if (a->q_start && (a->q_lens || a->k_lens)) return fail(OPT_EINVAL, "lengths and packed offsets exclude each other");
@@ -1076,6 +1105,7 @@ AttnArgs attn_args(const opt_attention_desc* a) {
     x.k_len = a->q_start && a->k_tokens < a->k_len ? (int32_t)a->k_tokens : a->k_len;
     x.causal = a->causal != 0, x.scale = a->scale;
     x.window = a->window < x.k_len ? a->window : 0;   // as long as the keys: it hides none
+    x.sinks = !x.window ? 0 : a->sinks < x.k_len ? a->sinks : x.k_len;
     return x;
 }
 
@@ -1092,7 +1122,8 @@ int64_t busy_blocks(const AttnArgs& x, bool keys) {
 // keys, over the heads of its group).
 int64_t block_steps(const AttnArgs& x, bool keys) {
     const int len = keys ? x.q_len : x.k_len;
-    const int64_t n = x.window && x.window + 128 < len ? x.window + 128 : len;
+    const int64_t most = (int64_t)x.window + 128 + (keys ? 0 : (x.sinks + kTile - 1) / kTile * kTile);
+    const int64_t n = x.window && most < len ? most : len;
     return (n + kTile - 1) / kTile * (keys ? x.heads / x.kv_heads : 1);
 }
 
@@ -1140,7 +1171,7 @@ Shape shape_of(const AttnArgs& x, Kind kind) {
     return wgs >= 1024 && !(keys && narrow) ? W8S1 : W4S1;
 }
 
-template <class T, int DB, int W, int SETS>
+template <class T, int DB, int W, int SETS, bool SINK>
 void launch_shape(Kind kind, AttnArgs x, hipStream_t s) {
     const bool keys = kind == DKV;
     int64_t blocks = row_blocks(keys ? x.k_len : x.q_len, 32 * W), sequences = x.batch;
@@ -1153,20 +1184,24 @@ void launch_shape(Kind kind, AttnArgs x, hipStream_t s) {
     for (int64_t first = 0; first < grid; first += most) {
         const dim3 g((uint32_t)(grid - first < most ? grid - first : most)), n(SETS * 64 * W);
         x.first = (uint32_t)first;
-        if (kind == FORWARD) attn_forward_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, (int)blocks);
-        else if (kind == DQ) attn_dq_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, (int)blocks);
-        else attn_dkv_kernel<T, DB, W, SETS><<<g, n, 0, s>>>(x, (int)blocks);
+        if (kind == FORWARD) attn_forward_kernel<T, DB, W, SETS, SINK><<<g, n, 0, s>>>(x, (int)blocks);
+        else if (kind == DQ) attn_dq_kernel<T, DB, W, SETS, SINK><<<g, n, 0, s>>>(x, (int)blocks);
+        else attn_dkv_kernel<T, DB, W, SETS, SINK><<<g, n, 0, s>>>(x, (int)blocks);
     }
 }
 
+template <class T, int DB, bool SINK>
+void launch_kind(Kind kind, const AttnArgs& x, hipStream_t s) {
+    switch (shape_of(x, kind)) {
+        case W4S2: launch_shape<T, DB, 4, 2, SINK>(kind, x, s); break;
+        case W4S1: launch_shape<T, DB, 4, 1, SINK>(kind, x, s); break;
+        case W8S1: launch_shape<T, DB, 8, 1, SINK>(kind, x, s); break;
+    }
+}
 template <class T, int DB>
 void launch(Kind kind, const AttnArgs& x, hipStream_t s) {
     if ((kind == DKV ? x.k_len : x.q_len) == 0 || x.batch == 0) return;
-    switch (shape_of(x, kind)) {
-        case W4S2: launch_shape<T, DB, 4, 2>(kind, x, s); break;
-        case W4S1: launch_shape<T, DB, 4, 1>(kind, x, s); break;
-        case W8S1: launch_shape<T, DB, 8, 1>(kind, x, s); break;
-    }
+    x.sinks ? launch_kind<T, DB, true>(kind, x, s) : launch_kind<T, DB, false>(kind, x, s);
     if (kind == DKV ? x.kv_splits > 1 : x.splits > 1) {
         const int jb = (int)row_blocks(kind == DKV ? x.k_len : x.q_len, kJoinRows);
         const int64_t n = (int64_t)jb * x.batch * (kind == DKV ? x.kv_heads : x.heads);

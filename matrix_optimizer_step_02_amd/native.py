@@ -90,6 +90,7 @@ class opt_attention_desc(C.Structure):
         ("head_dim", C.c_int32), ("q_len", C.c_int32), ("k_len", C.c_int32), ("causal", C.c_int32),
         ("window", C.c_int32), ("scale", C.c_float), ("q_start", C.c_void_p), ("k_start", C.c_void_p),
         ("q_tokens", C.c_int64), ("k_tokens", C.c_int64), ("q_lens", C.c_void_p), ("k_lens", C.c_void_p),
+        ("sinks", C.c_int32),
     ]
 
 

@@ -144,7 +144,7 @@ def _refuse_qkv(q, k, v, packed):
     raise ValueError(f"q has dtype {dt}, expected torch.bfloat16 or torch.float16")
 
 
-def _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens):
+def _desc(q, k, v, causal, window, sinks, scale, q_start, k_start, max_q, max_k, q_lens, k_lens):
     packed = q_start is not None
     if packed != (k_start is not None):
         raise ValueError("q_start and k_start come together")
@@ -163,11 +163,11 @@ def _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens
         a = native.opt_attention_desc(code, batch, heads, ks[1], dim, max_q, max_k, bool(causal), window,
                                       dim ** -0.5 if scale is None else scale,
                                       _vector(q_start, "q_start", dev, batch + 1, torch.int32),
-                                      _vector(k_start, "k_start", dev, batch + 1, torch.int32), nq, ks[0])
+                                      _vector(k_start, "k_start", dev, batch + 1, torch.int32), nq, ks[0], sinks=sinks)
         return a, dev, (heads, nq)
     batch, nq, heads, dim = qs
     a = native.opt_attention_desc(code, batch, heads, ks[2], dim, nq, ks[1], bool(causal), window,
-                                  dim ** -0.5 if scale is None else scale)
+                                  dim ** -0.5 if scale is None else scale, sinks=sinks)
     if q_lens is not None:
         a.q_lens = _vector(q_lens, "q_lens", dev, batch, torch.int32)
     if k_lens is not None:
@@ -196,16 +196,17 @@ def _bytes(like, n):
 
 
 @_streamed
-def attention_forward(q, k, v, *, causal=False, window=0, scale=None, q_start=None, k_start=None, max_q=None,
+def attention_forward(q, k, v, *, causal=False, window=0, sinks=0, scale=None, q_start=None, k_start=None, max_q=None,
                       max_k=None, q_lens=None, k_lens=None, out=None):
     """(out, lse) of softmax(scale q k^T) v. q is (batch, tokens, heads, dim);
     k and v (batch, tokens, kv_heads, dim); any strides with a contiguous last
-    axis. Packed sequences: q, k, v without the batch axis, q_start and k_start
+    axis. window > 0 (with causal) hides keys that lie ``window`` or more behind
+    a query, but for the sequence's first ``sinks``. Packed sequences: q, k, v without the batch axis, q_start and k_start
     int32 offsets of batch + 1, max_q and max_k the longest lengths. Padded
     batches: q_lens, k_lens int32 lengths. lse is fp32, (heads, all query
     tokens). scale defaults to dim^-1/2. Tokens outside every sequence, past a
     length or past max_q or max_k are not read; out is 0 and lse -inf there."""
-    a, dev, per_row = _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens)
+    a, dev, per_row = _desc(q, k, v, causal, window, sinks, scale, q_start, k_start, max_q, max_k, q_lens, k_lens)
     st = _stream(dev)
     o = _out(out, "out", q, dev)
     lse = q.new_empty(per_row, dtype=torch.float32)
@@ -217,12 +218,12 @@ def attention_forward(q, k, v, *, causal=False, window=0, scale=None, q_start=No
 
 
 @_streamed
-def attention_backward(dout, q, k, v, out, lse, *, causal=False, window=0, scale=None, q_start=None, k_start=None,
-                       max_q=None, max_k=None, q_lens=None, k_lens=None, dq=None, dk=None, dv=None):
+def attention_backward(dout, q, k, v, out, lse, *, causal=False, window=0, sinks=0, scale=None, q_start=None,
+                       k_start=None, max_q=None, max_k=None, q_lens=None, k_lens=None, dq=None, dk=None, dv=None):
     """(dq, dk, dv) from the output's gradient and what attention_forward took
     and returned. dq, dk, dv may be given, for instance as views of one
     projection's gradient. They are 0 for tokens outside every sequence."""
-    a, dev, per_row = _desc(q, k, v, causal, window, scale, q_start, k_start, max_q, max_k, q_lens, k_lens)
+    a, dev, per_row = _desc(q, k, v, causal, window, sinks, scale, q_start, k_start, max_q, max_k, q_lens, k_lens)
     for t, name in ((dout, "dout"), (out, "out")):
         if not (t.dtype == q.dtype and t.device == dev and t.shape == q.shape):
             _is(t, name, dev, q.dtype, q.shape)

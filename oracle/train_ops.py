@@ -9,14 +9,14 @@ import numpy as np
 # -------------------------------------------------------------- attention ----
 
 
-def visible(nq, nk, causal=False, window=0):
-    """(nq, nk) truth values: key j < nk, j <= i + nk - nq, j > i + nk - nq - window."""
+def visible(nq, nk, causal=False, window=0, sinks=0):
+    """(nq, nk) truth values: key j < nk, j <= i + nk - nq, j > i + nk - nq - window or j < sinks."""
     i, j = np.arange(nq)[:, None] + nk - nq, np.arange(nk)[None]
     see = np.ones((nq, nk), dtype=bool)
     if causal:
         see &= j <= i
     if window:
-        see &= j > i - window
+        see &= (j > i - window) | (j < sinks)
     return see
 
 
