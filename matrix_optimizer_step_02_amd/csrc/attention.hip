@@ -75,12 +75,14 @@ struct AttnArgs {
     Tensor q, k, v, o, dout, dq, dk, dv;
     float *lse, *delta;
     float *part, *part_v, *part_m, *part_l;   // partial results of splits (workspace)
+    float *tail, *tail_v;                     // those of the sinks' gradients
     const int32_t *q_start, *k_start, *q_lens, *k_lens;
     int64_t q_tokens, k_tokens;   // rows of lse and delta; packed: the token axes
     int32_t batch, heads, kv_heads, head_dim, q_len, k_len, causal, window, splits, kv_splits;
     uint32_t first;   // of the workgroups, this launch's first
     int32_t listed;   // packed: row blocks are found by their place in a list (find_listed)
-    int32_t sinks;    // first keys that the window does not hide (SINK kernels)
+    int32_t pack;     // forward: the heads of a group are rows of one block (PACK kernels)
+    int32_t sinks, tail_splits;   // first keys that the window does not hide (SINK kernels), splits of their queries
     float scale;
 };
 
@@ -403,13 +405,13 @@ struct Block {
 };
 // false: no rows here.
 __device__ __forceinline__ bool block_of(const AttnArgs& a, int blocks, int rows, Block& x) {
-    const int group = a.heads / a.kv_heads;
-    const int pairs = a.listed ? a.heads : a.batch * a.heads, per = blocks * pairs;   // workgroups of one split
+    const int heads = a.pack ? a.kv_heads : a.heads, group = heads / a.kv_heads;
+    const int pairs = a.listed ? heads : a.batch * heads, per = blocks * pairs;   // workgroups of one split
     const int at = a.first + blockIdx.x;
     x.split = at / per;
     int blk, pair;
     locate(at - x.split * per, blocks, pairs, group, a.causal && !a.listed, blk, pair);
-    x.b = pair / a.heads, x.hq = pair % a.heads, x.hk = x.hq / group;
+    x.b = pair / heads, x.hq = pair % heads, x.hk = x.hq / group;
     if (a.listed) {
         int levels;
         if (!find_listed(a.q_start, a.q_tokens, a.q_len, a.batch, rows, blk, x.b, blk, levels)) return false;
@@ -444,6 +446,11 @@ __device__ __forceinline__ void tile_range(const AttnArgs& a, const Sight& see, 
 // Row of the partial results: (split, head, row of lse).
 __device__ __forceinline__ int64_t part_row(const AttnArgs& a, int split, int hq, int64_t row) {
     return ((int64_t)split * a.heads + hq) * a.q_tokens + row;
+}
+
+// And of the sinks' gradients: (split, sequence, key head, key).
+__device__ __forceinline__ int64_t tail_row(const AttnArgs& a, int split, int b, int hk, int j) {
+    return (((int64_t)split * a.batch + b) * a.kv_heads + hk) * a.sinks + j;
 }
 
 // Lane's columns of a transposed accumulator as fp32 partial results.
@@ -506,7 +513,10 @@ __device__ __forceinline__ void take(const char* smem, int wave, float mine, flo
 
 // --------------------------------------------------------------- forward ----
 
-template <class T, int DB, int W, int SETS, bool SINK>
+// Few queries (PACK): a row is a query and one of the heads that share a key
+// head, row r query r / group, so that the group reads its keys once. One block of
+// 128 rows takes them all.
+template <class T, int DB, int W, int SETS, bool SINK, bool PACK>
 __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
     using FT = Frag<T>;
@@ -516,17 +526,21 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs
     if (!block_of(a, blocks, 32 * W, wg)) return;
     const int b = wg.b, hq = wg.hq, hk = wg.hk, i0 = wg.i0;
     const Seq sq = sequence(a, b);
-    if (i0 >= sq.q_rows) return;
+    const int group = PACK ? a.heads / a.kv_heads : 1;   // rows of a query
+    if (i0 >= sq.q_rows * group) return;
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
     const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % W;
     const int set = SETS > 1 ? wave8 / W : 0;
-    const int w0 = i0 + 32 * wave, i = w0 + l32;   // the wavefront's first query, the lane's query
+    const int w0 = i0 + 32 * wave, r0 = w0 + l32;   // the wavefront's first row, the lane's row
+    const int i = PACK ? r0 / group : r0, nrows = sq.nq * group;   // the lane's query
+    const int hl = PACK ? hk * group + r0 % group : hq;   // and head
+    const auto query = [&](int row) { return PACK ? row / group : row; };
     const Sight see = {sq.nk, sq.nk - sq.nq, a.window, a.causal};
 
     Lane<T, DB> ln;
     ln.init();
     F qf[2 * DB];
-    load_rows<T, DB>(qf, rows_of(a.q, b, sq.q0, hq), a.q.token, i, sq.nq, a.head_dim);
+    load_rows<T, DB>(qf, rows_of(a.q, b, sq.q0, hl), a.q.token, i, sq.nq, a.head_dim);
     Copy<DB, W> ck, cv;
     ck.init(a.k.token);
     cv.init(a.v.token);
@@ -538,13 +552,13 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs
     const float c = a.scale * kLog2e;
     int first_t, end_t;
     Tiles tiles = {0, 0};
-    tile_range<SINK>(a, see, i0, 32 * W, sq.nq, wg.split, first_t, end_t, tiles);
+    tile_range<SINK>(a, see, query(i0), PACK ? sq.nq : 32 * W, sq.nq, wg.split, first_t, end_t, tiles);
     // keys that any query of this wavefront sees, and the lane's
-    const int wlast = min(w0 + 32, sq.nq) - 1;
-    const int whi = w0 < sq.nq ? see.hi(wlast) : 0, wlo = see.lo(w0);
+    const int wfirst = query(w0), wlast = query(min(w0 + 32, nrows) - 1);
+    const int whi = w0 < nrows ? see.hi(wlast) : 0, wlo = see.lo(wfirst);
     const int hi = i < sq.nq ? see.hi(i) : 0, lo = see.lo(i);
     // tiles from full_lo up to full_hi need no mask
-    const int full_hi = see.hi(w0) / kTile, full_lo = (see.lo(max(wlast, w0)) + kTile - 1) / kTile;
+    const int full_hi = see.hi(wfirst) / kTile, full_lo = (see.lo(max(wlast, wfirst)) + kTile - 1) / kTile;
 
     // turn r of a set is tile first_t + SETS r + set, in buffers r & 1
     auto kt = [&](int r) { return smem + (4 * set + (r & 1)) * G::BYTES; };
@@ -571,7 +585,7 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs
         for (int ks = 0; ks < 2 * DB; ++ks)
 #pragma unroll
             for (int n = 0; n < 2; ++n) s[n] = FT::mma(at.rows(K, n, ks), qf[ks], s[n]);
-        if (t >= full_hi || (t < full_lo && (!SINK || (t + 1) * kTile > a.sinks)) || w0 + 32 > sq.nq) {
+        if (t >= full_hi || (t < full_lo && (!SINK || (t + 1) * kTile > a.sinks)) || w0 + 32 > nrows) {
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -624,9 +638,9 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs
         m = mn;
     }
     if (l == 0.f) clear(o);
-    if (i >= sq.q_rows) return;
+    if (PACK ? r0 >= sq.q_rows * group : i >= sq.q_rows) return;
     if (a.splits > 1) {
-        const int64_t row = part_row(a, wg.split, hq, sq.l0 + i);
+        const int64_t row = part_row(a, wg.split, hl, sq.l0 + i);
         store_part<DB>(o, a.part + row * (32 * DB));
         if (h == 0) {
             gptr(a.part_m)[row] = m;
@@ -634,8 +648,8 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs
         }
         return;
     }
-    store_t<T, DB>(o, l == 0.f ? 0.f : 1.f / l, rows_of(a.o, b, sq.q0, hq) + (int64_t)i * a.o.token, a.head_dim);
-    if (h == 0) gptr(a.lse)[(int64_t)hq * a.q_tokens + sq.l0 + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    store_t<T, DB>(o, l == 0.f ? 0.f : 1.f / l, rows_of(a.o, b, sq.q0, hl) + (int64_t)i * a.o.token, a.head_dim);
+    if (h == 0) gptr(a.lse)[(int64_t)hl * a.q_tokens + sq.l0 + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // Joins the key splits of one row: out and lse (ML), or the sum of partial
@@ -814,7 +828,14 @@ constexpr float kLower = 1.f / (1 << kLift<T>);
 // back in each step. At head_dim <= 64 a workgroup of
 // four is held to 168 registers, three wavefronts a SIMD: 68 us against 78 (6 x
 // 1000 tokens, 16 heads of 64).
-template <class T, int DB, int W, int SETS, bool SINK>
+//
+// Sinks. Theirs are the only keys that queries past their window see, few keys
+// and most of the queries: one workgroup would run through them long after the
+// others are done (542 us of 8192 tokens, window 1024, 4 sinks, 16 / 8 heads of
+// 128, where the windows alone take 140). So the windows' launch leaves them out,
+// and a second one (TAIL) takes the sinks with all of their queries, split over
+// workgroups that leave fp32 partial sums for a kernel that joins them.
+template <class T, int DB, int W, int SETS, bool TAIL>
 __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) void attn_dkv_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
     using FT = Frag<T>;
@@ -850,24 +871,25 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
     f32x16 dk[DB] = {}, dv[DB] = {};
     const float c = a.scale * kLog2e;
 
-    // queries [lo, hi) that see key j: j <= i + off, and j > i + off - window or j < sinks
+    // queries [lo, hi) that see key j: j <= i + off, and j > i + off - window (TAIL: j < sinks)
     auto qlo = [&](int key) { return a.causal ? clampi(key - off, 0, sq.nq) : 0; };
-    auto qhi = [&](int key) { return a.window && !(SINK && key < a.sinks) ? clampi(key - off + a.window, 0, sq.nq) : sq.nq; };
-    const int jl = min(j0 + 32 * W, sq.nk) - 1, wl = min(w0 + 32, sq.nk) - 1;
-    const bool any = j0 < sq.nk;
+    auto qhi = [&](int key) { return a.window && !TAIL ? clampi(key - off + a.window, 0, sq.nq) : sq.nq; };
+    const int keys = TAIL ? min(a.sinks, sq.nk) : sq.nk;
+    const int jl = min(j0 + 32 * W, keys) - 1, wl = min(w0 + 32, keys) - 1;
+    const bool any = j0 < keys;
     const int first_t = any ? qlo(j0) / kTile : 0;
-    const int end_t = any ? ((SINK ? max(qhi(j0), qhi(jl)) : qhi(jl)) + kTile - 1) / kTile : 0;
+    const int end_t = any ? (qhi(jl) + kTile - 1) / kTile : 0;
     const int tiles = max(end_t - first_t, 0);
-    const int wlo = qlo(w0), whi = w0 < sq.nk ? (SINK ? max(qhi(w0), qhi(wl)) : qhi(wl)) : 0;
-    const int lo = qlo(j), hi = j < sq.nk ? qhi(j) : 0;
-    const int full_lo = (qlo(max(wl, w0)) + kTile - 1) / kTile, full_hi = (SINK ? min(qhi(min(max(w0, a.sinks), max(wl, w0))), qhi(w0)) : qhi(w0)) / kTile;
+    const int wlo = qlo(w0), whi = w0 < keys ? qhi(wl) : 0;
+    const int lo = qlo(j), hi = j < keys ? qhi(j) : 0;
+    const int full_lo = (qlo(max(wl, w0)) + kTile - 1) / kTile, full_hi = qhi(w0) / kTile;
 
     // buffers of turn r
     auto qt = [&](int r) { return smem + (4 * set + (r & 1)) * G::BYTES; };
     auto gt = [&](int r) { return smem + (4 * set + 2 + (r & 1)) * G::BYTES; };
     // step n: query tile n % tiles of the group's head n / tiles; this split's
     // steps are [from, to), and turn r of a set is step from + SETS r + set
-    const int steps = tiles * group, each = (steps + a.kv_splits - 1) / a.kv_splits;
+    const int steps = tiles * group, splits = TAIL ? a.tail_splits : a.kv_splits, each = (steps + splits - 1) / splits;
     const int from = split * each, to = min(steps, from + each), turns = (to - from + SETS - 1) / SETS;
     auto fill = [&](int r) {
         const int n = from + SETS * r + set;
@@ -898,7 +920,7 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
         if (t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
         Lane<T, DB> at = ln.in(qt(r));
         constexpr int Q = 0, O = 2 * G::BYTES;
-        const bool edge = t < full_lo || t >= full_hi || w0 + 32 > sq.nk;
+        const bool edge = t < full_lo || t >= full_hi || w0 + 32 > keys;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             at.pin();
@@ -966,7 +988,13 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
             }
     }
     if (hi <= lo) clear(dk), clear(dv);
-    if (j >= sq.k_rows) return;
+    if (j >= (TAIL ? keys : sq.k_rows)) return;
+    if constexpr (TAIL) {
+        const int64_t row = tail_row(a, split, b, hk, j) * (32 * DB);
+        store_part<DB>(dk, a.tail + row);
+        store_part<DB>(dv, a.tail_v + row);
+        return;
+    }
     if (a.kv_splits > 1) {
         const int64_t row = (((int64_t)split * a.kv_heads + hk) * a.k_tokens + (a.q_start ? sq.k0 : (int64_t)b * a.k_len) + j) * (32 * DB);
         if (SETS == 1 || set == 0) store_part<DB>(dk, a.part + row);
@@ -995,6 +1023,35 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kv_kernel(AttnArgs a, 
         load8(part + (((int64_t)s * a.kv_heads + hk) * a.k_tokens + row) * width + col, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += v[e];
+    }
+    const float mul = v_part ? kLower<T> : a.scale;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= mul;
+    const Tensor& t = v_part ? a.dv : a.dk;
+    store8((T*)(rows_of(t, b, sq.k0, hk) + (int64_t)j * t.token) + col, x);
+}
+
+// Adds the splits of the sinks' dK and dV, in place of what the windows' launch
+// wrote there.
+template <class T>
+__global__ __launch_bounds__(kJoinThreads) void attn_join_tail_kernel(AttnArgs a, int width, int blocks) {
+    const int b = blockIdx.x / blocks / a.kv_heads, hk = blockIdx.x / blocks % a.kv_heads;
+    const Seq sq = sequence(a, b);
+    const int j = blockIdx.x % blocks * kJoinRows + threadIdx.x / 16, col = threadIdx.x % 16 * 8;
+    if (j >= min(a.sinks, sq.nk) || col >= a.head_dim) return;
+    const bool v_part = blockIdx.y;
+    const float* part = v_part ? a.tail_v : a.tail;
+    float x[8] = {};
+    for (int s = 0; s < a.tail_splits; s += 8) {   // eight loads in flight
+        float v[8][8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (s + k < a.tail_splits) load8(part + tail_row(a, s + k, b, hk, j) * width + col, v[k]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (s + k < a.tail_splits) x[e] += v[k][e];
     }
     const float mul = v_part ? kLower<T> : a.scale;
 #pragma unroll
@@ -1095,7 +1152,7 @@ opt_status output(const opt_attention_desc* a, const opt_attention_tensor* t, co
     return OPT_OK;
 }
 
-AttnArgs attn_args(const opt_attention_desc* a) {
+AttnArgs attn_args(const opt_attention_desc* a, bool backward) {
     AttnArgs x = {};
     x.q_start = a->q_start, x.k_start = a->k_start, x.q_lens = a->q_lens, x.k_lens = a->k_lens;
     x.q_tokens = a->q_start ? a->q_tokens : (int64_t)a->batch * a->q_len;
@@ -1106,6 +1163,8 @@ AttnArgs attn_args(const opt_attention_desc* a) {
     x.causal = a->causal != 0, x.scale = a->scale;
     x.window = a->window < x.k_len ? a->window : 0;   // as long as the keys: it hides none
     x.sinks = !x.window ? 0 : a->sinks < x.k_len ? a->sinks : x.k_len;
+    const int group = a->heads / a->kv_heads;
+    x.pack = !backward && x.sinks && group > 1 && (int64_t)x.q_len * group <= 128;
     return x;
 }
 
@@ -1114,6 +1173,7 @@ int64_t row_blocks(int len, int rows) { return (len + rows - 1) / rows; }
 // Blocks of 128 rows with work to do. Packed sequences: the launch covers the
 // longest for each, the blocks past a shorter one's end leave at once.
 int64_t busy_blocks(const AttnArgs& x, bool keys) {
+    if (x.pack) return (int64_t)x.batch * x.kv_heads;
     const int64_t n = row_blocks(keys ? x.k_len : x.q_len, 128) * x.batch;
     const int64_t packed = (keys ? x.k_tokens : x.q_tokens) / 128 + x.batch;
     return (x.q_start && packed < n ? packed : n) * (keys ? x.kv_heads : x.heads);
@@ -1132,15 +1192,33 @@ int64_t block_steps(const AttnArgs& x, bool keys) {
 // is read. Twice as many for the keys of a causal sequence, whose blocks are
 // uneven, if 32 steps are left to each (dK and dV of 4096 tokens, 16 / 8 heads
 // of 128: 232 us without, 181 with; 4 x 1024: 69 and 87). For its queries
-// twice as many gained nothing (46 against 42 us, 2048 tokens).
+// twice as many gained nothing (46 against 42 us, 2048 tokens). Few queries
+// whose heads share rows (pack) are all loads: two workgroups a CU, of two steps at
+// least. One token of each of 32 sequences, up to 4100 keys of 8 heads of 128 in
+// sight: 101 us, one workgroup a CU 128, four 107; of one sequence 27, with four
+// steps at least 26, but 20 against 16 on 1000 keys.
 int splits_of(const AttnArgs& x, bool keys) {
     const int64_t wgs = busy_blocks(x, keys), steps = block_steps(x, keys);
     if (wgs == 0) return 1;
+    if (x.pack) {
+        const int64_t s = 512 / wgs < steps / 2 ? 512 / wgs : steps / 2;
+        return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+    }
     int64_t s = 256 / wgs;
     if (s > steps / 8) s = steps / 8;
     if (s < 1) s = 1;
     if (keys && x.causal && wgs * s <= 256 && steps >= 64 * s) s *= 2;
     return (int)(s > 32 ? 32 : s);
+}
+
+// Parts to split the sinks' queries into: workgroups for every place (two a CU),
+// twice, and at least four steps each.
+int tail_splits_of(const AttnArgs& x) {
+    const int64_t wgs = row_blocks(x.sinks, 128) * x.batch * x.kv_heads;
+    const int64_t steps = row_blocks(x.q_len, kTile) * (x.heads / x.kv_heads);
+    int64_t s = wgs ? 1024 / wgs : 1;
+    if (s > steps / 4) s = steps / 4;
+    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
 enum Kind { FORWARD, DQ, DKV };
@@ -1153,41 +1231,70 @@ enum Kind { FORWARD, DQ, DKV };
 //    dK and dV with dQ: 946 / 1182 (8192 tokens, 8 key heads), but 440 / 428
 //    (2 x 4096, 16 of 96). The forward pass of packed sequences, which are
 //    uneven among themselves, up to 2048 where two such workgroups fit a CU:
-//    77 / 105 (8192 tokens, the longest sequence 4194, 16 heads of 64).
+//    77 / 105 (8192 tokens, the longest sequence 4194, 16 heads of 64). A window
+//    leaves a sequence's keys even: 292 / 285 with dQ (8192 tokens, window 1024).
 //  - Plenty: eight wavefronts share each tile. Half the copies into LDS, which
 //    cost power, and the clock follows the power drawn: 277 us against 298 of
 //    four (forward, 8192 tokens), 521 / 534 (not causal); few ones are left
 //    with a part-filled last round: 51 / 46 (6 x 1000, 16 heads of 64). Not
 //    for the keys at head_dim <= 64, where three workgroups of four fit a CU:
-//    1072 / 1026.
-//  - Else one set of four.
+//    1072 / 1026. Nor for the queries of a window: twice the rows see up to two
+//    more tiles, which only half of the wavefronts need. Forward, 8192 tokens, 16
+//    heads of 128: 105 against 112 (window 1024), 51 / 66 (256), 232 / 260 (4096);
+//    backward 289 / 295, 169 / 186, 814 / 824.
+//  - Else one set of four. Also for few queries whose heads share rows (pack): two
+//    workgroups a CU, 101 / 137 (as above).
 enum Shape { W4S2, W4S1, W8S1 };
 Shape shape_of(const AttnArgs& x, Kind kind) {
     const bool keys = kind == DKV, narrow = x.head_dim <= 64;
     const int splits = keys ? x.kv_splits : x.splits;
     const int64_t wgs = busy_blocks(x, keys) * splits, steps = block_steps(x, keys) / splits;
     const int64_t few = x.q_start && narrow && kind == FORWARD ? 2048 : 1024;
-    if (wgs <= 256 || (x.causal && wgs < few && steps >= 32)) return W4S2;
-    return wgs >= 1024 && !(keys && narrow) ? W8S1 : W4S1;
+    if (!keys && x.pack) return W4S1;
+    const bool even = keys && x.window && !x.q_start;
+    if (wgs <= 256 || (x.causal && !even && wgs < few && steps >= 32)) return W4S2;
+    return wgs >= 1024 && !(keys && narrow) && !(!keys && x.window) ? W8S1 : W4S1;
 }
 
 template <class T, int DB, int W, int SETS, bool SINK>
 void launch_shape(Kind kind, AttnArgs x, hipStream_t s) {
     const bool keys = kind == DKV;
-    int64_t blocks = row_blocks(keys ? x.k_len : x.q_len, 32 * W), sequences = x.batch;
+    int64_t blocks = x.pack ? 1 : row_blocks(keys ? x.k_len : x.q_len, 32 * W), sequences = x.batch;
     // the list where it is shorter than a block of every sequence for each of the longest one's
     const int64_t list = (keys ? x.k_tokens : x.q_tokens) / (32 * W) + x.batch;
-    x.listed = x.q_start && x.batch <= kListed && list < blocks * sequences;
+    x.listed = x.q_start && !x.pack && x.batch <= kListed && list < blocks * sequences;
     if (x.listed) blocks = list, sequences = 1;
-    const int64_t grid = blocks * sequences * (keys ? (int64_t)x.kv_heads * x.kv_splits : (int64_t)x.heads * x.splits);
+    const int64_t grid = blocks * sequences * (keys ? (int64_t)x.kv_heads * x.kv_splits : (int64_t)(x.pack ? x.kv_heads : x.heads) * x.splits);
     constexpr int64_t most = most_blocks(SETS * 64 * W);
     for (int64_t first = 0; first < grid; first += most) {
         const dim3 g((uint32_t)(grid - first < most ? grid - first : most)), n(SETS * 64 * W);
         x.first = (uint32_t)first;
-        if (kind == FORWARD) attn_forward_kernel<T, DB, W, SETS, SINK><<<g, n, 0, s>>>(x, (int)blocks);
+        if (kind == FORWARD) {
+            if constexpr (SINK && W == 4) {
+                if (x.pack) {
+                    attn_forward_kernel<T, DB, W, SETS, SINK, true><<<g, n, 0, s>>>(x, (int)blocks);
+                    continue;
+                }
+            }
+            attn_forward_kernel<T, DB, W, SETS, SINK, false><<<g, n, 0, s>>>(x, (int)blocks);
+        }
         else if (kind == DQ) attn_dq_kernel<T, DB, W, SETS, SINK><<<g, n, 0, s>>>(x, (int)blocks);
-        else attn_dkv_kernel<T, DB, W, SETS, SINK><<<g, n, 0, s>>>(x, (int)blocks);
+        else attn_dkv_kernel<T, DB, W, SETS, false><<<g, n, 0, s>>>(x, (int)blocks);
     }
+}
+
+// The sinks' gradients from all of their queries: four wavefronts, 128 keys.
+template <class T, int DB>
+void launch_tail(AttnArgs x, hipStream_t s) {
+    const int64_t blocks = row_blocks(x.sinks, 128), grid = blocks * x.batch * x.kv_heads * x.tail_splits;
+    constexpr int64_t most = most_blocks(256);
+    x.listed = 0;
+    for (int64_t first = 0; first < grid; first += most) {
+        x.first = (uint32_t)first;
+        attn_dkv_kernel<T, DB, 4, 1, true><<<dim3((uint32_t)(grid - first < most ? grid - first : most)), 256, 0, s>>>(x, (int)blocks);
+    }
+    const int jb = (int)row_blocks(x.sinks, kJoinRows);
+    attn_join_tail_kernel<T><<<dim3((uint32_t)((int64_t)jb * x.batch * x.kv_heads), 2), kJoinThreads, 0, s>>>(x, 32 * DB, jb);
 }
 
 template <class T, int DB, bool SINK>
@@ -1210,6 +1317,7 @@ void launch(Kind kind, const AttnArgs& x, hipStream_t s) {
         else if (kind == DQ) attn_join_kernel<T, false><<<j, kJoinThreads, 0, s>>>(x, 32 * DB, jb);
         else attn_join_kv_kernel<T><<<j, kJoinThreads, 0, s>>>(x, 32 * DB, jb);
     }
+    if (kind == DKV && x.sinks && x.q_len) launch_tail<T, DB>(x, s);
 }
 template <class T>
 void launch(Kind kind, const AttnArgs& x, hipStream_t s) {
@@ -1232,8 +1340,8 @@ void launch_uncovered(bool backward, const AttnArgs& x, hipStream_t s) {
 // The workspace: D (backward), then the splits' partial results. dQ's are
 // joined before dK's and dV's are written, in the same place.
 struct Space {
-    uint64_t delta, part, part_v, part_m, part_l, bytes;
-    int splits, kv_splits;
+    uint64_t delta, part, part_v, part_m, part_l, tail, tail_v, bytes;
+    int splits, kv_splits, tail_splits;
 };
 Space space_of(const AttnArgs& x, bool backward) {
     const auto up = [](uint64_t n) { return (n + 255) / 256 * 256; };
@@ -1249,6 +1357,12 @@ Space space_of(const AttnArgs& x, bool backward) {
         const uint64_t k_part = s.kv_splits > 1 ? up(s.kv_splits * k_rows * width * 4) : 0;
         s.part_v = s.part + k_part;
         s.bytes += q_part > 2 * k_part ? q_part : 2 * k_part;
+        if (x.sinks && k_rows) {
+            s.tail_splits = tail_splits_of(x);
+            const uint64_t each = up((uint64_t)s.tail_splits * x.batch * x.kv_heads * x.sinks * width * 4);
+            s.tail = s.bytes, s.tail_v = s.tail + each;
+            s.bytes += 2 * each;
+        }
     } else if (s.splits > 1) {
         s.bytes += q_part;
         s.part_m = s.bytes, s.bytes += up(s.splits * rows * 4);
@@ -1262,6 +1376,7 @@ void use_space(AttnArgs& x, const Space& s, void* ws) {
     x.delta = (float*)(p + s.delta);
     x.part = (float*)(p + s.part), x.part_v = (float*)(p + s.part_v);
     x.part_m = (float*)(p + s.part_m), x.part_l = (float*)(p + s.part_l);
+    x.tail = (float*)(p + s.tail), x.tail_v = (float*)(p + s.tail_v), x.tail_splits = s.tail_splits;
 }
 
 opt_status check_workspace(const void* ws, uint64_t bytes, uint64_t need) {
@@ -1281,7 +1396,7 @@ extern "C" {
 opt_status opt_attention_workspace_size(const opt_attention_desc* a, int32_t backward, uint64_t* bytes) {
     if (!bytes) return fail(OPT_EINVAL, "bytes is NULL");
     if (opt_status st = check_attention(a)) return st;
-    *bytes = space_of(attn_args(a), backward != 0).bytes;
+    *bytes = space_of(attn_args(a, backward != 0), backward != 0).bytes;
     return OPT_OK;
 }
 
@@ -1290,7 +1405,7 @@ opt_status opt_attention_forward(const opt_attention_desc* a, const opt_attentio
                                  const opt_attention_tensor* out, float* lse, void* workspace,
                                  uint64_t workspace_bytes, void* stream) {
     if (opt_status st = check_attention(a)) return st;
-    AttnArgs x = attn_args(a);
+    AttnArgs x = attn_args(a, false);
     // nothing to read, and nothing to write (packed tokens are written without sequences too)
     const bool no_q = x.q_tokens == 0 || a->q_len == 0 || a->batch == 0, no_k = x.k_tokens == 0 || a->k_len == 0;
     const bool no_out = x.q_tokens == 0;
@@ -1317,7 +1432,7 @@ opt_status opt_attention_backward(const opt_attention_desc* a, const opt_attenti
                                   const opt_attention_tensor* dv, void* workspace, uint64_t workspace_bytes,
                                   void* stream) {
     if (opt_status st = check_attention(a)) return st;
-    AttnArgs x = attn_args(a);
+    AttnArgs x = attn_args(a, true);
     const bool no_q = x.q_tokens == 0 || a->q_len == 0 || a->batch == 0;
     const bool no_k = x.k_tokens == 0 || a->k_len == 0 || a->batch == 0;
     const bool no_dq = x.q_tokens == 0, no_dk = x.k_tokens == 0;   // nothing to write
