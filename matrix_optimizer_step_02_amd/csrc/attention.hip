@@ -35,14 +35,14 @@
 // the caller holds. Holding P or dS as two 16-bit parts would double the
 // products that take it.
 //
-// What bounds it. The matrix units are busy 47 to 58 % of the time at the
-// clock measured (8192 x 8192, 16 heads of 128). The copies of the next tile
-// are issued before the products of this one, but the compiler, which cannot
-// tell the two tiles' LDS apart, waits for them before the first transposed
-// read: in the dQ kernel after 16 of 48 products, with two sets of wavefronts
-// also in the forward kernel, after 16 of 32 (not with one set). In the dK/dV
-// kernel the wait stands before the first product: the loads of L and D, which
-// follow the copies, complete in order behind them.
+// What bounds it: issue. Two wavefronts a SIMD, of which each alternates between
+// products and the softmax arithmetic on their results: 4 to 6 vector instructions
+// a product, the exponentials at a quarter of the rate, and as many scalar ones
+// around tiles and copies. By the counters (8192 tokens, window 1024, 4 sinks, 16 /
+// 8 heads of 128) the matrix units are busy 30 to 40 % of the time, LDS 15 to 26 %
+// and without conflicts. Copies that no wait stands before, of interior tiles
+// without a test in each lane, masks of one comparison and no spilled operand took
+// the pass from 434 us to 382.
 #include "train.h"
 
 namespace matopt {
@@ -52,8 +52,10 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// Read by every load that falls outside a sequence or past head_dim.
+// Read by every load that falls outside a sequence or past head_dim, and in the
+// place of the L of a row that is not there.
 __device__ __attribute__((aligned(64))) uint32_t g_attn_zero[16];
+__device__ float g_attn_inf[1] = {__builtin_huge_valf()};
 
 namespace {
 
@@ -73,7 +75,7 @@ struct Tensor {
 
 struct AttnArgs {
     Tensor q, k, v, o, dout, dq, dk, dv;
-    float *lse, *delta;
+    float *lse, *delta, *l2;   // l2: L as the dK/dV kernel takes it
     float *part, *part_v, *part_m, *part_l;   // partial results of splits (workspace)
     float *tail, *tail_v;                     // those of the sinks' gradients
     const int32_t *q_start, *k_start, *q_lens, *k_lens;
@@ -160,6 +162,27 @@ __device__ __forceinline__ char* rows_of(const Tensor& t, int b, int64_t row0, i
     return t.p + (int64_t)b * t.batch + row0 * t.token + (int64_t)h * t.head;
 }
 
+// Copies from global memory into LDS: 64 lanes of 16 (or 4) bytes each, to
+// consecutive places from `lds` on. Written out, because the compiler counts its
+// own copies as pending LDS writes, cannot tell the tile that is being filled from
+// the one that is being read, and waits for them before the first transposed read:
+// tile_barrier waits for these. (What the compiler waits for besides can only be
+// later than it thinks: vector memory operations complete in order.)
+__device__ __forceinline__ void copy16(uint32_t lds, const void* src) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src) : "memory");
+}
+// The same from a uniform address and an offset below 2^32 in each lane.
+__device__ __forceinline__ void copy16(uint32_t lds, const char* base, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t lds, const void* src) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_at(const void* p) { return (uint32_t)(uintptr_t)(lds_char)p; }
+
 // Copies 64-row tiles of one tensor into LDS. Chunk i of a wavefront is 1024
 // bytes of rows; its lanes' rows and groups follow from chunk 0's (rows 1024 /
 // RB further, the swizzle's low slot bits counting chunks), so two registers
@@ -173,27 +196,40 @@ struct Copy {
     int row0, group0;   // of chunk 0
     int64_t token;
 
-    __device__ __forceinline__ void init(int64_t token_stride) {
-        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % W;
-        token = token_stride;
+    __device__ __forceinline__ void place(int wave, int lane) {
         row0 = wave * PER_WAVE * (1024 / G::RB) + lane / G::SLOTS;
         group0 = (lane % G::SLOTS) ^ G::swz(row0);
     }
+    __device__ __forceinline__ void init(int64_t token_stride) {
+        token = token_stride;
+        if constexpr (!PIN) place(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % W, threadIdx.x & 63);
+    }
     // rows first .. first + 63 of a sequence of n rows
-    __device__ __forceinline__ void tile(char* lds, const char* base, int first, int n, int head_dim) const {
+    __device__ __forceinline__ void tile(char* lds, const char* base, int first, int n, int head_dim) {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % W;
         const char* origin = base + (int64_t)first * token;
-        int r0 = row0, g0 = group0;
-        if constexpr (PIN) asm volatile("" : "+v"(r0), "+v"(g0));
+        if constexpr (PIN) {
+            int lane = threadIdx.x & 63;
+            asm volatile("" : "+v"(lane));
+            place(wave, lane);
+        }
+        const int r0 = row0, g0 = group0;
+        // A tile of rows that are all there, all of whose groups hold columns: no
+        // lane has to look (a tenth of the instructions of an address of its own)
+        if (n - first >= kTile && head_dim * 2 == G::RB) {
+#pragma unroll
+            for (int i = 0; i < PER_WAVE; ++i)
+                copy16(lds_at(lds) + (wave * PER_WAVE + i) * 1024, origin + (int64_t)(i * (1024 / G::RB)) * token,
+                       (uint32_t)r0 * (uint32_t)token + (uint32_t)((g0 ^ G::chunk_swz(i)) << 4));
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < PER_WAVE; ++i) {
             const int row = r0 + i * (1024 / G::RB), group = g0 ^ G::chunk_swz(i);
             const uint32_t off = (uint32_t)row * (uint32_t)token + 16 * group;
             const bool in = row < n - first && 8 * group < head_dim;
             const void* src = in ? (const void*)(origin + off) : (const void*)g_attn_zero;
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                             (__attribute__((address_space(3))) void*)(lds + (wave * PER_WAVE + i) * 1024),
-                                             16, 0, 0);
+            copy16(lds_at(lds) + (wave * PER_WAVE + i) * 1024, src);
         }
     }
 };
@@ -511,6 +547,36 @@ __device__ __forceinline__ void take(const char* smem, int wave, float mine, flo
         }
 }
 
+// Scores of a 32-row block in accumulators that are out of sight: a lane's element
+// e lies at 8 (e / 4) + e % 4 of the other axis, counted from `at` + 4 (l / 32); the
+// ones from `hi` on, those below `lo`, or those that are below `lo` and not below
+// `keep`. One comparison of a register with a constant each.
+__device__ __forceinline__ constexpr int place(int e) { return 8 * (e >> 2) + (e & 3); }
+__device__ __forceinline__ void hide_from(f32x16& s, int hi, int at) {
+    const int x = hi - at - 4 * (int)((threadIdx.x & 63) >> 5);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = place(e) >= x ? -INFINITY : s[e];
+}
+__device__ __forceinline__ void hide_below(f32x16& s, int lo, int at) {
+    const int x = lo - at - 4 * (int)((threadIdx.x & 63) >> 5);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = place(e) < x ? -INFINITY : s[e];
+}
+__device__ __forceinline__ void hide_between(f32x16& s, int keep, int lo, int at) {
+    const int h = 4 * (int)((threadIdx.x & 63) >> 5), x = lo - at - h, y = keep - at - h;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = place(e) < x && place(e) >= y ? -INFINITY : s[e];
+}
+// Keys of a tile block from `at` on that a window hides, with sinks: those behind
+// the sinks where the block lies before the window of all the wavefront's queries
+// (`wlo`).
+template <bool SINK>
+__device__ __forceinline__ void hide_window(f32x16& s, int sinks, int wlo, int lo, int at) {
+    if (!SINK || at >= sinks) hide_below(s, lo, at);
+    else if (at + 32 <= wlo) hide_from(s, sinks, at);
+    else hide_between(s, sinks, lo, at);
+}
+
 // --------------------------------------------------------------- forward ----
 
 // Few queries (PACK): a row is a query and one of the heads that share a key
@@ -585,14 +651,13 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs
         for (int ks = 0; ks < 2 * DB; ++ks)
 #pragma unroll
             for (int n = 0; n < 2; ++n) s[n] = FT::mma(at.rows(K, n, ks), qf[ks], s[n]);
-        if (t >= full_hi || (t < full_lo && (!SINK || (t + 1) * kTile > a.sinks)) || w0 + 32 > nrows) {
+        if (t >= full_hi || w0 + 32 > nrows) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 2; ++n) hide_from(s[n], hi, t * kTile + 32 * n);
+        }
+        if (t < full_lo && (!SINK || (t + 1) * kTile > a.sinks)) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int j = t * kTile + 32 * n + 8 * (e >> 2) + 4 * h + (e & 3);
-                    if (j >= hi || (j < lo && (!SINK || j >= a.sinks))) s[n][e] = -INFINITY;
-                }
+            for (int n = 0; n < 2; ++n) hide_window<SINK>(s[n], a.sinks, wlo, lo, t * kTile + 32 * n);
         }
         float mx = s[0][0];
 #pragma unroll
@@ -686,7 +751,18 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
 
 // -------------------------------------------------------------- backward ----
 
-// dQ, and D for the other kernel. A lane owns one query, as in the forward pass.
+// The dK/dV kernel holds P times 2^kLift<T>. float16 has steps of 2^-24 below
+// 2^-14, which a P of 1 / n is at n keys seen alike: 1.3 % off, all to one
+// side, at 10^6, and 0 from 2^25. Lifted by 2^14 it is a normal number down to
+// 2^-28 (sequences have at most 2^29 tokens), and P = 1, with room for the
+// rounding of large scores, stays below float16's largest, 2^16. dP - D is
+// lowered by as much in the operation that forms it, and dV where it is stored.
+template <class T>
+constexpr int kLift = __is_same(T, _Float16) ? 14 : 0;
+template <class T>
+constexpr float kLower = 1.f / (1 << kLift<T>);
+
+// dQ, and L and D for the other kernel. A lane owns one query, as in the forward pass.
 template <class T, int DB, int W, int SETS, bool SINK>
 __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
@@ -731,7 +807,10 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
     if (i < sq.nq) {
         L2 = gptr(a.lse)[at_row] * kLog2e;
         if (L2 == -INFINITY) L2 = INFINITY;
-        if (h == 0 && set == 0 && wg.split == 0) gptr(a.delta)[at_row] = D;
+        if (h == 0 && set == 0 && wg.split == 0) {
+            gptr(a.delta)[at_row] = D * kLower<T>;
+            gptr(a.l2)[at_row] = L2 == INFINITY ? INFINITY : fmaf(gptr(a.lse)[at_row], kLog2e, (float)-kLift<T>);
+        }
     }
     Copy<DB, W> ck, cv;
     ck.init(a.k.token);
@@ -767,7 +846,7 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
         if (t * kTile >= whi || ((t + 1) * kTile <= wlo && (!SINK || t * kTile >= a.sinks))) continue;
         const Lane<T, DB> at = ln.in(kt(r));
         constexpr int K = 0, V = 2 * G::BYTES;
-        const bool edge = t >= full_hi || (t < full_lo && (!SINK || (t + 1) * kTile > a.sinks));
+        const bool last = t >= full_hi, before = t < full_lo && (!SINK || (t + 1) * kTile > a.sinks);
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             f32x16 s = {}, dp = {};
@@ -776,13 +855,8 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
                 s = FT::mma(at.rows(K, n, ks), qf[ks], s);
                 dp = FT::mma(at.rows(V, n, ks), gf[ks], dp);
             }
-            if (edge) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int j = t * kTile + 32 * n + 8 * (e >> 2) + 4 * h + (e & 3);
-                    if (j >= hi || (j < lo && (!SINK || j >= a.sinks))) s[e] = -INFINITY;
-                }
-            }
+            if (last) hide_from(s, hi, t * kTile + 32 * n);
+            if (before) hide_window<SINK>(s, a.sinks, wlo, lo, t * kTile + 32 * n);
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -L2)) * (dp[e] - D);
 #pragma unroll
@@ -808,24 +882,12 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
         store_t<T, DB>(dq, a.scale, rows_of(a.dq, b, sq.q0, hq) + (int64_t)i * a.dq.token, a.head_dim);
 }
 
-// The dK/dV kernel holds P times 2^kLift<T>. float16 has steps of 2^-24 below
-// 2^-14, which a P of 1 / n is at n keys seen alike: 1.3 % off, all to one
-// side, at 10^6, and 0 from 2^25. Lifted by 2^14 it is a normal number down to
-// 2^-28 (sequences have at most 2^29 tokens), and P = 1, with room for the
-// rounding of large scores, stays below float16's largest, 2^16. dP - D is
-// lowered by as much in the operation that forms it, and dV where it is stored.
-template <class T>
-constexpr int kLift = __is_same(T, _Float16) ? 14 : 0;
-template <class T>
-constexpr float kLower = 1.f / (1 << kLift<T>);
-
 // dK and dV of 32 W keys, summed over the queries that see them and over the
 // heads of the group; the steps are (head, query tile). A lane owns one key.
 // The keys' accumulators (128 registers at head_dim 128) and operands (64)
 // leave little of the 256 registers that two wavefronts a SIMD have, so the
-// addresses are computed where they are used; past head_dim 96 some are
-// spilled all the same (12 bytes a lane with two sets, 20 with one) and read
-// back in each step. At head_dim <= 64 a workgroup of
+// addresses and bounds are computed where they are used, and past head_dim 96 an
+// operand fragment waits in LDS: nothing is spilled. At head_dim <= 64 a workgroup of
 // four is held to 168 registers, three wavefronts a SIMD: 68 us against 78 (6 x
 // 1000 tokens, 16 heads of 64).
 //
@@ -865,6 +927,17 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
     F kf[2 * DB], vf[2 * DB];
     load_rows<T, DB>(kf, rows_of(a.k, b, sq.k0, hk), a.k.token, j, sq.nk, a.head_dim);
     load_rows<T, DB>(vf, rows_of(a.v, b, sq.k0, hk), a.v.token, j, sq.nk, a.head_dim);
+    // Where the registers do not hold all operands, the last fragments of V, and
+    // of K, wait in LDS: one that is spilled comes back from memory, behind the copies
+    constexpr int STASH = DB == 4 ? (W == 8 ? 2 : 1) : DB == 2 && SETS * W == 4 ? 1 : 0, LAST = 2 * DB - 1;
+    __shared__ F stash[STASH ? STASH * SETS * W * 64 : 1];
+    if constexpr (STASH > 0) stash[threadIdx.x] = vf[LAST];
+    if constexpr (STASH > 1) stash[threadIdx.x + SETS * W * 64] = kf[LAST];
+    auto stashed = [&](int n) {
+        int at = threadIdx.x + n * SETS * W * 64;
+        asm volatile("" : "+v"(at));
+        return stash[at];
+    };
     Copy<DB, W, true> cq, cg;
     cq.init(a.q.token);
     cg.init(a.dout.token);
@@ -881,7 +954,14 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
     const int end_t = any ? (qhi(jl) + kTile - 1) / kTile : 0;
     const int tiles = max(end_t - first_t, 0);
     const int wlo = qlo(w0), whi = w0 < keys ? qhi(wl) : 0;
-    const int lo = qlo(j), hi = j < keys ? qhi(j) : 0;
+    // the lane's, computed where they are used: registers held over the loop would spill
+    auto lane_key = [&]() {
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        return w0 + (l & 31);
+    };
+    auto lane_lo = [&]() { return qlo(lane_key()); };
+    auto lane_hi = [&]() { const int key = lane_key(); return key < keys ? qhi(key) : 0; };
     const int full_lo = (qlo(max(wl, w0)) + kTile - 1) / kTile, full_hi = qhi(w0) / kTile;
 
     // buffers of turn r
@@ -900,14 +980,8 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
         if (wave == 0) {
             const int i = first + lane;
             const int64_t at = (int64_t)hq * a.q_tokens + sq.l0 + i;
-            float L = INFINITY, D = 0.f;
-            if (i < sq.nq) {
-                L = gptr(a.lse)[at] * kLog2e;
-                L = L == -INFINITY ? INFINITY : L - kLift<T>;
-                D = gptr(a.delta)[at] * kLower<T>;
-            }
-            stat[set][r & 1][0][lane] = L;
-            stat[set][r & 1][1][lane] = D;
+            copy4(lds_at(stat[set][r & 1][0]), i < sq.nq ? (const void*)(a.l2 + at) : (const void*)g_attn_inf);
+            copy4(lds_at(stat[set][r & 1][1]), i < sq.nq ? (const void*)(a.delta + at) : (const void*)g_attn_zero);
         }
     };
     fill(0);
@@ -920,7 +994,7 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
         if (t * kTile >= whi || (t + 1) * kTile <= wlo) continue;
         Lane<T, DB> at = ln.in(qt(r));
         constexpr int Q = 0, O = 2 * G::BYTES;
-        const bool edge = t < full_lo || t >= full_hi || w0 + 32 > keys;
+        const bool before = t < full_lo, last = t >= full_hi || w0 + 32 > keys;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             at.pin();
@@ -928,16 +1002,11 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
             f32x16 s = {}, dp = {};
 #pragma unroll
             for (int ks = 0; ks < 2 * DB; ++ks) {
-                s = FT::mma(at.rows(Q, u, ks), kf[ks], s);
-                dp = FT::mma(at.rows(O, u, ks), vf[ks], dp);
+                s = FT::mma(at.rows(Q, u, ks), STASH > 1 && ks == LAST ? stashed(1) : kf[ks], s);
+                dp = FT::mma(at.rows(O, u, ks), STASH > 0 && ks == LAST ? stashed(0) : vf[ks], dp);
             }
-            if (edge) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int i = t * kTile + 32 * u + 8 * (e >> 2) + 4 * h + (e & 3);
-                    if (i >= hi || i < lo) s[e] = -INFINITY;
-                }
-            }
+            if (last) hide_from(s, lane_hi(), t * kTile + 32 * u);
+            if (before) hide_below(s, lane_lo(), t * kTile + 32 * u);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const f32x4 L = *(const f32x4*)&stat[set][r & 1][0][32 * u + 8 * g + 4 * h];
@@ -987,7 +1056,7 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
                     else dk[d][4 * g + e] += x[e];
             }
     }
-    if (hi <= lo) clear(dk), clear(dv);
+    if (lane_hi() <= lane_lo()) clear(dk), clear(dv);
     if (j >= (TAIL ? keys : sq.k_rows)) return;
     if constexpr (TAIL) {
         const int64_t row = tail_row(a, split, b, hk, j) * (32 * DB);
@@ -1232,7 +1301,8 @@ enum Kind { FORWARD, DQ, DKV };
 //    (2 x 4096, 16 of 96). The forward pass of packed sequences, which are
 //    uneven among themselves, up to 2048 where two such workgroups fit a CU:
 //    77 / 105 (8192 tokens, the longest sequence 4194, 16 heads of 64). A window
-//    leaves a sequence's keys even: 292 / 285 with dQ (8192 tokens, window 1024).
+//    leaves a sequence's keys even: 292 / 285 with dQ (8192 tokens, window 1024;
+//    taken with sinks).
 //  - Plenty: eight wavefronts share each tile. Half the copies into LDS, which
 //    cost power, and the clock follows the power drawn: 277 us against 298 of
 //    four (forward, 8192 tokens), 521 / 534 (not causal); few ones are left
@@ -1251,7 +1321,7 @@ Shape shape_of(const AttnArgs& x, Kind kind) {
     const int64_t wgs = busy_blocks(x, keys) * splits, steps = block_steps(x, keys) / splits;
     const int64_t few = x.q_start && narrow && kind == FORWARD ? 2048 : 1024;
     if (!keys && x.pack) return W4S1;
-    const bool even = keys && x.window && !x.q_start;
+    const bool even = keys && x.sinks && !x.q_start;
     if (wgs <= 256 || (x.causal && !even && wgs < few && steps >= 32)) return W4S2;
     return wgs >= 1024 && !(keys && narrow) && !(!keys && x.window) ? W8S1 : W4S1;
 }
@@ -1337,10 +1407,10 @@ void launch_uncovered(bool backward, const AttnArgs& x, hipStream_t s) {
     attn_uncovered_kernel<<<g, kGapThreads, 0, s>>>(x, backward);
 }
 
-// The workspace: D (backward), then the splits' partial results. dQ's are
+// The workspace: D and L (backward), then the splits' partial results. dQ's are
 // joined before dK's and dV's are written, in the same place.
 struct Space {
-    uint64_t delta, part, part_v, part_m, part_l, tail, tail_v, bytes;
+    uint64_t delta, l2, part, part_v, part_m, part_l, tail, tail_v, bytes;
     int splits, kv_splits, tail_splits;
 };
 Space space_of(const AttnArgs& x, bool backward) {
@@ -1350,7 +1420,7 @@ Space space_of(const AttnArgs& x, bool backward) {
     Space s = {};
     s.splits = rows ? splits_of(x, false) : 1;
     s.kv_splits = backward && k_rows ? splits_of(x, true) : 1;
-    if (backward) s.bytes += up(rows * 4);
+    if (backward) s.l2 = up(rows * 4), s.bytes += 2 * up(rows * 4);
     s.part = s.bytes;
     const uint64_t q_part = s.splits > 1 ? up(s.splits * rows * width * 4) : 0;
     if (backward) {
@@ -1373,7 +1443,7 @@ Space space_of(const AttnArgs& x, bool backward) {
 void use_space(AttnArgs& x, const Space& s, void* ws) {
     char* p = (char*)ws;
     x.splits = s.splits, x.kv_splits = s.kv_splits;
-    x.delta = (float*)(p + s.delta);
+    x.delta = (float*)(p + s.delta), x.l2 = (float*)(p + s.l2);
     x.part = (float*)(p + s.part), x.part_v = (float*)(p + s.part_v);
     x.part_m = (float*)(p + s.part_m), x.part_l = (float*)(p + s.part_l);
     x.tail = (float*)(p + s.tail), x.tail_v = (float*)(p + s.tail_v), x.tail_splits = s.tail_splits;
