@@ -6,10 +6,13 @@
 //   backward:  g = R^T dy,  z = g w,  xh = x rstd,  dx = rstd (z - xh mean(z xh)),  dw = sum g xh
 //
 // Every tensor is read once and written once. A head's row lies in L lanes of
-// a wavefront (a power of two), sixteen elements each: two groups of eight
-// that hold the partners of their pairs, so that the rotation needs no other
-// lane and the norm one sum over the L lanes. A lane keeps the cosines and
-// sines of its eight pairs over the heads of a token.
+// a wavefront (a power of two), two groups of G elements each that hold the
+// partners of their pairs, so that the rotation needs no other lane and the norm
+// one sum over the L lanes. A lane keeps the cosines and sines of its pairs over
+// the heads of a token. G is 4, or less where the turned part and the rest are not
+// made of whole groups of 4: a group is one load or store then too. (16384 tokens, 16
+// / 8 heads of 128 in bf16, forward and backward: rotation 79 us, norm 100; groups
+// of 8 83 and 102.)
 //
 // Angles. What turns is the fraction of a turn, so the frequencies come as
 // F_i = round(2^64 f_i / (2 pi)) and p F_i mod 2^64, an integer product, is the
@@ -52,7 +55,7 @@ struct Args {
     Side q, k;
     Rope r;
     uint32_t tokens, total, first;   // per sequence; in all, or up to this launch's end; this launch's first
-    int32_t dim, per, shift;         // heads to a thread's turn, log2 of L
+    int32_t dim, per, shift, group;  // heads to a thread's turn, log2 of L, group_of
     float eps;
 };
 
@@ -80,32 +83,36 @@ __device__ __forceinline__ void turn(uint32_t top, float& sn, float& cs) {
     cs = (quarter + 1) & 2 ? -b : b;
 }
 
-// A lane's sixteen elements: n_a from a, n_b from b, and its first pair.
+// A lane's two groups of G elements: n_a of them from a, n_b from b, and its first
+// pair of n_f (0: not turned).
 struct Unit {
-    int a, b, na, nb, f, nf;   // nf = 0: not rotated
+    int a, b, na, nb, f, nf;
 };
-__device__ __forceinline__ int upto8(int n) { return n < 0 ? 0 : n < 8 ? n : 8; }
+template <int G>
+__device__ __forceinline__ int upto(int n) { return n < 0 ? 0 : n < G ? n : G; }
+template <int G>
 __device__ __forceinline__ Unit unit_of(int u, int dim, int rot, bool pairs) {
     Unit x = {};
-    const int half = rot / 2, turned = pairs ? (rot + 15) / 16 : (half + 7) / 8;
+    const int half = rot / 2, turned = pairs ? (rot + 2 * G - 1) / (2 * G) : (half + G - 1) / G;
     if (u < turned) {
-        x.f = 8 * u;
-        x.nf = upto8(half - x.f);
+        x.f = G * u;
+        x.nf = upto<G>(half - x.f);
         if (pairs) {
-            x.a = 16 * u, x.b = x.a + 8;
-            x.na = upto8(rot - x.a), x.nb = upto8(rot - x.b);
+            x.a = 2 * G * u, x.b = x.a + G;
+            x.na = upto<G>(rot - x.a), x.nb = upto<G>(rot - x.b);
         } else {
-            x.a = 8 * u, x.b = half + x.a;
+            x.a = G * u, x.b = half + x.a;
             x.na = x.nb = x.nf;
         }
     } else {
-        x.a = rot + 16 * (u - turned), x.b = x.a + 8;
-        x.na = upto8(dim - x.a), x.nb = upto8(dim - x.b);
+        x.a = rot + 2 * G * (u - turned), x.b = x.a + G;
+        x.na = upto<G>(dim - x.a), x.nb = upto<G>(dim - x.b);
     }
     return x;
 }
 
-__device__ __forceinline__ void angles(const Rope& r, const Unit& x, uint32_t b, uint32_t t, float (&c)[8], float (&s)[8]) {
+template <int G>
+__device__ __forceinline__ void angles(const Rope& r, const Unit& x, uint32_t b, uint32_t t, float (&c)[G], float (&s)[G]) {
     if (x.nf == 0) return;
     int64_t p = r.first + t;
     if (r.pos) {
@@ -114,7 +121,7 @@ __device__ __forceinline__ void angles(const Rope& r, const Unit& x, uint32_t b,
     }
     if (r.inverse) p = (int64_t)(0 - (uint64_t)p);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < G; ++e) {
         const uint64_t f = e < x.nf ? gptr(r.turns)[x.f + e] : 0;
         turn((uint32_t)((uint64_t)p * f >> 32), s[e], c[e]);
         s[e] *= r.scale;
@@ -122,54 +129,75 @@ __device__ __forceinline__ void angles(const Rope& r, const Unit& x, uint32_t b,
     }
 }
 
-__device__ __forceinline__ void rotate(bool pairs, const Unit& x, const float (&c)[8], const float (&s)[8], float (&a)[8], float (&b)[8]) {
+__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
+    const float y = a, z = b;
+    a = y * c - z * s;
+    b = z * c + y * s;
+}
+template <int G>
+__device__ __forceinline__ void rotate(bool pairs, const Unit& x, const float (&c)[G], const float (&s)[G], float (&a)[G], float (&b)[G]) {
     if (x.nf == 0) return;
     if (pairs) {
+        if constexpr (G == 1) {   // the pair is the lane's two elements
+            turn_pair(a[0], b[0], c[0], s[0]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float y = a[2 * e], z = a[2 * e + 1];
-            a[2 * e] = y * c[e] - z * s[e];
-            a[2 * e + 1] = z * c[e] + y * s[e];
-            y = b[2 * e], z = b[2 * e + 1];
-            b[2 * e] = y * c[e + 4] - z * s[e + 4];
-            b[2 * e + 1] = z * c[e + 4] + y * s[e + 4];
+            for (int e = 0; e < G / 2; ++e) {
+                turn_pair(a[2 * e], a[2 * e + 1], c[e], s[e]);
+                turn_pair(b[2 * e], b[2 * e + 1], c[e + G / 2], s[e + G / 2]);
+            }
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float y = a[e], z = b[e];
-            a[e] = y * c[e] - z * s[e];
-            b[e] = z * c[e] + y * s[e];
-        }
+        for (int e = 0; e < G; ++e) turn_pair(a[e], b[e], c[e], s[e]);
     }
 }
 
-// Groups of a row, whole ones or none (EIGHTS) or any number of elements, as
+// Groups of a row, whole ones or none (WHOLE) or any number of elements, as
 // stored: loads in flight take half the registers in 16 bits.
-template <class T>
-using Eight = T __attribute__((ext_vector_type(8)));
-template <bool EIGHTS, class T>
-__device__ __forceinline__ Eight<T> get(const T* p, int n) {
-    typedef T at1 __attribute__((ext_vector_type(8), aligned(sizeof(T))));
-    Eight<T> f = {};
-    if (EIGHTS ? n != 0 : n >= 8) {
-        f = *(const __attribute__((address_space(1))) at1*)p;
-    } else if constexpr (!EIGHTS) {
+template <class T, int G>
+struct Group {
+    T v __attribute__((ext_vector_type(G)));
+};
+template <bool WHOLE, int G, class T>
+__device__ __forceinline__ Group<T, G> get(const T* p, int n) {
+    typedef T vec __attribute__((ext_vector_type(G), aligned(sizeof(T))));
+    Group<T, G> f = {};
+    if (WHOLE ? n != 0 : n >= G) {
+        if constexpr (G == 1) {
+            f.v[0] = *gptr(p);
+        } else {
+            f.v = *(const __attribute__((address_space(1))) vec*)p;
+        }
+    } else if constexpr (!WHOLE) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < n) f[e] = gptr(p)[e];
+        for (int e = 0; e < G; ++e)
+            if (e < n) f.v[e] = gptr(p)[e];
     }
     return f;
 }
-template <class T>
-__device__ __forceinline__ void widen(const Eight<T>& x, float (&f)[8], float mul = 1.f) {
+template <class T, int G>
+__device__ __forceinline__ void widen(const Group<T, G>& x, float (&f)[G], float mul = 1.f) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = (float)x[e] * mul;
+    for (int e = 0; e < G; ++e) f[e] = (float)x.v[e] * mul;
 }
-template <bool EIGHTS, class T>
-__device__ __forceinline__ void put(T* p, int n, const float (&f)[8]) {
-    if constexpr (!EIGHTS) return store_n(p, n, f);
-    if (n) store8(p, f);
+template <bool WHOLE, int G, class T>
+__device__ __forceinline__ void put(T* p, int n, const float (&f)[G]) {
+    typedef T vec __attribute__((ext_vector_type(G), aligned(sizeof(T))));
+    if (WHOLE ? n != 0 : n >= G) {
+        if constexpr (G == 1) {
+            *gptr(p) = (T)f[0];
+        } else {
+            vec x;
+#pragma unroll
+            for (int e = 0; e < G; ++e) x[e] = (T)f[e];
+            *(__attribute__((address_space(1))) vec*)p = x;
+        }
+    } else if constexpr (!WHOLE) {
+#pragma unroll
+        for (int e = 0; e < G; ++e)
+            if (e < n) gptr(p)[e] = (T)f[e];
+    }
 }
 
 template <class T>
@@ -186,8 +214,9 @@ __device__ __forceinline__ float lanes_sum(float x, int shift) {
 // ----------------------------------------------------------------- forward ----
 
 // A thread's turn is one token and `per` heads of q or of k, HB at a time.
-constexpr int kHeadsAhead = 4;   // heads whose loads are in flight together
-template <class T, bool EIGHTS, bool NORM>
+// heads whose loads are in flight together: 79 us as above, four 96, eight 99
+constexpr int kHeadsAhead = 2;
+template <class T, int G, bool WHOLE, bool NORM>
 __global__ __launch_bounds__(kThreads) void heads_forward_kernel(Args a) {
     constexpr int HB = kHeadsAhead;
     const int u = threadIdx.x & ((1 << a.shift) - 1);
@@ -199,48 +228,48 @@ __global__ __launch_bounds__(kThreads) void heads_forward_kernel(Args a) {
     const Side& x = is_k ? a.k : a.q;
     if (is_k) part -= a.q.parts;
     const uint32_t b = row / a.tokens, t = row - b * a.tokens;
-    const Unit n = unit_of(u, a.dim, a.r.rot, a.r.pairs);
-    float c[8], s[8];
-    Eight<float> wa, wb;
+    const Unit n = unit_of<G>(u, a.dim, a.r.rot, a.r.pairs);
+    float c[G], s[G];
+    Group<float, G> wa, wb;
     const int end = min((part + 1) * a.per, x.heads);
     for (int h0 = part * a.per; h0 < end; h0 += HB) {
-        Eight<T> ra[HB], rb[HB];
+        Group<T, G> ra[HB], rb[HB];
 #pragma unroll
         for (int i = 0; i < HB; ++i) {
             if (h0 + i >= end) continue;
             const T* p = row_of<T>(x.in, b, t, h0 + i);
-            ra[i] = get<EIGHTS>(p + n.a, n.na);
-            rb[i] = get<EIGHTS>(p + n.b, n.nb);
+            ra[i] = get<WHOLE, G>(p + n.a, n.na);
+            rb[i] = get<WHOLE, G>(p + n.b, n.nb);
         }
         if (h0 == part * a.per) {
             if constexpr (NORM) {
-                wa = get<EIGHTS>(x.w + n.a, n.na);
-                wb = get<EIGHTS>(x.w + n.b, n.nb);
+                wa = get<WHOLE, G>(x.w + n.a, n.na);
+                wb = get<WHOLE, G>(x.w + n.b, n.nb);
             }
             angles(a.r, n, b, t, c, s);
         }
 #pragma unroll
         for (int i = 0; i < HB; ++i) {
             if (h0 + i >= end) continue;
-            float fa[8], fb[8];
-            widen<T>(ra[i], fa);
-            widen<T>(rb[i], fb);
+            float fa[G], fb[G];
+            widen<T, G>(ra[i], fa);
+            widen<T, G>(rb[i], fb);
             if constexpr (NORM) {
                 float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum += fa[e] * fa[e] + fb[e] * fb[e];
+                for (int e = 0; e < G; ++e) sum += fa[e] * fa[e] + fb[e] * fb[e];
                 const float rstd = 1.f / sqrtf(lanes_sum(sum, a.shift) / (float)a.dim + a.eps);
                 if (u == 0) gptr(x.rstd)[(int64_t)row * x.heads + h0 + i] = rstd;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    fa[e] = fa[e] * rstd * wa[e];
-                    fb[e] = fb[e] * rstd * wb[e];
+                for (int e = 0; e < G; ++e) {
+                    fa[e] = fa[e] * rstd * wa.v[e];
+                    fb[e] = fb[e] * rstd * wb.v[e];
                 }
             }
             rotate(a.r.pairs, n, c, s, fa, fb);
             T* p = row_of<T>(x.out, b, t, h0 + i);
-            put<EIGHTS>(p + n.a, n.na, fa);
-            put<EIGHTS>(p + n.b, n.nb, fb);
+            put<WHOLE, G>(p + n.a, n.na, fa);
+            put<WHOLE, G>(p + n.b, n.nb, fb);
         }
     }
 }
@@ -249,82 +278,82 @@ __global__ __launch_bounds__(kThreads) void heads_forward_kernel(Args a) {
 
 // Workgroups [0, q.blocks) take q, the others k. Each keeps its lanes' weight
 // gradients over all its turns and leaves one row of them.
-template <class T, bool EIGHTS>
-__global__ __launch_bounds__(kThreads, 3) void heads_backward_kernel(Args a) {
+template <class T, int G, bool WHOLE>
+__global__ __launch_bounds__(kThreads, 4) void heads_backward_kernel(Args a) {
     constexpr int HB = sizeof(T) == 4 ? 1 : 2;
-    __shared__ float cross[16][kThreads + 1];
+    __shared__ float cross[2 * G][kThreads + 1];
     const int u = threadIdx.x & ((1 << a.shift) - 1), slots = kThreads >> a.shift;
     const bool is_k = (int)blockIdx.x >= a.q.blocks;
     const Side& x = is_k ? a.k : a.q;
     const uint32_t block = blockIdx.x - (is_k ? a.q.blocks : 0);
-    const Unit n = unit_of(u, a.dim, a.r.rot, a.r.pairs);
+    const Unit n = unit_of<G>(u, a.dim, a.r.rot, a.r.pairs);
     const float inv = 1.f / (float)a.dim;
-    float da[8] = {}, db[8] = {};
-    const Eight<float> wa = get<EIGHTS>(x.w + n.a, n.na), wb = get<EIGHTS>(x.w + n.b, n.nb);
+    float da[G] = {}, db[G] = {};
+    const Group<float, G> wa = get<WHOLE, G>(x.w + n.a, n.na), wb = get<WHOLE, G>(x.w + n.b, n.nb);
     const uint64_t items = (uint64_t)a.total * x.parts;
     for (uint64_t item = (uint64_t)block * slots + (threadIdx.x >> a.shift); item < items; item += (uint64_t)x.blocks * slots) {
         const uint32_t row = x.parts == 1 ? (uint32_t)item : (uint32_t)(item / (uint32_t)x.parts);
         const int part = (int)(item - (uint64_t)row * x.parts);
         const uint32_t b = row / a.tokens, t = row - b * a.tokens;
-        float c[8], s[8];
+        float c[G], s[G];
         const int end = min((part + 1) * a.per, x.heads);
         for (int h0 = part * a.per; h0 < end; h0 += HB) {
-            Eight<T> rxa[HB], rxb[HB], rga[HB], rgb[HB];
+            Group<T, G> rxa[HB], rxb[HB], rga[HB], rgb[HB];
             float rstd[HB];
 #pragma unroll
             for (int i = 0; i < HB; ++i) {
                 if (h0 + i >= end) continue;
                 const T* p = row_of<T>(x.in, b, t, h0 + i);
                 const T* g = row_of<T>(x.dy, b, t, h0 + i);
-                rxa[i] = get<EIGHTS>(p + n.a, n.na);
-                rxb[i] = get<EIGHTS>(p + n.b, n.nb);
-                rga[i] = get<EIGHTS>(g + n.a, n.na);
-                rgb[i] = get<EIGHTS>(g + n.b, n.nb);
+                rxa[i] = get<WHOLE, G>(p + n.a, n.na);
+                rxb[i] = get<WHOLE, G>(p + n.b, n.nb);
+                rga[i] = get<WHOLE, G>(g + n.a, n.na);
+                rgb[i] = get<WHOLE, G>(g + n.b, n.nb);
                 rstd[i] = gptr(x.rstd)[(int64_t)row * x.heads + h0 + i];
             }
             if (h0 == part * a.per) angles(a.r, n, b, t, c, s);
 #pragma unroll
             for (int i = 0; i < HB; ++i) {
                 if (h0 + i >= end) continue;
-                float xa[8], xb[8], ga[8], gb[8], sum = 0.f;
-                widen<T>(rga[i], ga);
-                widen<T>(rgb[i], gb);
+                float xa[G], xb[G], ga[G], gb[G], sum = 0.f;
+                widen<T, G>(rga[i], ga);
+                widen<T, G>(rgb[i], gb);
                 rotate(a.r.pairs, n, c, s, ga, gb);
-                widen<T>(rxa[i], xa, rstd[i]);
-                widen<T>(rxb[i], xb, rstd[i]);
+                widen<T, G>(rxa[i], xa, rstd[i]);
+                widen<T, G>(rxb[i], xb, rstd[i]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < G; ++e) {
                     da[e] += ga[e] * xa[e];
                     db[e] += gb[e] * xb[e];
-                    ga[e] *= wa[e];
-                    gb[e] *= wb[e];
+                    ga[e] *= wa.v[e];
+                    gb[e] *= wb.v[e];
                     sum += ga[e] * xa[e] + gb[e] * xb[e];
                 }
                 sum = lanes_sum(sum, a.shift) * inv;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < G; ++e) {
                     ga[e] = (ga[e] - xa[e] * sum) * rstd[i];
                     gb[e] = (gb[e] - xb[e] * sum) * rstd[i];
                 }
                 T* p = row_of<T>(x.out, b, t, h0 + i);
-                put<EIGHTS>(p + n.a, n.na, ga);
-                put<EIGHTS>(p + n.b, n.nb, gb);
+                put<WHOLE, G>(p + n.a, n.na, ga);
+                put<WHOLE, G>(p + n.b, n.nb, gb);
             }
         }
     }
     // the slots' sums meet in LDS and are added in order
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < G; ++e) {
         cross[e][threadIdx.x] = da[e];
-        cross[e + 8][threadIdx.x] = db[e];
+        cross[e + G][threadIdx.x] = db[e];
     }
     __syncthreads();
-    for (int v = threadIdx.x; v < 16 << a.shift; v += kThreads) {
+    for (int v = threadIdx.x; v < 2 * G << a.shift; v += kThreads) {
         const int e = v >> a.shift, at = v & ((1 << a.shift) - 1);
         float sum = 0.f;
         for (int j = 0; j < slots; ++j) sum += cross[e][(j << a.shift) + at];
-        const Unit m = unit_of(at, a.dim, a.r.rot, a.r.pairs);
-        const int col = e < 8 ? m.a + e : m.b + e - 8, left = e < 8 ? m.na - e : m.nb - (e - 8);
+        const Unit m = unit_of<G>(at, a.dim, a.r.rot, a.r.pairs);
+        const int col = e < G ? m.a + e : m.b + e - G, left = e < G ? m.na - e : m.nb - (e - G);
         if (left > 0) gptr(x.part)[(int64_t)block * a.dim + col] = sum;
     }
 }
@@ -363,14 +392,18 @@ __global__ __launch_bounds__(kSumCols* kSumSlices) void heads_sum_kernel(int dim
 // -------------------------------------------------------------------- host ----
 
 constexpr int kMaxHeadDim = 512;
-constexpr int kBackwardBlocks = 768;   // what the GPU holds at once at three wavefronts a SIMD
+constexpr int kBackwardBlocks = 1024;   // what the GPU holds at once at four wavefronts a SIMD
 
-int units_of(int dim, int rot, bool pairs) {
-    const int turned = pairs ? (rot + 15) / 16 : (rot / 2 + 7) / 8;
-    return turned + (dim - rot + 15) / 16;
+int units_of(int dim, int rot, bool pairs, int g) {
+    const int turned = pairs ? (rot + 2 * g - 1) / (2 * g) : (rot / 2 + g - 1) / g;
+    return turned + (dim - rot + 2 * g - 1) / (2 * g);
 }
-bool whole_groups(int dim, int rot, bool pairs) {
-    return (dim - rot) % 8 == 0 && (pairs ? rot : rot / 2) % 8 == 0;
+// The largest group of which both parts are whole ones, if a wavefront holds the
+// row in them; else 0: groups of eight, looked at element by element.
+int group_of(int dim, int rot, bool pairs) {
+    for (int g : {4, 2, 1})
+        if ((dim - rot) % g == 0 && (pairs ? rot : rot / 2) % g == 0) return units_of(dim, rot, pairs, g) <= 64 ? g : 0;
+    return 0;
 }
 
 opt_status check_heads(const opt_heads_desc* d) {
@@ -433,26 +466,26 @@ opt_status check_vector(const float* p, const char* name) {
 void set_rows(const opt_heads_desc* d, Args& a) {
     a.tokens = (uint32_t)d->tokens, a.total = (uint32_t)(d->batch * d->tokens), a.dim = d->head_dim;
     a.q.heads = d->heads, a.k.heads = d->kv_heads;
-    const int units = units_of(a.dim, a.r.rot, a.r.pairs);
+    a.group = group_of(a.dim, a.r.rot, a.r.pairs);
+    const int units = units_of(a.dim, a.r.rot, a.r.pairs, a.group ? a.group : 8);
     a.shift = 0;
     while ((1 << a.shift) < units) ++a.shift;
 }
 
-// Heads to a thread's turn: all that share a token's angles, but fewer where
+// Heads to a thread's turn: `most`, which share a token's angles (forward, as
+// above: rotation 79 us with four, 81 with eight, 90 with all; norm, both
+// directions, backward with four 100, with eight 99, with all 113), but fewer where
 // the launch would leave CUs without work.
-void set_per(Args& a, int64_t want, int step) {
-    const int most = a.q.heads > a.k.heads ? a.q.heads : a.k.heads;
-    const auto parts = [&](int heads, int per) { return (heads + per - 1) / per; };
-    a.per = most;
-    while (a.per > step && ((int64_t)a.total * (parts(a.q.heads, a.per) + parts(a.k.heads, a.per)) << a.shift) < want)
-        a.per = (a.per / 2 + step - 1) / step * step;
-    while (a.per > 1 && ((int64_t)a.total * (parts(a.q.heads, a.per) + parts(a.k.heads, a.per)) << a.shift) < want / 8) a.per = (a.per + 1) / 2;
-    a.q.parts = parts(a.q.heads, a.per), a.k.parts = parts(a.k.heads, a.per);
+void set_per(Args& a, int most) {
+    const auto parts = [&](int heads) { return (heads + a.per - 1) / a.per; };
+    for (a.per = most; a.per > 1; a.per /= 2)
+        if (((int64_t)a.total * (parts(a.q.heads) + parts(a.k.heads)) << a.shift) >= 1 << 16) break;
+    a.q.parts = parts(a.q.heads), a.k.parts = parts(a.k.heads);
 }
 
 template <class T, bool NORM>
 void forward(Args a, hipStream_t s) {
-    set_per(a, 1 << 19, kHeadsAhead);
+    set_per(a, 4);
     const int64_t parts = a.q.parts + a.k.parts, slots = kThreads >> a.shift;
     int64_t step = most_blocks(kThreads) * slots / parts;   // tokens of one launch
     const int64_t total = a.total;
@@ -460,8 +493,12 @@ void forward(Args a, hipStream_t s) {
         const int64_t n = total - first < step ? total - first : step;
         a.first = (uint32_t)first, a.total = (uint32_t)(first + n);   // none of the next launch's: out may be in
         const dim3 g((uint32_t)((n * parts + slots - 1) / slots));
-        if (whole_groups(a.dim, a.r.rot, a.r.pairs)) heads_forward_kernel<T, true, NORM><<<g, kThreads, 0, s>>>(a);
-        else heads_forward_kernel<T, false, NORM><<<g, kThreads, 0, s>>>(a);
+        switch (a.group) {
+            case 4: heads_forward_kernel<T, 4, true, NORM><<<g, kThreads, 0, s>>>(a); break;
+            case 2: heads_forward_kernel<T, 2, true, NORM><<<g, kThreads, 0, s>>>(a); break;
+            case 1: heads_forward_kernel<T, 1, true, NORM><<<g, kThreads, 0, s>>>(a); break;
+            default: heads_forward_kernel<T, 8, false, NORM><<<g, kThreads, 0, s>>>(a);
+        }
     }
 }
 template <bool NORM>
@@ -473,7 +510,7 @@ void forward(int32_t dtype, const Args& a, hipStream_t s) {
 
 // Workgroups of the backward pass for each tensor, in proportion to its heads.
 void set_blocks(Args& a) {
-    set_per(a, 1 << 18, 2);
+    set_per(a, 8);
     const int64_t slots = kThreads >> a.shift, heads = a.q.heads + a.k.heads;
     for (Side* x : {&a.q, &a.k}) {
         const int64_t need = ((int64_t)a.total * x->parts + slots - 1) / slots;
@@ -485,8 +522,12 @@ void set_blocks(Args& a) {
 template <class T>
 void backward(const Args& a, hipStream_t s) {
     const dim3 g((uint32_t)(a.q.blocks + a.k.blocks));
-    if (whole_groups(a.dim, a.r.rot, a.r.pairs)) heads_backward_kernel<T, true><<<g, kThreads, 0, s>>>(a);
-    else heads_backward_kernel<T, false><<<g, kThreads, 0, s>>>(a);
+    switch (a.group) {
+        case 4: heads_backward_kernel<T, 4, true><<<g, kThreads, 0, s>>>(a); break;
+        case 2: heads_backward_kernel<T, 2, true><<<g, kThreads, 0, s>>>(a); break;
+        case 1: heads_backward_kernel<T, 1, true><<<g, kThreads, 0, s>>>(a); break;
+        default: heads_backward_kernel<T, 8, false><<<g, kThreads, 0, s>>>(a);
+    }
 }
 
 }  // namespace

@@ -287,6 +287,8 @@ class _Rotary(NamedTuple):
     rot: int
     layout: int
     scale: float
+    device: torch.device
+    ptr: int
 
 
 class Rotary(_Rotary):
@@ -307,60 +309,70 @@ class Rotary(_Rotary):
         turns = [round(Fraction(x) / _TWO_PI * (1 << 64)) % (1 << 64) for x in f]
         table = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
         code = native.OPT_ROTARY_HALF if layout == "half" else native.OPT_ROTARY_PAIRS
-        return super().__new__(cls, table, 2 * len(f), code, float(scale))
+        return super().__new__(cls, table, 2 * len(f), code, float(scale), table.device, table.data_ptr())
 
-    def c(self, positions, first, dev, lead):
-        """The descriptor for tokens of shape ``lead``, (batch, tokens) or (tokens,)."""
-        if self.turns.device != dev:
-            raise ValueError(f"rope is on {self.turns.device}, expected {dev}")
+    def c(self, positions, first, q):
+        """The descriptor for the tokens of q."""
+        turns, rot, layout, scale, device, ptr = self
+        dev = q.device
+        if device != dev:
+            raise ValueError(f"rope is on {device}, expected {dev}")
         if positions is None:
-            return native.opt_rotary(self.turns.data_ptr(), self.rot, self.layout, self.scale, 0, 0, 0, 0, first)
+            return native.opt_rotary(ptr, rot, layout, scale, 0, 0, 0, 0, first)
         if first:
             raise ValueError("first goes without positions")
         if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
             raise ValueError("positions must be an int32 or int64 tensor")
-        shape = positions.shape
+        lead, shape = q.shape[:-2], positions.shape
         if positions.device != dev or (shape != lead and shape != lead[-1:]):
             _is(positions, "positions", dev, positions.dtype, lead)
         s = positions.stride()
-        return native.opt_rotary(self.turns.data_ptr(), self.rot, self.layout, self.scale,
-                                 positions.dtype == torch.int64, positions.data_ptr(), s[0] if len(s) == 2 else 0,
-                                 s[-1])
+        return native.opt_rotary(ptr, rot, layout, scale, positions.dtype is torch.int64, positions.data_ptr(),
+                                 s[0] if len(s) == 2 else 0, s[-1])
 
 
-def _heads(q, k, names):
-    """(descriptor, device, leading shape) of queries and keys (k may be None)."""
-    code, dim = _code(q, names[0]), q.dim()
-    if dim not in (3, 4):
-        raise ValueError(f"{names[0]} must have axes (batch, tokens, heads, dim) or (tokens, heads, dim)")
-    qs, ks = q.shape, None if k is None else k.shape
-    if k is not None and not (k.dtype == q.dtype and k.device == q.device and len(ks) == dim
-                              and ks[:-2] == qs[:-2] and ks[-1] == qs[-1]):
-        _is(k, names[1], q.device, q.dtype)
-        raise ValueError(f"{names[1]} has shape {tuple(ks)}, expected {tuple(qs)} but for the heads")
-    d = native.opt_heads_desc(code, qs[-2], 0 if k is None else ks[-2], qs[-1], qs[0] if dim == 4 else 1, qs[-3])
-    return d, q.device, qs[:-2]
+def _heads(q, k, q_name, k_name):
+    """The descriptor of queries and keys (k may be None)."""
+    qs = q.shape
+    if len(qs) == 4:
+        batch, tokens, heads, dim = qs
+    elif len(qs) == 3:
+        batch, (tokens, heads, dim) = 1, qs
+    else:
+        raise ValueError(f"{q_name} must have axes (batch, tokens, heads, dim) or (tokens, heads, dim)")
+    kv = 0
+    if k is not None:
+        ks = k.shape
+        if not (k.dtype is q.dtype and k.device == q.device and len(ks) == len(qs) and ks[-1] == dim
+                and ks[-3] == tokens and ks[0] == qs[0]):
+            _is(k, k_name, q.device, q.dtype)
+            raise ValueError(f"{k_name} has shape {tuple(ks)}, expected {tuple(qs)} but for the heads")
+        kv = ks[-2]
+    return native.opt_heads_desc(_code(q, q_name), heads, kv, dim, batch, tokens)
 
 
-def _like(t, name, like, dev):
-    if not (t.dtype == like.dtype and t.device == dev and t.shape == like.shape):
-        _is(t, name, dev, like.dtype, like.shape)
+def _like(t, name, like):
+    """The given result, or a new one."""
+    if t is None:
+        return torch.empty_like(like)
+    if not (t.dtype is like.dtype and t.device == like.device and t.shape == like.shape):
+        _is(t, name, like.device, like.dtype, like.shape)
     return t
 
 
 def _rotary(names, q, k, rope, positions, first, out_q, out_k, inverse):
-    d, dev, lead = _heads(q, k, names)
-    if not isinstance(rope, Rotary):
+    d = _heads(q, k, names[0], names[1])
+    if rope.__class__ is not Rotary:
         raise TypeError("rope must be a Rotary")
-    r = rope.c(positions, first, dev, lead)
-    st = _stream(dev)
-    yq = q.new_empty(q.shape) if out_q is None else _like(out_q, names[2], q, dev)
-    tq, ty = _bhtd(q, names[0]), _bhtd(yq, names[2])
+    r = rope.c(positions, first, q)
+    st = _stream(q.device)
+    yq = _like(out_q, names[2], q)
     if k is None:
-        native.opt_rotary_apply(d, r, inverse, tq, None, ty, None, st)
+        native.opt_rotary_apply(d, r, inverse, _bhtd(q, names[0]), None, _bhtd(yq, names[2]), None, st)
         return yq, None
-    yk = k.new_empty(k.shape) if out_k is None else _like(out_k, names[3], k, dev)
-    native.opt_rotary_apply(d, r, inverse, tq, _bhtd(k, names[1]), ty, _bhtd(yk, names[3]), st)
+    yk = _like(out_k, names[3], k)
+    native.opt_rotary_apply(d, r, inverse, _bhtd(q, names[0]), _bhtd(k, names[1]), _bhtd(yq, names[2]),
+                            _bhtd(yk, names[3]), st)
     return yq, yk
 
 
@@ -380,14 +392,14 @@ def rotary_backward(dyq, dyk, rope, positions=None, *, first=0, dq=None, dk=None
     return _rotary(("dyq", "dyk", "dq", "dk"), dyq, dyk, rope, positions, first, dq, dk, 1)
 
 
-def _rope(rope, positions, first, dev, lead):
+def _rope(rope, positions, first, q):
     if rope is None:
         if positions is not None or first:
             raise ValueError("positions go with a rope")
         return None
-    if not isinstance(rope, Rotary):
+    if rope.__class__ is not Rotary:
         raise TypeError("rope must be a Rotary or None")
-    return rope.c(positions, first, dev, lead)
+    return rope.c(positions, first, q)
 
 
 @_streamed
@@ -397,19 +409,20 @@ def qk_norm_forward(q, k, q_weight, k_weight, *, eps=1e-6, rope=None, positions=
     turned as rotary_forward turns it (rope None: not turned). k may be None, and
     with it what belongs to keys. out_q may be q and out_k may be k (but the
     backward pass needs q and k)."""
-    d, dev, lead = _heads(q, k, ("q", "k"))
-    r = _rope(rope, positions, first, dev, lead)
-    wq = _vector(q_weight, "q_weight", dev, d.head_dim)
+    d, dev = _heads(q, k, "q", "k"), q.device
+    r = _rope(rope, positions, first, q)
+    dim = q.shape[-1]
+    wq = _vector(q_weight, "q_weight", dev, dim)
+    wk = 0 if k is None else _vector(k_weight, "k_weight", dev, dim)
     st = _stream(dev)
-    yq = q.new_empty(q.shape) if out_q is None else _like(out_q, "out_q", q, dev)
+    yq = _like(out_q, "out_q", q)
     q_rstd = q_weight.new_empty(q.shape[:-1])
     if k is None:
         native.opt_qk_norm_forward(d, r, _bhtd(q, "q"), None, wq, 0, eps, _bhtd(yq, "out_q"), None,
                                    q_rstd.data_ptr(), 0, st)
         return yq, None, q_rstd, None
-    wk = _vector(k_weight, "k_weight", dev, d.head_dim)
-    yk = k.new_empty(k.shape) if out_k is None else _like(out_k, "out_k", k, dev)
-    k_rstd = k_weight.new_empty(k.shape[:-1])
+    yk = _like(out_k, "out_k", k)
+    k_rstd = q_weight.new_empty(k.shape[:-1])
     native.opt_qk_norm_forward(d, r, _bhtd(q, "q"), _bhtd(k, "k"), wq, wk, eps, _bhtd(yq, "out_q"), _bhtd(yk, "out_k"),
                                q_rstd.data_ptr(), k_rstd.data_ptr(), st)
     return yq, yk, q_rstd, k_rstd
@@ -429,20 +442,23 @@ def qk_norm_backward(dyq, dyk, q, k, q_weight, k_weight, q_rstd, k_rstd, *, rope
     """(dq, dk, dq_weight, dk_weight) from the gradients of qk_norm_forward's
     results, what it took and the rstd it returned. dq and dk may be given, for
     instance as views of one projection's gradient, or be dyq and dyk."""
-    d, dev, lead = _heads(q, k, ("q", "k"))
-    r = _rope(rope, positions, first, dev, lead)
-    for t, name, like in ((dyq, "dyq", q), (dyk, "dyk", k)):
-        if like is not None:
-            _like(t, name, like, dev)
+    d, dev = _heads(q, k, "q", "k"), q.device
+    r = _rope(rope, positions, first, q)
+    if dyq is None or (dyk is None) != (k is None):
+        raise ValueError("dyq goes with q and dyk with k")
+    dyq = _like(dyq, "dyq", q)
+    dyk = dyk if k is None else _like(dyk, "dyk", k)
     if dyq.stride(-1) != 1:   # an expanded gradient has stride 0
         dyq = dyq.contiguous()
     if k is not None and dyk.stride(-1) != 1:
         dyk = dyk.contiguous()
-    wq = _vector(q_weight, "q_weight", dev, d.head_dim)
+    dim = q.shape[-1]
+    wq, wk = _vector(q_weight, "q_weight", dev, dim), 0 if k is None else _vector(k_weight, "k_weight", dev, dim)
     sq = _statistic(q_rstd, "q_rstd", dev, q.shape[:-1])
+    sk = 0 if k is None else _statistic(k_rstd, "k_rstd", dev, k.shape[:-1])
     st = _stream(dev)
-    gq = q.new_empty(q.shape) if dq is None else _like(dq, "dq", q, dev)
-    gwq = q_weight.new_empty(d.head_dim)
+    gq = _like(dq, "dq", q)
+    gwq = torch.empty_like(q_weight)
     n = native.opt_qk_norm_workspace_size(d)
     ws = _bytes(q, n)
     wp = ws.data_ptr() if n else 0
@@ -450,10 +466,8 @@ def qk_norm_backward(dyq, dyk, q, k, q_weight, k_weight, q_rstd, k_rstd, *, rope
         native.opt_qk_norm_backward(d, r, _bhtd(dyq, "dyq"), None, _bhtd(q, "q"), None, wq, 0, sq, 0, _bhtd(gq, "dq"),
                                     None, gwq.data_ptr(), 0, wp, n, st)
         return gq, None, gwq, None
-    wk = _vector(k_weight, "k_weight", dev, d.head_dim)
-    sk = _statistic(k_rstd, "k_rstd", dev, k.shape[:-1])
-    gk = k.new_empty(k.shape) if dk is None else _like(dk, "dk", k, dev)
-    gwk = k_weight.new_empty(d.head_dim)
+    gk = _like(dk, "dk", k)
+    gwk = torch.empty_like(k_weight)
     native.opt_qk_norm_backward(d, r, _bhtd(dyq, "dyq"), _bhtd(dyk, "dyk"), _bhtd(q, "q"), _bhtd(k, "k"), wq, wk, sq, sk,
                                 _bhtd(gq, "dq"), _bhtd(gk, "dk"), gwq.data_ptr(), gwk.data_ptr(), wp, n, st)
     return gq, gk, gwq, gwk
