@@ -84,7 +84,8 @@ struct AttnArgs {
     uint32_t first;   // of the workgroups, this launch's first
     int32_t listed;   // packed: row blocks are found by their place in a list (find_listed)
     int32_t pack;     // forward: the heads of a group are rows of one block (PACK kernels)
-    int32_t sinks, tail_splits;   // first keys that the window does not hide (SINK kernels), splits of their queries
+    int32_t sinks, tail_splits;   // first keys that the window does not hide, splits of their queries
+    int32_t sink_kernels;         // sinks were asked for: the SINK kernels, also where the window hides nothing
     float scale;
 };
 
@@ -174,8 +175,11 @@ __device__ __forceinline__ void copy16(uint32_t lds, const void* src) {
 }
 // The same from a uniform address and an offset below 2^32 in each lane.
 __device__ __forceinline__ void copy16(uint32_t lds, const char* base, uint32_t off) {
+    const uint64_t b = (uint64_t)base;
+    const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);   // in scalar registers, whatever computed it
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base) : "memory");
+                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(u) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t lds, const void* src) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
@@ -459,8 +463,8 @@ __device__ __forceinline__ bool block_of(const AttnArgs& a, int blocks, int rows
 // Key tiles [first, end) of this workgroup's queries and split; with sinks,
 // places in the list that `tiles` maps to tiles.
 template <bool SINK>
-__device__ __forceinline__ void tile_range(const AttnArgs& a, const Sight& see, int i0, int rows, int nq, int split, int& first, int& end,
-                                           Tiles& tiles) {
+__device__ __forceinline__ void tile_range(const AttnArgs& a, const Sight& see, int i0, int rows, int nq, int splits, int split, int& first,
+                                           int& end, Tiles& tiles) {
     first = end = 0;
     if (i0 >= nq) return;
     const int hi = see.hi(min(i0 + rows, nq) - 1);
@@ -472,8 +476,8 @@ __device__ __forceinline__ void tile_range(const AttnArgs& a, const Sight& see, 
         first = 0;
         end -= tiles.skip;
     }
-    if (a.splits > 1) {
-        const int each = (max(end - first, 0) + a.splits - 1) / a.splits;
+    if (splits > 1) {
+        const int each = (max(end - first, 0) + splits - 1) / splits;
         first += split * each;
         end = min(end, first + each);
     }
@@ -618,7 +622,7 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_forward_kernel(AttnArgs
     const float c = a.scale * kLog2e;
     int first_t, end_t;
     Tiles tiles = {0, 0};
-    tile_range<SINK>(a, see, query(i0), PACK ? sq.nq : 32 * W, sq.nq, wg.split, first_t, end_t, tiles);
+    tile_range<SINK>(a, see, query(i0), PACK ? sq.nq : 32 * W, sq.nq, a.splits, wg.split, first_t, end_t, tiles);
     // keys that any query of this wavefront sees, and the lane's
     const int wfirst = query(w0), wlast = query(min(w0 + 32, nrows) - 1);
     const int whi = w0 < nrows ? see.hi(wlast) : 0, wlo = see.lo(wfirst);
@@ -807,27 +811,73 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
     if (i < sq.nq) {
         L2 = gptr(a.lse)[at_row] * kLog2e;
         if (L2 == -INFINITY) L2 = INFINITY;
-        if (h == 0 && set == 0 && wg.split == 0) {
-            gptr(a.delta)[at_row] = D * kLower<T>;
-            gptr(a.l2)[at_row] = L2 == INFINITY ? INFINITY : fmaf(gptr(a.lse)[at_row], kLog2e, (float)-kLift<T>);
-        }
     }
     Copy<DB, W> ck, cv;
     ck.init(a.k.token);
     cv.init(a.v.token);
     const char* kb = rows_of(a.k, b, sq.k0, hk);
     const char* vb = rows_of(a.v, b, sq.k0, hk);
-    f32x16 dq[DB] = {};
     const float c = a.scale * kLog2e;
     int first_t, end_t;
     Tiles tiles = {0, 0};
-    tile_range<SINK>(a, see, i0, 32 * W, sq.nq, wg.split, first_t, end_t, tiles);
+    tile_range<SINK>(a, see, i0, 32 * W, sq.nq, a.splits, wg.split, first_t, end_t, tiles);
     const int wlast = min(w0 + 32, sq.nq) - 1;
     const int whi = w0 < sq.nq ? see.hi(wlast) : 0, wlo = see.lo(w0);
     const int hi = i < sq.nq ? see.hi(i) : 0, lo = see.lo(i);
     const int full_hi = see.hi(w0) / kTile, full_lo = (see.lo(max(wlast, w0)) + kTile - 1) / kTile;
 
     auto kt = [&](int r) { return smem + (4 * set + (r & 1)) * G::BYTES; };
+    if constexpr (SINK) {
+        // D of rows that see few keys, from P and dP themselves: O is a sum of
+        // rounded P and rounded itself, which dP - D shows where it does not
+        // average out (4 keys in sight, bf16: dQ 6.4e-3 off in norm, 2.4e-3 so;
+        // from 32 keys on it is below the rounding of dS). Such rows are a sequence's
+        // first ones, or all with a window below 32: a few tiles, which every set and
+        // split walks through as a whole. A row of one key keeps the D above.
+        const auto seen = [&](int row) { return see.hi(row) - see.lo(row) + min(see.lo(row), a.sinks); };
+        if (i0 < sq.nq && seen(i0) < 32) {
+            int from, to;
+            Tiles all = {0, 0};
+            tile_range<true>(a, see, i0, 32 * W, sq.nq, 1, 0, from, to, all);
+            auto load = [&](int n) {
+                if (n >= to) return;
+                ck.tile(kt(n - from), kb, all(n) * kTile, sq.nk, a.head_dim);
+                cv.tile(kt(n - from) + 2 * G::BYTES, vb, all(n) * kTile, sq.nk, a.head_dim);
+            };
+            float x = 0.f;
+            load(from);
+            for (int n = from; n < to; ++n) {
+                tile_barrier();
+                load(n + 1);
+                const int t = all(n);
+                const Lane<T, DB> at = ln.in(kt(n - from));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    f32x16 s = {}, dp = {};
+#pragma unroll
+                    for (int ks = 0; ks < 2 * DB; ++ks) {
+                        s = FT::mma(at.rows(0, u, ks), qf[ks], s);
+                        dp = FT::mma(at.rows(2 * G::BYTES, u, ks), gf[ks], dp);
+                    }
+                    hide_from(s, hi, t * kTile + 32 * u);
+                    hide_window<true>(s, a.sinks, wlo, lo, t * kTile + 32 * u);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float p = __builtin_amdgcn_exp2f(fmaf(s[e], c, -L2));
+                        x = p > 0.f ? fmaf(p, dp[e], x) : x;   // not 0 times what is out of sight
+                    }
+                }
+            }
+            x += other_half(x);
+            if (i < sq.nq && seen(i) > 1) D = x;
+            tile_barrier();   // the tiles are read: the loop below fills them anew
+        }
+    }
+    if (i < sq.nq && h == 0 && set == 0 && wg.split == 0) {
+        gptr(a.delta)[at_row] = D * kLower<T>;
+        gptr(a.l2)[at_row] = L2 == INFINITY ? INFINITY : fmaf(gptr(a.lse)[at_row], kLog2e, (float)-kLift<T>);
+    }
+    f32x16 dq[DB] = {};
     auto fill = [&](int r) {
         int t = first_t + SETS * r + set;
         if (t >= end_t) return;
@@ -1233,7 +1283,8 @@ AttnArgs attn_args(const opt_attention_desc* a, bool backward) {
     x.window = a->window < x.k_len ? a->window : 0;   // as long as the keys: it hides none
     x.sinks = !x.window ? 0 : a->sinks < x.k_len ? a->sinks : x.k_len;
     const int group = a->heads / a->kv_heads;
-    x.pack = !backward && x.sinks && group > 1 && (int64_t)x.q_len * group <= 128;
+    x.sink_kernels = a->sinks > 0;
+    x.pack = !backward && x.sink_kernels && group > 1 && (int64_t)x.q_len * group <= 128;
     return x;
 }
 
@@ -1378,7 +1429,7 @@ void launch_kind(Kind kind, const AttnArgs& x, hipStream_t s) {
 template <class T, int DB>
 void launch(Kind kind, const AttnArgs& x, hipStream_t s) {
     if ((kind == DKV ? x.k_len : x.q_len) == 0 || x.batch == 0) return;
-    x.sinks ? launch_kind<T, DB, true>(kind, x, s) : launch_kind<T, DB, false>(kind, x, s);
+    x.sink_kernels ? launch_kind<T, DB, true>(kind, x, s) : launch_kind<T, DB, false>(kind, x, s);
     if (kind == DKV ? x.kv_splits > 1 : x.splits > 1) {
         const int jb = (int)row_blocks(kind == DKV ? x.k_len : x.q_len, kJoinRows);
         const int64_t n = (int64_t)jb * x.batch * (kind == DKV ? x.kv_heads : x.heads);

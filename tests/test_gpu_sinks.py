@@ -240,3 +240,45 @@ def test_equal_inputs_give_equal_bits_and_graphs_replay(nq, nk):
 def run_unsynced(train, q, k, v, dout, **how):
     out, lse = train.attention_forward(q, k, v, **how)
     return (out, lse, *train.attention_backward(dout, q, k, v, out, lse, **how))
+
+
+@pytest.mark.parametrize("nq,nk,window,sinks,batch", [(1, 300, 4, 1, 2), (1, 300, 1, 3, 1), (2, 2, 22, 4, 3), (200, 200, 3, 2, 1),
+                                                      (60, 60, 100, 4, 2), (300, 300, 2, 20, 1), (25, 25, 9, 9, 40)])
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_rows_of_few_keys_lose_nothing_to_rounded_outputs(nq, nk, window, sinks, batch, d, dtype):
+    """Where a row sees few keys, D comes from P and dP in fp32 and not from the stored out: the bound of
+    test_gpu_attention.py without out's error in D, which is off by what P and dP are, 2^-12 of sum P |dP|."""
+    from tests.test_gpu_attention import SLACK, TINY, worst
+    print(f"sinks few keys {nq} {nk} window {window} sinks {sinks} batch {batch} d {d} {dtype}", flush=True)
+    mk = normal(nq + d, dtype)
+    q, k, v, dout = mk(batch, nq, 4, d), mk(batch, nk, 2, d), mk(batch, nk, 2, d), mk(batch, nq, 4, d)
+    got = {n: np64(t) for n, t in run(q, k, v, dout, causal=True, window=window, sinks=sinks).items()}
+    see, u, scale = T.visible(nq, nk, True, window, sinks), U[dtype], d ** -0.5
+    few = see.sum(1) < 32
+    assert few.any()
+    for b in range(batch):
+        dk, bound = np.zeros((nk, 2, d)), np.zeros((nk, 2, d))
+        for h in range(4):
+            x, kk, vv, g = np64(q[b, :, h]), np64(k[b, :, h // 2]), np64(v[b, :, h // 2]), np64(dout[b, :, h])
+            r = T.attention(x, kk, vv, scale, see, g)
+            e_D = SLACK * (r["p"] * np.abs(r["dp"])).sum(1)
+            e_ds = (u * np.abs(r["ds"]) + r["p"] * e_D[:, None] + SLACK * r["p"] * (np.abs(r["dp"]) + np.abs(r["D"])[:, None])
+                    + TINY * see)
+            e_dq = u * np.abs(r["dq"]) + scale * e_ds @ np.abs(kk) + SLACK * scale * np.abs(r["ds"]) @ np.abs(kk)
+            assert worst(got["dq"][b, few, h], r["dq"][few], e_dq[few]) <= 1
+            dk[:, h // 2] += r["dk"]
+            bound[:, h // 2] += scale * e_ds.T @ np.abs(x) + SLACK * scale * np.abs(r["ds"]).T @ np.abs(x)
+        if few.all():
+            assert worst(got["dk"][b], dk, bound + u * np.abs(dk)) <= 1
+
+
+def test_one_key_in_sight_has_no_score_gradient():
+    """One query at the first position of a cache of one key, and windows of one key without other sinks in reach."""
+    torch = _torch()
+    mk = normal(3)
+    for batch, nq, nk in ((17, 1, 1), (2, 40, 1)):
+        q, k, v, dout = mk(batch, nq, 8, 64), mk(batch, nk, 4, 64), mk(batch, nk, 4, 64), mk(batch, nq, 8, 64)
+        got = run(q, k, v, dout, causal=True, window=3, sinks=1)
+        assert not got["dq"].any() and not got["dk"].any()
+        assert torch.equal(got["out"][:, -1], v[:, 0].repeat_interleave(2, dim=1))
