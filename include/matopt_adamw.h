@@ -67,7 +67,8 @@ typedef struct {
 opt_status opt_adamw_workspace_size(const opt_adamw_desc* descs, int32_t count, uint64_t* bytes);
 
 /* Checks the tensors (none may overlap, but for gradients with each other) and
- * uploads the table; returns when it is on the device. t starts at 0. */
+ * uploads the table; returns when it is on the device (so the stream may not be
+ * captured). t starts at 0. */
 opt_status opt_adamw_create(const opt_adamw_desc* descs, int32_t count, const opt_adamw_hparams* hp, void* workspace,
                             uint64_t workspace_bytes, void* stream, opt_adamw_t* out);
 

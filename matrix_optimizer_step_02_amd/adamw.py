@@ -104,7 +104,10 @@ class AdamWGroup:
     float8_e4m3fn and float8_e5m2 with m_scale and v_scale), and, where wanted, W16 (a bf16
     or fp16 copy of W that each step writes), weight_decay and lr_scale. All
     tensors are the caller's, contiguous, on the current device, and referenced here.
-    The order of the tensors is part of what 8-bit states are rounded by."""
+    The order of the tensors is part of what 8-bit states are rounded by.
+
+    A group outlives the graphs that its calls are captured into. Its calls share a
+    workspace: two of them on different streams are the caller's to order."""
 
     def __init__(self, params: Sequence[dict], hp: Optional[AdamWHyper] = None, stream=None):
         self.params, self.hp = list(params), AdamWHyper() if hp is None else hp
@@ -116,10 +119,11 @@ class AdamWGroup:
             if p["W"].device != dev:
                 raise ValueError(f"W is on {p['W'].device}, expected {dev}")
         n = native.opt_adamw_workspace_size(self.descs)
+        self._streams = set()   # that have run calls of the group
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=dev) if dev.type == "cuda" else None
+        # what the table points to, whatever becomes of the dicts
+        self._held = [self.workspace, *(t for p in self.params for t in p.values() if isinstance(t, torch.Tensor))]
         st = self._stream(stream)
-        self.workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            self.workspace.record_stream(stream)
         self._g = native.opt_adamw_create(self.descs, self.hp.c(), self.workspace.data_ptr(), n, st)
 
     def _stream(self, stream):
@@ -128,7 +132,12 @@ class AdamWGroup:
             raise ValueError("tensors must live on a HIP device")
         if dev.index != torch._C._cuda_getDevice():
             raise ValueError(f"tensors are on {dev}, which is not the current device (torch.cuda.device)")
-        return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+        st = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+        if st not in self._streams:   # no memory of the group is handed out again before this stream is past its calls
+            for t in self._held:
+                t.record_stream(torch.cuda.current_stream() if stream is None else stream)
+            self._streams.add(st)
+        return st
 
     def _scalar(self, t, name, dtype, stream):
         if t is None:

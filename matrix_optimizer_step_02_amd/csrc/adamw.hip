@@ -445,6 +445,12 @@ opt_status create(const opt_adamw_desc* d, int32_t count, const opt_adamw_hparam
     for (const Span& s : spans)
         if (s.lo < (uintptr_t)ws + l.bytes && (uintptr_t)ws < s.hi)
             return fail(OPT_EINVAL, "tensor %d: %s overlaps the workspace", s.tensor, s.what);
+    if (stream) {
+        hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+        const hipError_t e = hipStreamIsCapturing((hipStream_t)stream, &capture);
+        if (e != hipSuccess) return hip_fail(e, "hipStreamIsCapturing");
+        if (capture != hipStreamCaptureStatusNone) return fail(OPT_ESTATE, "a group is not created while its stream is captured");
+    }
     std::vector<char> image(l.part, 0);
     Seg* segs = (Seg*)image.data();
     Chunk* chunks = (Chunk*)(image.data() + l.chunks);

@@ -340,6 +340,49 @@ def test_learning_rate_is_set_between_steps():
     check(p, 0, before, 2, lr=1.0)
 
 
+def test_a_group_is_not_created_in_a_capture():
+    torch, mo = _torch(), _mo()
+    p, x = param(100), torch.zeros(8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.add_(1)
+        with pytest.raises(mo.MatoptError, match="captured"):
+            mo.AdamWGroup([p])
+        x.add_(1)
+    for n in range(1, 4):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bool((x == 2 * n).all())
+
+
+def test_memory_is_kept_until_every_stream_is_past_it():
+    """A group that is dropped behind its last call on another stream: its table is
+    not handed out again while that call waits. Nor is a gradient that the caller's
+    dict no longer names while the group lives."""
+    torch, mo = _torch(), _mo()
+    p, s = param(5000), torch.cuda.Stream()
+    group = mo.AdamWGroup([p], mo.AdamWHyper(**HP))
+    at, n = group.workspace.data_ptr(), group.workspace.numel()
+    before, grad = snap(p), p["G"].clone()
+    g_at = p["G"].data_ptr()
+    p["G"] = torch.zeros_like(grad)
+    assert all(torch.empty_like(grad).data_ptr() != g_at for _ in range(4))
+    p["G"] = grad
+    a = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            a @ a
+        group.step()
+    del group
+    got = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    if not s.query():
+        assert all(x.data_ptr() != at for x in got)
+    torch.cuda.synchronize()
+    check(p, 0, before, 1)
+
+
 def test_past_2_31_elements():
     torch, mo = _torch(), _mo()
     from matrix_optimizer_step_02_amd import train
