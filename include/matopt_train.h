@@ -137,7 +137,7 @@ typedef struct {
     int64_t batch, tokens;     /* batch * tokens < 2^31 */
 } opt_heads_desc;
 
-/* yq may be q and yk may be k (same strides). */
+/* yq may be q and yk may be k (same strides); results do not overlap otherwise. */
 opt_status opt_rotary_apply(const opt_heads_desc* d, const opt_rotary* r, int32_t inverse, const opt_attention_tensor* q,
                             const opt_attention_tensor* k, const opt_attention_tensor* yq,
                             const opt_attention_tensor* yk, void* stream);
@@ -149,7 +149,7 @@ opt_status opt_rotary_apply(const opt_heads_desc* d, const opt_rotary* r, int32_
  *   g = R^T dy,  z = g w,  xh = x rstd,  dx = rstd (z - xh mean(z xh)),  dw = sum g xh
  * Weights (head_dim) and their gradients are fp32, one for all heads of q and one
  * for those of k; rstd is fp32, (batch, tokens, heads) contiguous. yq may be q, dq
- * may be dyq or q (same strides), and so for k.
+ * may be dyq or q (same strides), and so for k; results do not overlap otherwise.
  */
 opt_status opt_qk_norm_forward(const opt_heads_desc* d, const opt_rotary* r, const opt_attention_tensor* q,
                                const opt_attention_tensor* k, const float* q_weight, const float* k_weight, float eps,

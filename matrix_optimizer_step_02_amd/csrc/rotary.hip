@@ -458,6 +458,32 @@ opt_status check_tensor(const opt_heads_desc* d, const opt_attention_tensor* t, 
     return OPT_OK;
 }
 
+// A result in its input's place: every element has to be written where it was read.
+opt_status check_place(const opt_heads_desc* d, int heads, const Heads& y, const Heads& x, const char* y_name, const char* x_name) {
+    const bool same = (d->batch == 1 || y.batch == x.batch) && (d->tokens == 1 || y.token == x.token) && (heads == 1 || y.head == x.head);
+    if (y.p == x.p && !same) return fail(OPT_EINVAL, "%s is %s with other strides", y_name, x_name);
+    return OPT_OK;
+}
+opt_status check_apart(const opt_heads_desc* d, const Args& a, const char* q_name, const char* k_name) {
+    if (d->kv_heads && a.q.out.p == a.k.out.p) return fail(OPT_EINVAL, "%s and %s are the same memory", q_name, k_name);
+    return OPT_OK;
+}
+opt_status check_places(const opt_heads_desc* d, const Args& a) {
+    if (opt_status st = check_place(d, d->heads, a.q.out, a.q.in, "yq", "q")) return st;
+    if (d->kv_heads)
+        if (opt_status st = check_place(d, d->kv_heads, a.k.out, a.k.in, "yk", "k")) return st;
+    return check_apart(d, a, "yq", "yk");
+}
+opt_status check_gradient_places(const opt_heads_desc* d, const Args& a) {
+    if (opt_status st = check_place(d, d->heads, a.q.out, a.q.in, "dq", "q")) return st;
+    if (opt_status st = check_place(d, d->heads, a.q.out, a.q.dy, "dq", "dyq")) return st;
+    if (d->kv_heads) {
+        if (opt_status st = check_place(d, d->kv_heads, a.k.out, a.k.in, "dk", "k")) return st;
+        if (opt_status st = check_place(d, d->kv_heads, a.k.out, a.k.dy, "dk", "dyk")) return st;
+    }
+    return check_apart(d, a, "dq", "dk");
+}
+
 opt_status check_vector(const float* p, const char* name) {
     if (!p || !train_aligned(p, 4)) return fail(OPT_EINVAL, "%s is NULL or not aligned to 4 bytes", name);
     return OPT_OK;
@@ -551,6 +577,7 @@ opt_status opt_rotary_apply(const opt_heads_desc* d, const opt_rotary* r, int32_
         if (opt_status st = check_tensor(d, k, "k", d->kv_heads, false, a.k.in)) return st;
         if (opt_status st = check_tensor(d, yk, "yk", d->kv_heads, true, a.k.out)) return st;
     }
+    if (opt_status st = check_places(d, a)) return st;
     if (opt_status st = train_pending()) return st;
     set_rows(d, a);
     forward<false>(d->dtype, a, (hipStream_t)stream);
@@ -576,6 +603,7 @@ opt_status opt_qk_norm_forward(const opt_heads_desc* d, const opt_rotary* r, con
         if (opt_status st = check_vector(k_weight, "k_weight")) return st;
         if (opt_status st = check_vector(k_rstd, "k_rstd")) return st;
     }
+    if (opt_status st = check_places(d, a)) return st;
     if (opt_status st = train_pending()) return st;
     a.q.w = q_weight, a.k.w = k_weight, a.q.rstd = q_rstd, a.k.rstd = k_rstd, a.eps = eps;
     set_rows(d, a);
@@ -620,6 +648,7 @@ opt_status opt_qk_norm_backward(const opt_heads_desc* d, const opt_rotary* r, co
             return fail(OPT_ENOWS, "workspace of %llu bytes, %llu needed", (unsigned long long)workspace_bytes,
                         (unsigned long long)need);
         if (!workspace || !train_aligned(workspace, 256)) return fail(OPT_EINVAL, "workspace is NULL or not 256-byte aligned");
+        if (opt_status st = check_gradient_places(d, a)) return st;
     }
     if (opt_status st = train_pending()) return st;
     hipStream_t s = (hipStream_t)stream;

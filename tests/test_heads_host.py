@@ -164,3 +164,20 @@ def test_a_ropes_table_is_recorded_with_the_tensors(N):
     from matrix_optimizer_step_02_amd import train
     r = train.Rotary([1.0, 2.0], device="cpu")
     assert any(t is r.turns for t in train._tensors((r,)))
+
+
+def test_results_that_overlap_are_refused(N):
+    """In the place of an input with other strides, or both in one place."""
+    d, r = desc(N), rope(N)
+    far = [tensor(N, BASE + (i << 20)) for i in range(8)]   # q, k, yq, yk, dyq, dyk, dq, dk
+    other = dict(b=8 * 512, t=512, h=128)
+    for call, pairs in ((0, ((2, 0), (3, 1))), (1, ((2, 0), (3, 1))), (2, ((6, 2), (6, 4), (7, 3), (7, 5)))):
+        for y, x in pairs:
+            ts = list(far)
+            if call == 2:   # q and k of the backward pass
+                x = {2: 0, 3: 1, 4: 4, 5: 5}[x]
+            ts[y] = tensor(N, ts[x].data, **other)
+            refused(N, "EINVAL", *calls(N, d, r, ts)[call])
+        ts = list(far)
+        ts[3 if call < 2 else 7] = ts[2 if call < 2 else 6]
+        refused(N, "EINVAL", *calls(N, d, r, ts)[call])
