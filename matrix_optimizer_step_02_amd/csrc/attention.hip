@@ -1153,10 +1153,11 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kv_kernel(AttnArgs a, 
 // Adds the splits of the sinks' dK and dV, in place of what the windows' launch
 // wrote there.
 template <class T>
-__global__ __launch_bounds__(kJoinThreads) void attn_join_tail_kernel(AttnArgs a, int width, int blocks) {
-    const int b = blockIdx.x / blocks / a.kv_heads, hk = blockIdx.x / blocks % a.kv_heads;
+__global__ __launch_bounds__(kJoinThreads) void attn_join_tail_kernel(AttnArgs a, int width, uint32_t blocks) {
+    const uint32_t at = a.first + blockIdx.x, pair = at / blocks;
+    const int b = pair / a.kv_heads, hk = pair % a.kv_heads;
     const Seq sq = sequence(a, b);
-    const int j = blockIdx.x % blocks * kJoinRows + threadIdx.x / 16, col = threadIdx.x % 16 * 8;
+    const int j = at % blocks * kJoinRows + threadIdx.x / 16, col = threadIdx.x % 16 * 8;
     if (j >= min(a.sinks, sq.nk) || col >= a.head_dim) return;
     const bool v_part = blockIdx.y;
     const float* part = v_part ? a.tail_v : a.tail;
@@ -1414,8 +1415,13 @@ void launch_tail(AttnArgs x, hipStream_t s) {
         x.first = (uint32_t)first;
         attn_dkv_kernel<T, DB, 4, 1, true><<<dim3((uint32_t)(grid - first < most ? grid - first : most)), 256, 0, s>>>(x, (int)blocks);
     }
-    const int jb = (int)row_blocks(x.sinks, kJoinRows);
-    attn_join_tail_kernel<T><<<dim3((uint32_t)((int64_t)jb * x.batch * x.kv_heads), 2), kJoinThreads, 0, s>>>(x, 32 * DB, jb);
+    const int64_t jb = row_blocks(x.sinks, kJoinRows), joins = jb * x.batch * x.kv_heads;
+    constexpr int64_t most_joins = most_blocks(kJoinThreads);
+    for (int64_t first = 0; first < joins; first += most_joins) {
+        x.first = (uint32_t)first;
+        const dim3 g((uint32_t)(joins - first < most_joins ? joins - first : most_joins), 2);
+        attn_join_tail_kernel<T><<<g, kJoinThreads, 0, s>>>(x, 32 * DB, (uint32_t)jb);
+    }
 }
 
 template <class T, int DB, bool SINK>

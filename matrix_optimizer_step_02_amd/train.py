@@ -145,6 +145,8 @@ def _refuse_qkv(q, k, v, packed):
 
 
 def _desc(q, k, v, causal, window, sinks, scale, q_start, k_start, max_q, max_k, q_lens, k_lens):
+    if sinks >> 31:
+        raise ValueError("sinks must be in [0, 2^31)")
     packed = q_start is not None
     if packed != (k_start is not None):
         raise ValueError("q_start and k_start come together")
@@ -361,6 +363,8 @@ def _like(t, name, like):
 
 
 def _rotary(names, q, k, rope, positions, first, out_q, out_k, inverse):
+    if inverse and 0 in (q.stride(-1), 1 if k is None else k.stride(-1)):   # an expanded gradient
+        q, k = q.contiguous(), None if k is None else k.contiguous()
     d = _heads(q, k, names[0], names[1])
     if rope.__class__ is not Rotary:
         raise TypeError("rope must be a Rotary")

@@ -354,3 +354,18 @@ def test_another_stream():
     got, _ = train.rotary_forward(q, None, rope, stream=s)
     s.synchronize()
     assert torch.equal(want, got)
+
+
+def test_expanded_gradients():
+    """One value for all elements, as the gradient of a sum is."""
+    torch = _torch()
+    from matrix_optimizer_step_02_amd import train
+    rope = train.Rotary(train.rotary_frequencies(64)[0])
+    dyq = torch.full((1,), 0.75, device="cuda", dtype=torch.bfloat16).expand(2, 5, 4, 64)
+    dyk = torch.randn(2, 5, 2, 64, device="cuda").bfloat16()
+    got, want = train.rotary_backward(dyq, dyk, rope), train.rotary_backward(dyq.contiguous(), dyk, rope)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    got = train.rotary_backward(dyq, None, rope)
+    assert torch.equal(got[0], want[0])
+    with pytest.raises(train.native.MatoptError, match="overlap"):
+        train.rotary_backward(dyq, dyk, rope, dq=dyk[0, 0, 0].expand(2, 5, 4, 64))

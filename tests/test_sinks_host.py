@@ -25,3 +25,12 @@ def test_the_oracles_mask():
     assert np.array_equal(see, want)
     assert np.array_equal(T.visible(9, 5, True, 3, 0), T.visible(9, 5, True, 3))
     assert np.array_equal(T.visible(7, 7, True, 2, 7), T.visible(7, 7, True))
+
+
+@pytest.mark.parametrize("sinks", [-1, 1 << 31, 1 << 32])
+def test_numbers_past_31_bits_are_refused(N, sinks):  # noqa: F811
+    import torch
+    from matrix_optimizer_step_02_amd import train
+    x = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="sinks"):
+        train.attention_forward(x, x, x, causal=True, window=2, sinks=sinks)
