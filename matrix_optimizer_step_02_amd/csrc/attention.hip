@@ -1151,28 +1151,38 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kv_kernel(AttnArgs a, 
 }
 
 // Adds the splits of the sinks' dK and dV, in place of what the windows' launch
-// wrote there.
+// wrote there. A workgroup takes one key: 16 threads of 8 columns each, 16 slices of the
+// splits, all loads in flight together (5 us; 16 keys a workgroup, one split after the other 8).
+constexpr int kTailSplits = 64;
 template <class T>
-__global__ __launch_bounds__(kJoinThreads) void attn_join_tail_kernel(AttnArgs a, int width, uint32_t blocks) {
-    const uint32_t at = a.first + blockIdx.x, pair = at / blocks;
-    const int b = pair / a.kv_heads, hk = pair % a.kv_heads;
+__global__ __launch_bounds__(kJoinThreads) void attn_join_tail_kernel(AttnArgs a, int width, int64_t first) {
+    constexpr int SLICES = kJoinThreads / 16;
+    __shared__ __attribute__((aligned(16))) float sum[SLICES][16][8];
+    const int64_t at = first + blockIdx.x, pair = at / a.sinks;
+    const int b = (int)(pair / a.kv_heads), hk = (int)(pair % a.kv_heads), j = (int)(at % a.sinks);
     const Seq sq = sequence(a, b);
-    const int j = at % blocks * kJoinRows + threadIdx.x / 16, col = threadIdx.x % 16 * 8;
-    if (j >= min(a.sinks, sq.nk) || col >= a.head_dim) return;
+    if (j >= sq.nk) return;
+    const int slice = threadIdx.x / 16, group = threadIdx.x % 16, col = group * 8;
     const bool v_part = blockIdx.y;
     const float* part = v_part ? a.tail_v : a.tail;
-    float x[8] = {};
-    for (int s = 0; s < a.tail_splits; s += 8) {   // eight loads in flight
-        float v[8][8];
+    float v[kTailSplits / SLICES][8] = {};
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (s + k < a.tail_splits) load8(part + tail_row(a, s + k, b, hk, j) * width + col, v[k]);
+    for (int k = 0; k < kTailSplits / SLICES; ++k)
+        if (slice + k * SLICES < a.tail_splits && col < a.head_dim) load8(part + tail_row(a, slice + k * SLICES, b, hk, j) * width + col, v[k]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+    for (int e = 0; e < 8; ++e) {
+        float x = v[0][e];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (s + k < a.tail_splits) x[e] += v[k][e];
+        for (int k = 1; k < kTailSplits / SLICES; ++k) x += v[k][e];
+        sum[slice][group][e] = x;
     }
+    __syncthreads();
+    if (slice || col >= a.head_dim) return;
+    float x[8] = {};
+#pragma unroll
+    for (int k = 0; k < SLICES; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] += sum[k][group][e];
     const float mul = v_part ? kLower<T> : a.scale;
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] *= mul;
@@ -1339,7 +1349,7 @@ int tail_splits_of(const AttnArgs& x) {
     const int64_t steps = row_blocks(x.q_len, kTile) * (x.heads / x.kv_heads);
     int64_t s = wgs ? 1024 / wgs : 1;
     if (s > steps / 4) s = steps / 4;
-    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+    return (int)(s < 1 ? 1 : s > kTailSplits ? kTailSplits : s);
 }
 
 enum Kind { FORWARD, DQ, DKV };
@@ -1415,12 +1425,11 @@ void launch_tail(AttnArgs x, hipStream_t s) {
         x.first = (uint32_t)first;
         attn_dkv_kernel<T, DB, 4, 1, true><<<dim3((uint32_t)(grid - first < most ? grid - first : most)), 256, 0, s>>>(x, (int)blocks);
     }
-    const int64_t jb = row_blocks(x.sinks, kJoinRows), joins = jb * x.batch * x.kv_heads;
+    const int64_t joins = (int64_t)x.sinks * x.batch * x.kv_heads;
     constexpr int64_t most_joins = most_blocks(kJoinThreads);
     for (int64_t first = 0; first < joins; first += most_joins) {
-        x.first = (uint32_t)first;
         const dim3 g((uint32_t)(joins - first < most_joins ? joins - first : most_joins), 2);
-        attn_join_tail_kernel<T><<<g, kJoinThreads, 0, s>>>(x, 32 * DB, (uint32_t)jb);
+        attn_join_tail_kernel<T><<<g, kJoinThreads, 0, s>>>(x, 32 * DB, first);
     }
 }
 
