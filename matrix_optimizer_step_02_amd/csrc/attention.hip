@@ -944,9 +944,9 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
 // Sinks. Theirs are the only keys that queries past their window see, few keys
 // and most of the queries: one workgroup would run through them long after the
 // others are done (542 us of 8192 tokens, window 1024, 4 sinks, 16 / 8 heads of
-// 128, where the windows alone take 140). So the windows' launch leaves them out,
-// and a second one (TAIL) takes the sinks with all of their queries, split over
-// workgroups that leave fp32 partial sums for a kernel that joins them.
+// 128). So the windows' launch leaves them out (157 us), and a second one (TAIL)
+// takes the sinks with all of their queries, split over workgroups that leave fp32
+// partial sums for a kernel that joins them (25 + 5 us).
 template <class T, int DB, int W, int SETS, bool TAIL>
 __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) void attn_dkv_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
