@@ -119,9 +119,10 @@ class AdamWGroup:
             if p["W"].device != dev:
                 raise ValueError(f"W is on {p['W'].device}, expected {dev}")
         n = native.opt_adamw_workspace_size(self.descs)
-        self._streams = set()   # that have run calls of the group
-        self.workspace = torch.empty(n, dtype=torch.uint8, device=dev) if dev.type == "cuda" else None
-        # what the table points to, whatever becomes of the dicts
+        # what the table points to, whatever becomes of the dicts, and the streams that know of it
+        self._held, self._streams = (), set()
+        self._stream(None)   # the one that the workspace is of
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=dev)
         self._held = [self.workspace, *(t for p in self.params for t in p.values() if isinstance(t, torch.Tensor))]
         st = self._stream(stream)
         self._g = native.opt_adamw_create(self.descs, self.hp.c(), self.workspace.data_ptr(), n, st)
