@@ -282,6 +282,14 @@ def rotary_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_
 
 
 _TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+_TURN = round((1 << 256) / _TWO_PI)
+
+
+def _turns(f: float) -> int:
+    """2^64 f / (2 pi), rounded and reduced to one turn: f is n / 2^k."""
+    n, d = f.as_integer_ratio()
+    shift = 256 - 64 + d.bit_length() - 1
+    return ((n * _TURN + (1 << (shift - 1))) >> shift) % (1 << 64)
 
 
 class _Rotary(NamedTuple):
@@ -307,8 +315,7 @@ class Rotary(_Rotary):
             raise ValueError("frequencies must be finite, one at least")
         if not (scale > 0 and math.isfinite(scale)):
             raise ValueError("scale must be positive and finite")
-        # 2^64 f / (2 pi), rounded and reduced to one turn, as the two's complement that int64 holds
-        turns = [round(Fraction(x) / _TWO_PI * (1 << 64)) % (1 << 64) for x in f]
+        turns = [_turns(x) for x in f]   # as the two's complement that int64 holds
         table = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
         code = native.OPT_ROTARY_HALF if layout == "half" else native.OPT_ROTARY_PAIRS
         return super().__new__(cls, table, 2 * len(f), code, float(scale), table.device, table.data_ptr())

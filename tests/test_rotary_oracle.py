@@ -102,3 +102,19 @@ def test_turns_of_the_table():
                 dict(frequencies=[1.0], scale=0.0)):
         with pytest.raises(ValueError):
             train.Rotary(device="cpu", **bad)
+
+
+def test_turns_are_the_fraction_rounded():
+    import random
+    from fractions import Fraction
+    from matrix_optimizer_step_02_amd import train
+    rng = random.Random(5)
+    fs = [rng.choice((-1, 1)) * 10.0 ** rng.uniform(-12, 12) for _ in range(300)]
+    fs += [0.0, -0.0, 1.0, 5e-324, -5e-324, 1.7e308, 2.0 ** 52 + 1, *train.rotary_frequencies(128, scaling="ramp", factor=4.0,
+                                                                                            original_length=4096)[0]]
+    for f in fs:
+        exact = Fraction(f) / train._TWO_PI * (1 << 64)
+        if abs(f) > 1e20:   # past the digits of 2 pi: only that a turn comes out
+            assert 0 <= train._turns(f) < 1 << 64
+        else:
+            assert train._turns(f) == round(exact) % (1 << 64), f
