@@ -292,6 +292,9 @@ def _turns(f: float) -> int:
     return ((n * _TURN + (1 << (shift - 1))) >> shift) % (1 << 64)
 
 
+_WIDE = {torch.int32: 0, torch.int64: 1}
+
+
 class _Rotary(NamedTuple):
     turns: torch.Tensor
     rot: int
@@ -320,44 +323,48 @@ class Rotary(_Rotary):
         code = native.OPT_ROTARY_HALF if layout == "half" else native.OPT_ROTARY_PAIRS
         return super().__new__(cls, table, 2 * len(f), code, float(scale), table.device, table.data_ptr())
 
-    def c(self, positions, first, q):
-        """The descriptor for the tokens of q."""
+    def c(self, positions, first, qs, dev):
+        """The descriptor for the tokens of queries of shape qs."""
         turns, rot, layout, scale, device, ptr = self
-        dev = q.device
         if device != dev:
             raise ValueError(f"rope is on {device}, expected {dev}")
         if positions is None:
             return native.opt_rotary(ptr, rot, layout, scale, 0, 0, 0, 0, first)
         if first:
             raise ValueError("first goes without positions")
-        if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
+        if not isinstance(positions, torch.Tensor):
             raise ValueError("positions must be an int32 or int64 tensor")
-        lead, shape = q.shape[:-2], positions.shape
-        if positions.device != dev or (shape != lead and shape != lead[-1:]):
-            _is(positions, "positions", dev, positions.dtype, lead)
-        s = positions.stride()
-        return native.opt_rotary(ptr, rot, layout, scale, positions.dtype is torch.int64, positions.data_ptr(),
-                                 s[0] if len(s) == 2 else 0, s[-1])
+        wide = _WIDE.get(positions.dtype)
+        if wide is None:
+            raise ValueError("positions must be an int32 or int64 tensor")
+        shape, s, b = positions.shape, positions.stride(), 0
+        if len(shape) == 2:
+            ok, b = len(qs) == 4 and shape[0] == qs[0] and shape[1] == qs[1], s[0]
+        else:
+            ok = len(shape) == 1 and shape[0] == qs[-3]
+        if not ok or positions.device != dev:
+            _is(positions, "positions", dev, positions.dtype, qs[:-2])
+        return native.opt_rotary(ptr, rot, layout, scale, wide, positions.data_ptr(), b, s[-1])
 
 
 def _heads(q, k, q_name, k_name):
-    """The descriptor of queries and keys (k may be None)."""
-    qs = q.shape
+    """The descriptor of queries and keys (k may be None), q's shape and device."""
+    qs, dev, kv = q.shape, q.device, 0
     if len(qs) == 4:
         batch, tokens, heads, dim = qs
     elif len(qs) == 3:
         batch, (tokens, heads, dim) = 1, qs
     else:
         raise ValueError(f"{q_name} must have axes (batch, tokens, heads, dim) or (tokens, heads, dim)")
-    kv = 0
+    code = _code(q, q_name)
     if k is not None:
         ks = k.shape
-        if not (k.dtype is q.dtype and k.device == q.device and len(ks) == len(qs) and ks[-1] == dim
+        if not (k.dtype is q.dtype and k.device == dev and len(ks) == len(qs) and ks[-1] == dim
                 and ks[-3] == tokens and ks[0] == qs[0]):
-            _is(k, k_name, q.device, q.dtype)
+            _is(k, k_name, dev, q.dtype)
             raise ValueError(f"{k_name} has shape {tuple(ks)}, expected {tuple(qs)} but for the heads")
         kv = ks[-2]
-    return native.opt_heads_desc(_code(q, q_name), heads, kv, dim, batch, tokens)
+    return native.opt_heads_desc(code, heads, kv, dim, batch, tokens), qs, dev
 
 
 def _like(t, name, like):
@@ -370,13 +377,16 @@ def _like(t, name, like):
 
 
 def _rotary(names, q, k, rope, positions, first, out_q, out_k, inverse):
-    if inverse and 0 in (q.stride(-1), 1 if k is None else k.stride(-1)):   # an expanded gradient
-        q, k = q.contiguous(), None if k is None else k.contiguous()
-    d = _heads(q, k, names[0], names[1])
+    d, qs, dev = _heads(q, k, names[0], names[1])
+    if inverse:   # an expanded gradient has stride 0
+        if q.stride(-1) == 0:
+            q = q.contiguous()
+        if k is not None and k.stride(-1) == 0:
+            k = k.contiguous()
     if rope.__class__ is not Rotary:
         raise TypeError("rope must be a Rotary")
-    r = rope.c(positions, first, q)
-    st = _stream(q.device)
+    r = rope.c(positions, first, qs, dev)
+    st = _stream(dev)
     yq = _like(out_q, names[2], q)
     if k is None:
         native.opt_rotary_apply(d, r, inverse, _bhtd(q, names[0]), None, _bhtd(yq, names[2]), None, st)
@@ -403,14 +413,14 @@ def rotary_backward(dyq, dyk, rope, positions=None, *, first=0, dq=None, dk=None
     return _rotary(("dyq", "dyk", "dq", "dk"), dyq, dyk, rope, positions, first, dq, dk, 1)
 
 
-def _rope(rope, positions, first, q):
+def _rope(rope, positions, first, qs, dev):
     if rope is None:
         if positions is not None or first:
             raise ValueError("positions go with a rope")
         return None
     if rope.__class__ is not Rotary:
         raise TypeError("rope must be a Rotary or None")
-    return rope.c(positions, first, q)
+    return rope.c(positions, first, qs, dev)
 
 
 @_streamed
@@ -420,14 +430,14 @@ def qk_norm_forward(q, k, q_weight, k_weight, *, eps=1e-6, rope=None, positions=
     turned as rotary_forward turns it (rope None: not turned). k may be None, and
     with it what belongs to keys. out_q may be q and out_k may be k (but the
     backward pass needs q and k)."""
-    d, dev = _heads(q, k, "q", "k"), q.device
-    r = _rope(rope, positions, first, q)
-    dim = q.shape[-1]
+    d, qs, dev = _heads(q, k, "q", "k")
+    r = _rope(rope, positions, first, qs, dev)
+    dim = qs[-1]
     wq = _vector(q_weight, "q_weight", dev, dim)
     wk = 0 if k is None else _vector(k_weight, "k_weight", dev, dim)
     st = _stream(dev)
     yq = _like(out_q, "out_q", q)
-    q_rstd = q_weight.new_empty(q.shape[:-1])
+    q_rstd = q_weight.new_empty(qs[:-1])
     if k is None:
         native.opt_qk_norm_forward(d, r, _bhtd(q, "q"), None, wq, 0, eps, _bhtd(yq, "out_q"), None,
                                    q_rstd.data_ptr(), 0, st)
@@ -453,8 +463,8 @@ def qk_norm_backward(dyq, dyk, q, k, q_weight, k_weight, q_rstd, k_rstd, *, rope
     """(dq, dk, dq_weight, dk_weight) from the gradients of qk_norm_forward's
     results, what it took and the rstd it returned. dq and dk may be given, for
     instance as views of one projection's gradient, or be dyq and dyk."""
-    d, dev = _heads(q, k, "q", "k"), q.device
-    r = _rope(rope, positions, first, q)
+    d, qs, dev = _heads(q, k, "q", "k")
+    r = _rope(rope, positions, first, qs, dev)
     if dyq is None or (dyk is None) != (k is None):
         raise ValueError("dyq goes with q and dyk with k")
     dyq = _like(dyq, "dyq", q)
@@ -463,9 +473,9 @@ def qk_norm_backward(dyq, dyk, q, k, q_weight, k_weight, q_rstd, k_rstd, *, rope
         dyq = dyq.contiguous()
     if k is not None and dyk.stride(-1) != 1:
         dyk = dyk.contiguous()
-    dim = q.shape[-1]
+    dim = qs[-1]
     wq, wk = _vector(q_weight, "q_weight", dev, dim), 0 if k is None else _vector(k_weight, "k_weight", dev, dim)
-    sq = _statistic(q_rstd, "q_rstd", dev, q.shape[:-1])
+    sq = _statistic(q_rstd, "q_rstd", dev, qs[:-1])
     sk = 0 if k is None else _statistic(k_rstd, "k_rstd", dev, k.shape[:-1])
     st = _stream(dev)
     gq = _like(dq, "dq", q)
