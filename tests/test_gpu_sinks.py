@@ -282,3 +282,32 @@ def test_one_key_in_sight_has_no_score_gradient():
         got = run(q, k, v, dout, causal=True, window=3, sinks=1)
         assert not got["dq"].any() and not got["dk"].any()
         assert torch.equal(got["out"][:, -1], v[:, 0].repeat_interleave(2, dim=1))
+
+
+@pytest.mark.parametrize("nq", [1, 3])
+def test_a_cache_past_2_31_elements(nq):
+    """What lies between the sinks and the window is out of sight: without it the
+    sequence gives the same."""
+    torch, train = _torch(), _train()
+    print(f"sinks cache past 2^31, {nq} queries", flush=True)
+    batch, nk, heads, kv, d, window, sinks = 3, 700001, 16, 8, 128, 1000, 5
+    tail = window + nq - 1
+    mk = normal(nq)
+    q, dout = mk(batch, nq, heads, d), mk(batch, nq, heads, d)
+    k, v = (torch.zeros(batch, nk, kv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert k.numel() > 1 << 31
+    seen = lambda t: torch.cat([t[:, :sinks], t[:, nk - tail:]], 1)  # noqa: E731
+    for t in (k, v):
+        t[:, :sinks] = mk(batch, sinks, kv, d)
+        t[:, nk - tail:] = mk(batch, tail, kv, d)
+    how = dict(causal=True, window=window, sinks=sinks)
+    out, lse = train.attention_forward(q, k, v, **how)
+    dq, dk, dv = train.attention_backward(dout, q, k, v, out, lse, **how)
+    for t in (dk, dv):
+        assert not bool(t[:, sinks:nk - tail].any())
+    see = T.visible(nq, sinks + tail, True, window, sinks)
+    ks, vs, dks, dvs = (np64(seen(t)) for t in (k, v, dk, dv))
+    lse = np64(lse).reshape(heads, batch, nq)
+    for b in range(batch):
+        one = {"out": np64(out[b]), "dq": np64(dq[b]), "dk": dks[b], "dv": dvs[b], "lse": lse[:, b]}
+        check_sequence(np64(q[b]), ks[b], vs[b], np64(dout[b]), one, d ** -0.5, see, U["bf16"])
