@@ -173,13 +173,18 @@ __device__ __forceinline__ void copy16(uint32_t lds, const void* src) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                  :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src) : "memory");
 }
-// The same from a uniform address and an offset below 2^32 in each lane.
+// The same from a uniform address and an offset below 2^32 in each lane. A vector
+// memory instruction reads a scalar register that a vector one wrote (readfirstlane)
+// 5 wait states later at the earliest, which neither the hardware checks nor the
+// compiler ahead of inline assembly: the address goes through a scalar move, which
+// the hardware does hold back, and which is m0's wait state too.
 __device__ __forceinline__ void copy16(uint32_t lds, const char* base, uint32_t off) {
     const uint64_t b = (uint64_t)base;
     const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32 |
                        (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);   // in scalar registers, whatever computed it
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(u) : "memory");
+    uint64_t from;
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
+                 : "=&s"(from) : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(u) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t lds, const void* src) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
