@@ -168,10 +168,14 @@ __device__ __forceinline__ char* rows_of(const Tensor& t, int b, int64_t row0, i
 // own copies as pending LDS writes, cannot tell the tile that is being filled from
 // the one that is being read, and waits for them before the first transposed read:
 // tile_barrier waits for these. (What the compiler waits for besides can only be
-// later than it thinks: vector memory operations complete in order.)
+// later than it thinks: vector memory operations complete in order.) m0, the place in
+// LDS, is named as written for a compiler that sets it around these; it warns that
+// it will not keep the register's value, which is what is asked for.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy16(uint32_t lds, const void* src) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src) : "memory");
+                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src) : "m0", "memory");
 }
 // The same from a uniform address and an offset below 2^32 in each lane. A vector
 // memory instruction reads a scalar register that a vector one wrote (readfirstlane)
@@ -184,12 +188,13 @@ __device__ __forceinline__ void copy16(uint32_t lds, const char* base, uint32_t 
                        (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);   // in scalar registers, whatever computed it
     uint64_t from;
     asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
-                 : "=&s"(from) : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(u) : "memory");
+                 : "=&s"(from) : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(u) : "m0", "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t lds, const void* src) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
-                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src) : "memory");
+                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src) : "m0", "memory");
 }
+#pragma clang diagnostic pop
 __device__ __forceinline__ uint32_t lds_at(const void* p) { return (uint32_t)(uintptr_t)(lds_char)p; }
 
 // Copies 64-row tiles of one tensor into LDS. Chunk i of a wavefront is 1024

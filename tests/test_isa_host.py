@@ -121,3 +121,15 @@ def test_scalar_bases_of_copies_are_waited_for(tmp_path):
             bad += [(name, hex(address), states) for address, states in short_waits(code)]
     assert copies > 1000
     assert not bad, f"{len(bad)} sites, the first: {bad[:5]}"
+
+
+def test_inline_assembly_names_what_it_writes():
+    """A statement that writes m0 says so: a compiler that holds a value of its own there would not know."""
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "matrix_optimizer_step_02_amd", "csrc")
+    seen = 0
+    for name in sorted(os.listdir(csrc)):
+        for statement in re.findall(r"\basm volatile\((.*?)\);", open(os.path.join(csrc, name)).read(), flags=re.S):
+            if "m0," in statement.split("::")[0]:
+                seen += 1
+                assert '"m0"' in statement, f"{name}: {statement}"
+    assert seen == 3
