@@ -121,10 +121,13 @@ class AdamWGroup:
         n = native.opt_adamw_workspace_size(self.descs)
         # what the table points to, whatever becomes of the dicts, and the streams that know of it
         self._held, self._streams = (), set()
-        self._stream(None)   # the one that the workspace is of
-        self.workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        self._held = [self.workspace, *(t for p in self.params for t in p.values() if isinstance(t, torch.Tensor))]
         st = self._stream(stream)
+        with torch.cuda.stream(stream):   # the table's: another stream may still write to what it hands out
+            self.workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        self._held = [self.workspace, *(t for p in self.params for t in p.values() if isinstance(t, torch.Tensor))]
+        if stream is not None:
+            self._streams.clear()
+            self._stream(stream)
         self._g = native.opt_adamw_create(self.descs, self.hp.c(), self.workspace.data_ptr(), n, st)
 
     def _stream(self, stream):
