@@ -119,26 +119,27 @@ class AdamWGroup:
             if p["W"].device != dev:
                 raise ValueError(f"W is on {p['W'].device}, expected {dev}")
         n = native.opt_adamw_workspace_size(self.descs)
-        # what the table points to, whatever becomes of the dicts, and the streams that know of it
-        self._held, self._streams = (), set()
-        st = self._stream(stream)
+        st = self._handle(stream)
         with torch.cuda.stream(stream):   # the table's: another stream may still write to what it hands out
             self.workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        # what the table points to, whatever becomes of the dicts, and the streams that know of it
         self._held = [self.workspace, *(t for p in self.params for t in p.values() if isinstance(t, torch.Tensor))]
-        if stream is not None:
-            self._streams.clear()
-            self._stream(stream)
+        self._streams = set()
+        self._stream(stream)
         self._g = native.opt_adamw_create(self.descs, self.hp.c(), self.workspace.data_ptr(), n, st)
 
-    def _stream(self, stream):
+    def _handle(self, stream):
         dev = self._dev
         if dev.type != "cuda":
             raise ValueError("tensors must live on a HIP device")
         if dev.index != torch._C._cuda_getDevice():
             raise ValueError(f"tensors are on {dev}, which is not the current device (torch.cuda.device)")
-        st = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+
+    def _stream(self, stream):
+        st = self._handle(stream)
         if st not in self._streams:   # no memory of the group is handed out again before this stream is past its calls
-            for t in self._held:
+            for t in {t.untyped_storage().data_ptr(): t for t in self._held}.values():   # a flat buffer's parts once
                 t.record_stream(torch.cuda.current_stream() if stream is None else stream)
             self._streams.add(st)
         return st

@@ -16,6 +16,9 @@ class Recorded(torch.Tensor):
     def record_stream(self, stream):
         self.__dict__.setdefault("on", []).append(stream.cuda_stream)
 
+    def __repr__(self):
+        return "Recorded()"
+
 
 class Stream:
     def __init__(self, handle):
@@ -52,9 +55,8 @@ def device(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: Device.now[-1].cuda_stream, raising=False)
     monkeypatch.setattr(adamw, "make_adamw_desc", lambda p, hp: None)
     monkeypatch.setattr(adamw.native, "opt_adamw_workspace_size", lambda d: 512)
-    monkeypatch.setattr(adamw.native, "opt_adamw_create", lambda *a: 1)
+    monkeypatch.setattr(adamw.native, "opt_adamw_create", lambda *a: 0)
     monkeypatch.setattr(adamw.native, "opt_adamw_step", lambda *a: None)
-    monkeypatch.setattr(adamw.native, "opt_adamw_destroy", lambda *a: None)
     return Device
 
 
@@ -67,3 +69,28 @@ def test_the_workspace_is_taken_on_the_stream_that_fills_it(device, stream):
     """Memory handed out on another stream may have that stream's writes still to come, over the table."""
     adamw.AdamWGroup([param()], stream=stream)
     assert device.taken == [10 if stream is None else 11]
+
+
+@pytest.mark.parametrize("stream", [None, Stream(11)])
+def test_tensors_are_recorded_on_every_stream_that_steps_them(device, stream):
+    """They may be from another stream's memory, the one the group was made on included."""
+    p = param()
+    made = 10 if stream is None else 11
+    group = adamw.AdamWGroup([p], stream=stream)
+    where = lambda: [t.__dict__.get("on", []) for t in (*p.values(), group.workspace)]  # noqa: E731
+    assert where() == [[made]] * 5
+    group.step(stream=stream)
+    group.step(stream=Stream(12))
+    group.step(stream=Stream(12))
+    assert where() == [[made, 12]] * 5
+
+
+def test_a_storage_is_recorded_once(device):
+    """Tensors cut from one buffer."""
+    parts = tensor(900).split(300)
+    rest = [param() for _ in parts]
+    adamw.AdamWGroup([p | {"W": x} for p, x in zip(rest, parts)])
+    on = [x.__dict__.get("on", []) for x in parts]
+    assert sorted(map(len, on)) == [0, 0, 1]
+    on = [p["m"].__dict__.get("on", []) for p in rest]
+    assert on == [[10]] * 3

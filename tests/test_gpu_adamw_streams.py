@@ -31,3 +31,26 @@ def test_a_groups_table_beside_writes_that_are_still_to_come():
     group.step(stream=s)
     torch.cuda.synchronize()
     check(p, 0, before, 1)
+
+
+def test_tensors_of_another_stream_outlive_a_dropped_group():
+    """Tensors made on the current stream; a group made, stepped and dropped on another one, whose step still waits."""
+    torch, mo = _torch(), _mo()
+    p, s = param(5000), torch.cuda.Stream()
+    before, want = snap(p), {k: t.clone() for k, t in p.items()}
+    places = {t.untyped_storage().data_ptr() for t in p.values()}
+    group = mo.AdamWGroup([want], mo.AdamWHyper(**HP))
+    group.step()
+    check(want, 0, before, 1)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        group = mo.AdamWGroup([p], mo.AdamWHyper(**HP))
+        busy(torch)
+        group.step()
+    sizes = [t.untyped_storage().nbytes() for t in p.values()]
+    del group, p
+    got = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+    if not s.query():
+        assert not places & {x.data_ptr() for x in got}
+    torch.cuda.synchronize()
+    assert all(bool((x == 7).all()) for x in got)
