@@ -20,6 +20,10 @@
  * discarded fraction of a step plus r / 65536 reaches 1, down otherwise: at beta2 =
  * 0.999 an average moves by less than half a step of 8 bits, so rounding to nearest
  * would leave it where it is, while the mean of this rounding is the value itself.
+ * A v above 0 takes the smallest code above 0 at least: where it became 0 beside an
+ * m that does not, the steps after it would divide m by next to nothing. So sqrt(v)
+ * counts as 2^-15.5 to 2^-15 of the block's largest at least, and elements whose gradients
+ * stay below that move less than with 32 bits.
  * Element i of tensor n takes for r 16 bits of Philox4x32-10 (see opt_dropout) with
  * counter (i / 8, n, offset low, offset high) and key (seed low, seed high): word
  * (i % 8) / 2, its low half for even i; m takes them with their two bytes exchanged.

@@ -200,13 +200,18 @@ __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t
 // Magnitude y = |x| / scale to a code with DIGITS mantissa bits, r 16 random
 // bits. From 2^(1 - BIAS) on the bits below the code's are y's low 23 - DIGITS:
 // r is added at their top and they are cut off, which carries into the exponent.
-// Below, a step is 2^(1 - BIAS - DIGITS) and the code their number.
-template <int DIGITS, int BIAS>
+// Below, a step is 2^(1 - BIAS - DIGITS) and the code their number. KEEP: what is
+// above 0 stays so. A v that is lost while its m is not (2^-16 of the block's largest
+// m, where v's smallest code is 2^-31 to 2^-30 of the largest v) would have the next
+// steps divide that m by next to nothing: gradients spread over 2^14 and more of a
+// block made steps of 1000 times the rate.
+template <int DIGITS, int BIAS, bool KEEP>
 __device__ __forceinline__ uint32_t encode(float x, float inverse, uint32_t r) {
     const float y = fabsf(x) * inverse;
     const uint32_t normal = ((__float_as_uint(y) + (r << (7 - DIGITS))) >> (23 - DIGITS)) - ((127 - BIAS) << DIGITS);
     const uint32_t small = ((uint32_t)(y * (float)(uint64_t(1) << (BIAS - 1 + DIGITS + 16))) + r) >> 16;
     uint32_t code = y < 1.f / (1 << (BIAS - 1)) ? small : normal;
+    if (KEEP && x > 0.f && code == 0) code = 1;
     if (!(fabsf(x) < INFINITY)) code = 0x7f;
     return code | (x < 0.f ? 0x80u : 0u);
 }
@@ -258,8 +263,8 @@ __global__ __launch_bounds__(kThreads) void adamw8_kernel(StepArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const uint32_t r = e & 1 ? bits[e >> 1] >> 16 : bits[e >> 1] & 0xffffu;
-            mo[e >> 2] |= encode<3, 7>(m[e], mi, (r >> 8) | (r & 255u) << 8) << (8 * (e & 3));
-            vo[e >> 2] |= encode<2, 15>(v[e], vi, r) << (8 * (e & 3));
+            mo[e >> 2] |= encode<3, 7, false>(m[e], mi, (r >> 8) | (r & 255u) << 8) << (8 * (e & 3));
+            vo[e >> 2] |= encode<2, 15, true>(v[e], vi, r) << (8 * (e & 3));
         }
         store_bytes((char*)s.m + i, n, mo);
         store_bytes((char*)s.v + i, n, vo);

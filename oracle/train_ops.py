@@ -153,17 +153,21 @@ def rms_norm_backward(g, x, w, eps):
 # ------------------------------------------------------------------ AdamW ----
 
 
+class SecondMoment(np.ndarray):
+    """Averages of squares, of which encode8 makes no 0 that was none."""
+
+
 def adamw_moments(m, v, g, b1, b2):
     """In float32, each product and sum rounded: what the states of 8 bits are made from."""
     f = np.float32
     m, v, g = (np.asarray(x, dtype=f) for x in (m, v, g))
     with np.errstate(over="ignore", invalid="ignore", under="ignore"):
-        return m * f(b1) + g * f(1 - b1), v * f(b2) + (g * g) * f(1 - b2)
+        return m * f(b1) + g * f(1 - b1), (v * f(b2) + (g * g) * f(1 - b2)).view(SecondMoment)
 
 
 def adamw_weights(w, m, v, t, lr, b1, b2, eps, decay):
     """In float64, from the moments after step t."""
-    u = m / (1 - b1 ** t) / (np.sqrt(v / (1 - b2 ** t)) + eps)
+    u = m / (1 - b1 ** t) / (np.sqrt(np.asarray(v) / (1 - b2 ** t)) + eps)
     return w - lr * (u + decay * w)
 
 
@@ -178,7 +182,9 @@ def random16(n, tensor, seed, offset, first=0):
 
 def encode8(x, r, digits, bias, top, block=256):
     """(values, scales): x (float32) in blocks with a power of two each, rounded up in magnitude where the discarded
-    fraction plus r / 65536 reaches 1. Values are what the codes stand for, scale included; NaN where x is not finite."""
+    fraction plus r / 65536 reaches 1, and a second moment that is not 0 to the smallest code at least. Values are what
+    the codes stand for, scale included; NaN where x is not finite."""
+    second, x = isinstance(x, SecondMoment), np.asarray(x)
     n, f = x.size, np.float64
     mag = np.abs(np.pad(x.astype(f), (0, -n % block)).reshape(-1, block))
     big = np.where(np.isfinite(mag), mag, 0).max(axis=1)
@@ -190,5 +196,7 @@ def encode8(x, r, digits, bias, top, block=256):
         _, ye = np.frexp(np.where(np.isfinite(y), y, 1.0))
         step = np.ldexp(1.0, np.maximum(ye - 1, 1 - bias) - digits)
         q = np.floor(y / step + r / 65536) * step
+        if second:
+            q = np.where((y > 0) & (q == 0), step, q)
     q = np.where(np.isfinite(x), np.copysign(q, x), np.nan)
     return q * np.repeat(scale, block)[:n], scale
