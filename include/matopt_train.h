@@ -137,7 +137,8 @@ typedef struct {
     int64_t batch, tokens;     /* batch * tokens < 2^31 */
 } opt_heads_desc;
 
-/* yq may be q and yk may be k (same strides); results do not overlap otherwise. */
+/* yq may be q and yk may be k (same strides); results that overlap these tensors or each
+ * other otherwise are refused. */
 opt_status opt_rotary_apply(const opt_heads_desc* d, const opt_rotary* r, int32_t inverse, const opt_attention_tensor* q,
                             const opt_attention_tensor* k, const opt_attention_tensor* yq,
                             const opt_attention_tensor* yk, void* stream);
@@ -149,7 +150,9 @@ opt_status opt_rotary_apply(const opt_heads_desc* d, const opt_rotary* r, int32_
  *   g = R^T dy,  z = g w,  xh = x rstd,  dx = rstd (z - xh mean(z xh)),  dw = sum g xh
  * Weights (head_dim) and their gradients are fp32, one for all heads of q and one
  * for those of k; rstd is fp32, (batch, tokens, heads) contiguous. yq may be q, dq
- * may be dyq or q (same strides), and so for k; results do not overlap otherwise.
+ * may be dyq or q (same strides), and so for k; results of the tensors' type that
+ * overlap them or each other otherwise are refused. The fp32 results and the workspace
+ * overlap nothing.
  */
 opt_status opt_qk_norm_forward(const opt_heads_desc* d, const opt_rotary* r, const opt_attention_tensor* q,
                                const opt_attention_tensor* k, const float* q_weight, const float* k_weight, float eps,

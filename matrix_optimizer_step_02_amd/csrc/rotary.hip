@@ -20,6 +20,7 @@
 // 2^31 is as exact as position 1, where p f_i in fp32 would be off by 2^31 2^-24
 // = 128 radians. The top 32 bits go into polynomials on an eighth of a turn to
 // each side (the Taylor series, cut below 2^-29).
+#include "places.h"
 #include "train.h"
 
 #include <utility>
@@ -458,30 +459,42 @@ opt_status check_tensor(const opt_heads_desc* d, const opt_attention_tensor* t, 
     return OPT_OK;
 }
 
-// A result in its input's place: every element has to be written where it was read.
-opt_status check_place(const opt_heads_desc* d, int heads, const Heads& y, const Heads& x, const char* y_name, const char* x_name) {
-    const bool same = (d->batch == 1 || y.batch == x.batch) && (d->tokens == 1 || y.token == x.token) && (heads == 1 || y.head == x.head);
-    if (y.p == x.p && !same) return fail(OPT_EINVAL, "%s is %s with other strides", y_name, x_name);
-    return OPT_OK;
+Place place_of(const opt_heads_desc* d, int heads, const Heads& t) {
+    return {(int64_t)((uintptr_t)t.p / train_bytes(d->dtype)), {{d->batch, t.batch}, {d->tokens, t.token}, {heads, t.head}}, d->head_dim};
 }
-opt_status check_apart(const opt_heads_desc* d, const Args& a, const char* q_name, const char* k_name) {
-    if (d->kv_heads && a.q.out.p == a.k.out.p) return fail(OPT_EINVAL, "%s and %s are the same memory", q_name, k_name);
-    return OPT_OK;
+// A result and what is read by threads that may not have read it yet when it is
+// written: other memory, or (OWN: what the same thread reads) the same place, every
+// element written where it was read.
+template <bool OWN>
+opt_status check_place(const opt_heads_desc* d, int y_heads, const Heads& y, const char* y_name, int x_heads, const Heads& x, const char* x_name) {
+    if (OWN && y.p == x.p) {
+        const bool same = (d->batch == 1 || y.batch == x.batch) && (d->tokens == 1 || y.token == x.token) && (x_heads == 1 || y.head == x.head);
+        return same ? OPT_OK : fail(OPT_EINVAL, "%s is %s with other strides", y_name, x_name);
+    }
+    if (!shares(place_of(d, y_heads, y), place_of(d, x_heads, x))) return OPT_OK;
+    return fail(OPT_EINVAL, OWN ? "%s overlaps %s other than in its place" : "%s overlaps %s", y_name, x_name);
 }
 opt_status check_places(const opt_heads_desc* d, const Args& a) {
-    if (opt_status st = check_place(d, d->heads, a.q.out, a.q.in, "yq", "q")) return st;
-    if (d->kv_heads)
-        if (opt_status st = check_place(d, d->kv_heads, a.k.out, a.k.in, "yk", "k")) return st;
-    return check_apart(d, a, "yq", "yk");
+    const int h = d->heads, kv = d->kv_heads;
+    if (opt_status st = check_place<true>(d, h, a.q.out, "yq", h, a.q.in, "q")) return st;
+    if (kv == 0) return OPT_OK;
+    if (opt_status st = check_place<true>(d, kv, a.k.out, "yk", kv, a.k.in, "k")) return st;
+    if (opt_status st = check_place<false>(d, h, a.q.out, "yq", kv, a.k.in, "k")) return st;
+    if (opt_status st = check_place<false>(d, kv, a.k.out, "yk", h, a.q.in, "q")) return st;
+    return check_place<false>(d, h, a.q.out, "yq", kv, a.k.out, "yk");
 }
 opt_status check_gradient_places(const opt_heads_desc* d, const Args& a) {
-    if (opt_status st = check_place(d, d->heads, a.q.out, a.q.in, "dq", "q")) return st;
-    if (opt_status st = check_place(d, d->heads, a.q.out, a.q.dy, "dq", "dyq")) return st;
-    if (d->kv_heads) {
-        if (opt_status st = check_place(d, d->kv_heads, a.k.out, a.k.in, "dk", "k")) return st;
-        if (opt_status st = check_place(d, d->kv_heads, a.k.out, a.k.dy, "dk", "dyk")) return st;
-    }
-    return check_apart(d, a, "dq", "dk");
+    const int h = d->heads, kv = d->kv_heads;
+    if (opt_status st = check_place<true>(d, h, a.q.out, "dq", h, a.q.in, "q")) return st;
+    if (opt_status st = check_place<true>(d, h, a.q.out, "dq", h, a.q.dy, "dyq")) return st;
+    if (kv == 0) return OPT_OK;
+    if (opt_status st = check_place<true>(d, kv, a.k.out, "dk", kv, a.k.in, "k")) return st;
+    if (opt_status st = check_place<true>(d, kv, a.k.out, "dk", kv, a.k.dy, "dyk")) return st;
+    for (const auto& x : {std::make_pair(&a.k.in, "k"), std::make_pair(&a.k.dy, "dyk")})
+        if (opt_status st = check_place<false>(d, h, a.q.out, "dq", kv, *x.first, x.second)) return st;
+    for (const auto& x : {std::make_pair(&a.q.in, "q"), std::make_pair(&a.q.dy, "dyq")})
+        if (opt_status st = check_place<false>(d, kv, a.k.out, "dk", h, *x.first, x.second)) return st;
+    return check_place<false>(d, h, a.q.out, "dq", kv, a.k.out, "dk");
 }
 
 opt_status check_vector(const float* p, const char* name) {
