@@ -321,7 +321,14 @@ class Rotary(_Rotary):
         turns = [_turns(x) for x in f]   # as the two's complement that int64 holds
         table = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
         code = native.OPT_ROTARY_HALF if layout == "half" else native.OPT_ROTARY_PAIRS
-        return super().__new__(cls, table, 2 * len(f), code, float(scale), table.device, table.data_ptr())
+        return cls._of(table, code, float(scale))
+
+    @classmethod
+    def _of(cls, table, code, scale):
+        return super().__new__(cls, table, 2 * table.numel(), code, scale, table.device, table.data_ptr())
+
+    def __reduce__(self):   # copies and pickles: a table of their own has another address
+        return Rotary._of, (self.turns, self.layout, self.scale)
 
     def c(self, positions, first, qs, dev):
         """The descriptor for the tokens of queries of shape qs."""
