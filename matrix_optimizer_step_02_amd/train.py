@@ -385,10 +385,10 @@ def _like(t, name, like):
 
 def _rotary(names, q, k, rope, positions, first, out_q, out_k, inverse):
     d, qs, dev = _heads(q, k, names[0], names[1])
-    if inverse:   # an expanded gradient has stride 0
-        if q.stride(-1) == 0:
+    if inverse:   # a gradient may have any strides: 0 where it is expanded, others behind a transposition
+        if q.stride(-1) != 1:
             q = q.contiguous()
-        if k is not None and k.stride(-1) == 0:
+        if k is not None and k.stride(-1) != 1:
             k = k.contiguous()
     if rope.__class__ is not Rotary:
         raise TypeError("rope must be a Rotary")
