@@ -956,7 +956,9 @@ __global__ __launch_bounds__(SETS * 64 * W, 2) void attn_dq_kernel(AttnArgs a, i
 // others are done (542 us of 8192 tokens, window 1024, 4 sinks, 16 / 8 heads of
 // 128). So the windows' launch leaves them out (157 us), and a second one (TAIL)
 // takes the sinks with all of their queries, split over workgroups that leave fp32
-// partial sums for a kernel that joins them (25 + 5 us).
+// partial sums for a kernel that joins them (25 + 5 us). Where there are sequences
+// and heads enough for a part each they store what the windows' launch left out
+// themselves, and need no workspace.
 template <class T, int DB, int W, int SETS, bool TAIL>
 __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) void attn_dkv_kernel(AttnArgs a, int blocks) {
     using G = Geo<DB>;
@@ -1118,13 +1120,13 @@ __global__ __launch_bounds__(SETS * 64 * W, DB <= 2 && SETS * W == 4 ? 3 : 2) vo
     }
     if (lane_hi() <= lane_lo()) clear(dk), clear(dv);
     if (j >= (TAIL ? keys : sq.k_rows)) return;
-    if constexpr (TAIL) {
+    if (TAIL && a.tail_splits > 1) {
         const int64_t row = tail_row(a, split, b, hk, j) * (32 * DB);
         store_part<DB>(dk, a.tail + row);
         store_part<DB>(dv, a.tail_v + row);
         return;
     }
-    if (a.kv_splits > 1) {
+    if (!TAIL && a.kv_splits > 1) {
         const int64_t row = (((int64_t)split * a.kv_heads + hk) * a.k_tokens + (a.q_start ? sq.k0 : (int64_t)b * a.k_len) + j) * (32 * DB);
         if (SETS == 1 || set == 0) store_part<DB>(dk, a.part + row);
         if (SETS == 1 || set == 1) store_part<DB>(dv, a.part_v + row);
@@ -1435,6 +1437,7 @@ void launch_tail(AttnArgs x, hipStream_t s) {
         x.first = (uint32_t)first;
         attn_dkv_kernel<T, DB, 4, 1, true><<<dim3((uint32_t)(grid - first < most ? grid - first : most)), 256, 0, s>>>(x, (int)blocks);
     }
+    if (x.tail_splits == 1) return;
     const int64_t joins = (int64_t)x.sinks * x.batch * x.kv_heads;
     constexpr int64_t most_joins = most_blocks(kJoinThreads);
     for (int64_t first = 0; first < joins; first += most_joins) {
@@ -1505,7 +1508,7 @@ Space space_of(const AttnArgs& x, bool backward) {
         s.bytes += q_part > 2 * k_part ? q_part : 2 * k_part;
         if (x.sinks && k_rows) {
             s.tail_splits = tail_splits_of(x);
-            const uint64_t each = up((uint64_t)s.tail_splits * x.batch * x.kv_heads * x.sinks * width * 4);
+            const uint64_t each = s.tail_splits == 1 ? 0 : up((uint64_t)s.tail_splits * x.batch * x.kv_heads * x.sinks * width * 4);
             s.tail = s.bytes, s.tail_v = s.tail + each;
             s.bytes += 2 * each;
         }
