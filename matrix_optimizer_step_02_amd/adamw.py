@@ -41,7 +41,9 @@ def _blocks(n: int) -> int:
 
 
 def adamw_state(W: torch.Tensor, bits: int = 32) -> dict:
-    """Fresh moments of one tensor: m and v in fp32, or in 8 bits with a scale per 256 elements."""
+    """Fresh moments of one tensor: m and v in fp32, or in 8 bits with a scale per 256
+    elements (which move less than in fp32 where their gradients stay 2^15 below the
+    largest of the 256)."""
     if bits == 32:
         return {"m": torch.zeros_like(W, dtype=torch.float32), "v": torch.zeros_like(W, dtype=torch.float32)}
     if bits != 8:
@@ -168,10 +170,11 @@ class AdamWGroup:
 
     def step(self, grad_scale=None, rng: Optional[Rng] = None, device_step=None, stream=None):
         """One step. grad_scale: an fp32 scalar on the device that multiplies the
-        gradients (where it is NaN, nothing is written). rng: the random bits that
-        round 8-bit states; give each step another offset. device_step: an int64
-        scalar on the device that holds this step's number, counted from 1, for a
-        replayed graph (else the group counts)."""
+        gradients (where it is NaN, nothing is written; the group counts the step all the
+        same: a program that does not want that sets t back, or counts in device_step).
+        rng: the random bits that round 8-bit states; give each step another offset.
+        device_step: an int64 scalar on the device that holds this step's number,
+        counted from 1, for a replayed graph (else the group counts)."""
         st = self._stream(stream)
         bits = None
         if rng is not None:

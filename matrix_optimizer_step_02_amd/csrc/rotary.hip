@@ -62,8 +62,8 @@ struct Args {
 
 // ------------------------------------------------------------------ angles ----
 
-// sin and cos of `top` 2^-32 turns. Within 2^-29 of a turn to the nearest
-// quarter, x = 2 pi r 2^-32 in [-pi / 4, pi / 4]; the terms left out are below
+// sin and cos of `top` 2^-32 turns. r = top less the nearest quarter lies within 2^29,
+// an eighth of a turn, and x = 2 pi r 2^-32 in [-pi / 4, pi / 4]; the terms left out are below
 // 2e-9 (sine) and 2e-10 (cosine), and both are within 2 2^-24 of the exact ones.
 __device__ __forceinline__ void turn(uint32_t top, float& sn, float& cs) {
     const uint32_t quarter = (top + 0x20000000u) >> 30;
