@@ -171,6 +171,9 @@ class RotatedAdamGroup:
         _, _, ngroups = RotatedAdamGroup.plan([(int(d.m), int(d.n)) for d in self.descs], self.hp)
         return native.opt_group_read_group_timing(self._g, ngroups)
 
+    def __reduce__(self):   # two objects would free one handle
+        raise TypeError("a group is not copied: make another group from its tensors, or copies of them, and set its t")
+
     def close(self):
         if getattr(self, "_g", None):
             native.opt_group_destroy(self._g)

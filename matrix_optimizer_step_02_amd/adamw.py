@@ -195,6 +195,9 @@ class AdamWGroup:
         native.opt_adamw_set_lr(self._g, lr)
         self.hp.lr = lr
 
+    def __reduce__(self):   # two objects would free one handle
+        raise TypeError("a group is not copied: make another group from its tensors, or copies of them, and set its t")
+
     def close(self):
         if getattr(self, "_g", None):
             native.opt_adamw_destroy(self._g)
